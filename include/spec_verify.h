@@ -63,6 +63,7 @@ extern "C" {
 #define SV_ERR_TIMEOUT (-6)   /* a bounded device-side wait ran out          */
 #define SV_ERR_TOKEN (-7)     /* a draft token was outside [0, V)            */
 #define SV_ERR_NONFINITE (-8) /* logits or draft logits were NaN/inf         */
+#define SV_ERR_CACHE (-9)     /* a cache slot, page or length out of bounds  */
 
 /* Element type of hidden and W_lm. */
 #define SV_BF16 0 /* production path: TMA + tcgen05 tensor-core contraction   */

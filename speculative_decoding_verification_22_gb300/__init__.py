@@ -26,6 +26,7 @@ SV_ERR_ARCH = -5
 SV_ERR_TIMEOUT = -6
 SV_ERR_TOKEN = -7
 SV_ERR_NONFINITE = -8
+SV_ERR_CACHE = -9
 SV_BF16 = 0
 SV_FP32 = 1
 SV_FP8 = 2
@@ -34,7 +35,7 @@ SV_MAX_B = 4096
 SV_MAX_ROWS_BF16 = 384
 SV_NGRAM_MAX = 16
 
-# every symbol of include/spec_verify.h
+# every symbol of include/spec_verify.h and include/spec_target.h
 EXPORTS = ("spec_verify_create", "spec_verify_run", "spec_verify_run_host",
            "spec_verify_status", "spec_verify_set_stream",
            "spec_verify_debug_logits", "spec_verify_debug_lse",
@@ -43,7 +44,11 @@ EXPORTS = ("spec_verify_create", "spec_verify_run", "spec_verify_run_host",
            "spec_verify_strerror", "spec_verify_destroy",
            "spec_verify_run_noalloc", "spec_ngram_draft", "spec_verify_run_truncated",
            "spec_verify_tree_greedy", "spec_verify_run_fp8", "spec_verify_plan",
-           "spec_verify_debug_stall", "spec_verify_submit_host", "spec_verify_wait_host")
+           "spec_verify_debug_stall", "spec_verify_submit_host", "spec_verify_wait_host",
+           "spec_target_create", "spec_target_destroy", "spec_target_status",
+           "spec_target_set_wait_limit", "spec_target_rms_norm", "spec_target_rms_norm_fp8",
+           "spec_target_matmul_fp8", "spec_target_rope_freqs", "spec_target_rope_append",
+           "spec_target_attention", "spec_target_tree_mask")
 
 
 class sv_plan_t(ctypes.Structure):
@@ -110,8 +115,24 @@ def load_library():
                                          vp]
         lib.spec_verify_plan.argtypes = [ctypes.POINTER(sv_config_t), i32, i32,
                                          ctypes.POINTER(sv_plan_t)]
+        lib.spec_target_create.argtypes = [ctypes.POINTER(vp)]
+        lib.spec_target_destroy.argtypes = [vp]
+        lib.spec_target_destroy.restype = None
+        lib.spec_target_status.argtypes = [vp, vp]
+        lib.spec_target_set_wait_limit.argtypes = [vp, ctypes.c_uint64]
+        lib.spec_target_rms_norm.argtypes = [vp, vp, i64, vp, i64, vp, f32, i64, i64, i32, vp,
+                                             i64, vp, i64, vp]
+        lib.spec_target_rms_norm_fp8.argtypes = [vp, vp, i64, vp, i64, vp, f32, i64, i64, i32,
+                                                 i32, vp, vp, vp, i64, vp]
+        lib.spec_target_matmul_fp8.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, i32, vp, i64,
+                                               vp]
+        lib.spec_target_rope_freqs.argtypes = [vp, vp, vp]
+        lib.spec_target_rope_append.argtypes = [vp, vp, vp]
+        lib.spec_target_attention.argtypes = [vp, vp, vp]
+        lib.spec_target_tree_mask.argtypes = [vp, vp, i32, i32, vp, vp]
         for name in EXPORTS:
-            if name not in ("spec_verify_strerror", "spec_verify_destroy"):
+            if name not in ("spec_verify_strerror", "spec_verify_destroy",
+                            "spec_target_destroy"):
                 getattr(lib, name).restype = ctypes.c_int
         _lib = lib
     return _lib
@@ -395,3 +416,7 @@ class SpecVerify:
             self.close()
         except Exception:
             pass
+
+
+from .target import (ROPE_SCALINGS, SV_FP16, SV_MAX_HEAD_DIM, SV_SCALE_BLOCK,  # noqa: E402
+                     TargetOps, spec_target_rope_freqs)

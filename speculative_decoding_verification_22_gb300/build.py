@@ -18,8 +18,9 @@ LIB = os.path.join(HERE, "libspec_verify.so")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 SOURCES = ["sv_api.cu", "sv_lmhead_tc.cu", "sv_lmhead_simt.cu", "sv_tail.cu", "sv_noalloc.cu",
            "sv_trunc.cu",
-           "sv_ngram.cu"]
-HEADERS = ["sv_internal.cuh", "sv_kernels.h"]
+           "sv_ngram.cu",
+           "sv_target_api.cu", "sv_norm.cu", "sv_rope.cu", "sv_matmul8.cu", "sv_attn.cu"]
+HEADERS = ["sv_internal.cuh", "sv_kernels.h", "sv_target.cuh", "sv_attn.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
          "--expt-relaxed-constexpr", "-I", INCLUDE]
@@ -41,7 +42,8 @@ def _stale(out, deps):
 def build(force: bool = False, ptxas_verbose: bool = False, verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     nvcc = _nvcc()
-    hdrs = [os.path.join(CSRC, h) for h in HEADERS] + [os.path.join(INCLUDE, "spec_verify.h")]
+    hdrs = [os.path.join(CSRC, h) for h in HEADERS] + [
+        os.path.join(INCLUDE, h) for h in ("spec_verify.h", "spec_target.h")]
     jobs = []
     objs = []
     for src in SOURCES:

@@ -236,6 +236,7 @@ const char *spec_verify_strerror(int code) {
     case SV_ERR_TIMEOUT: return "a device-side wait ran out";
     case SV_ERR_TOKEN: return "draft token outside [0, V)";
     case SV_ERR_NONFINITE: return "non-finite logits or draft logits";
+    case SV_ERR_CACHE: return "cache slot, page, length or token range out of bounds";
     default: return "unknown error";
   }
 }

@@ -1,0 +1,277 @@
+// sv_norm.cu -- residual RMS norm, with the result in the rows' type or in
+// E4M3 with one scale per 128 columns or per row.
+//
+//   h = x + residual,  y = h / sqrt(mean(h^2) + eps) * weight
+//
+// One pass: a row stays in registers between the sum of squares and the
+// output, so x and the residual are read once and the results written once
+// (the bytes the operator cannot do without); HBM bounds it for many rows,
+// the launch for few.  A thread holds kVec vectors of eight elements; a row
+// takes `wpr` whole warps, and a block several short rows.  Sixteen lanes
+// hold the 128 columns of one scale, so the block maximum is four shuffles.
+#include "sv_target.cuh"
+
+namespace sv {
+namespace {
+
+__device__ __forceinline__ float warp_max_nan(float x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x = max_nan(x, __shfl_xor_sync(0xffffffffu, x, o));
+  return x;
+}
+
+// scale = max(amax, 1e-30) / 448
+__device__ __forceinline__ float e4m3_scale(float amax) { return max_nan(amax, 1e-30f) / 448.0f; }
+
+__device__ __forceinline__ uint8_t to_e4m3(float y) {
+  return static_cast<uint8_t>(__nv_cvt_float_to_fp8(y, __NV_SATFINITE, __NV_E4M3));
+}
+
+// `red` holds one value for each of a row's wpr warps; all threads of the
+// block take part.
+template <class Op>
+__device__ __forceinline__ float row_reduce(float v, float *red, int wpr, int warp, int lane,
+                                            Op op) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = op(v, __shfl_xor_sync(0xffffffffu, v, o));
+  if (wpr == 1) return v;
+  if (lane == 0) red[warp] = v;
+  __syncthreads();
+  const int first = warp / wpr * wpr;
+  float r = red[first];
+  for (int i = 1; i < wpr; ++i) r = op(r, red[first + i]);
+  return r;
+}
+
+template <class T, int kVec, int kQuant>
+__global__ void norm_kernel(const NormParams P, int wpr) {
+  __shared__ float red[2][32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * ((blockDim.x >> 5) / wpr) + warp / wpr;
+  const bool live = row < P.rows;
+  const int t = (warp % wpr) * 32 + lane, step = wpr * 32;
+  const int nvec = P.d >> 3;
+  const T *w = static_cast<const T *>(P.w);
+  pdl_wait();
+  pdl_launch_dependents();
+  float h[kVec][8];
+  {
+    const T *x = static_cast<const T *>(P.x) + row * P.xs;
+    const T *r = static_cast<const T *>(P.res) + row * P.rs;
+    Vec8<T> xv[kVec], rv[kVec];
+#pragma unroll
+    for (int v = 0; v < kVec; ++v) {
+      const int i = t + v * step;
+      if (live && i < nvec) {
+        xv[v] = load8(x + 8 * i);
+        if (P.res) rv[v] = load8(r + 8 * i);
+      }
+    }
+#pragma unroll
+    for (int v = 0; v < kVec; ++v) {
+      const bool in = live && t + v * step < nvec;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        float s = in ? to_float(xv[v].e[e]) : 0.0f;
+        if (P.res && in) s += to_float(rv[v].e[e]);
+        h[v][e] = s;
+      }
+    }
+  }
+  float ss = 0.0f;
+#pragma unroll
+  for (int v = 0; v < kVec; ++v)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) ss = fmaf(h[v][e], h[v][e], ss);
+  ss = row_reduce(ss, red[0], wpr, warp, lane, [](float a, float b) { return a + b; });
+  const float inv = 1.0f / sqrtf(ss / static_cast<float>(P.d) + P.eps);
+
+  float rmax = 0.0f;
+#pragma unroll
+  for (int v = 0; v < kVec; ++v) {
+    const int i = t + v * step;
+    const bool in = live && i < nvec;
+    if (in && P.res_out) {
+      Vec8<T> o;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) o.e[e] = from_float<T>(h[v][e]);
+      store8(static_cast<T *>(P.res_out) + row * P.ros + 8 * i, o);
+    }
+    if (in) {
+      const Vec8<T> wv = load8(w + 8 * i);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) h[v][e] = h[v][e] * inv * to_float(wv.e[e]);
+    }
+    if constexpr (kQuant == 0) {
+      if (in) {
+        Vec8<T> o;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o.e[e] = from_float<T>(h[v][e]);
+        store8(static_cast<T *>(P.out) + row * P.os + 8 * i, o);
+      }
+    } else {
+      // lanes past the row hold zeros
+      float m = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) m = max_nan(m, fabsf(h[v][e]));
+      if constexpr (kQuant == 1) {
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+        const float s = e4m3_scale(m);
+        if (in) {
+          alignas(8) uint8_t q[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) q[e] = to_e4m3(h[v][e] / s);
+          *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(P.out) + row * P.os + 8 * i) =
+              *reinterpret_cast<const uint2 *>(q);
+          if ((i & 15) == 0)
+            P.scale[row * ((P.d + 127) / 128) + (i >> 4)] = s;
+        }
+      } else {
+        rmax = max_nan(rmax, m);
+      }
+    }
+  }
+  if constexpr (kQuant == 2) {
+    rmax = row_reduce(rmax, red[1], wpr, warp, lane,
+                      [](float a, float b) { return max_nan(a, b); });
+    const float s = e4m3_scale(rmax);
+#pragma unroll
+    for (int v = 0; v < kVec; ++v) {
+      const int i = t + v * step;
+      if (live && i < nvec) {
+        alignas(8) uint8_t q[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) q[e] = to_e4m3(h[v][e] / s);
+        *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(P.out) + row * P.os + 8 * i) =
+            *reinterpret_cast<const uint2 *>(q);
+      }
+    }
+    if (live && t == 0) P.scale[row] = s;
+  }
+}
+
+// Any width, stride and alignment: one block a row, the row read once for
+// each of sum, maximum (row scale) and output (the later reads come from
+// cache).  A thread rereads only elements that it writes itself, so the
+// in-place forms hold here too.
+constexpr int kAnyThreads = 512;
+template <class T>
+__global__ void __launch_bounds__(kAnyThreads) norm_any_kernel(const NormParams P) {
+  __shared__ float red[2][32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t row = blockIdx.x;
+  const T *x = static_cast<const T *>(P.x) + row * P.xs;
+  const T *r = P.res ? static_cast<const T *>(P.res) + row * P.rs : nullptr;
+  const T *w = static_cast<const T *>(P.w);
+  T *ro = P.res_out ? static_cast<T *>(P.res_out) + row * P.ros : nullptr;
+  pdl_wait();
+  pdl_launch_dependents();
+  auto at = [&](int i) { return r ? to_float(x[i]) + to_float(r[i]) : to_float(x[i]); };
+  // a warp takes 128 columns at a time, lane l the columns l, l + 32, ...
+  auto each = [&](auto &&f) {
+    for (int g = warp * 128; g < P.d; g += kAnyThreads * 4) f(g);
+  };
+  float ss = 0.0f;
+  each([&](int g) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int i = g + 32 * k + lane;
+      if (i < P.d) {
+        const float h = at(i);
+        ss = fmaf(h, h, ss);
+      }
+    }
+  });
+  ss = row_reduce(ss, red[0], kAnyThreads / 32, warp, lane,
+                  [](float a, float b) { return a + b; });
+  const float inv = 1.0f / sqrtf(ss / static_cast<float>(P.d) + P.eps);
+  float s = 0.0f;
+  if (P.quant == 2) {
+    float m = 0.0f;
+    each([&](int g) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int i = g + 32 * k + lane;
+        if (i < P.d) m = max_nan(m, fabsf(at(i) * inv * to_float(w[i])));
+      }
+    });
+    s = e4m3_scale(row_reduce(m, red[1], kAnyThreads / 32, warp, lane,
+                              [](float a, float b) { return max_nan(a, b); }));
+    if (threadIdx.x == 0) P.scale[row] = s;
+  }
+  each([&](int g) {
+    float y[4], m = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int i = g + 32 * k + lane;
+      y[k] = 0.0f;
+      if (i < P.d) {
+        const float h = at(i);
+        if (ro) ro[i] = from_float<T>(h);
+        y[k] = h * inv * to_float(w[i]);
+      }
+      m = max_nan(m, fabsf(y[k]));
+    }
+    if (P.quant == 1) {
+      s = e4m3_scale(warp_max_nan(m));
+      if (lane == 0) P.scale[row * ((P.d + 127) / 128) + g / 128] = s;
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int i = g + 32 * k + lane;
+      if (i >= P.d) break;
+      if (P.quant)
+        static_cast<uint8_t *>(P.out)[row * P.os + i] = to_e4m3(y[k] / s);
+      else
+        static_cast<T *>(P.out)[row * P.os + i] = from_float<T>(y[k]);
+    }
+  });
+}
+
+template <class T, int kVec>
+cudaError_t launch_vec(const NormParams &P, int wpr, int per_block, cudaStream_t stream) {
+  const dim3 grid(static_cast<unsigned>((P.rows + per_block - 1) / per_block));
+  const dim3 block(32 * wpr * per_block);
+  switch (P.quant) {
+    case 0: return launch_chained(norm_kernel<T, kVec, 0>, grid, block, 0, stream, P, wpr);
+    case 1: return launch_chained(norm_kernel<T, kVec, 1>, grid, block, 0, stream, P, wpr);
+    default: return launch_chained(norm_kernel<T, kVec, 2>, grid, block, 0, stream, P, wpr);
+  }
+}
+
+template <class T>
+cudaError_t launch_typed(const NormParams &P, cudaStream_t stream) {
+  auto ok = [](const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; };
+  const int es = sizeof(T);
+  const bool vec = P.d % 8 == 0 && P.d <= 32768 && P.xs * es % 16 == 0 && ok(P.x) && ok(P.w) &&
+                   (!P.res || (P.rs * es % 16 == 0 && ok(P.res))) &&
+                   (!P.res_out || (P.ros * es % 16 == 0 && ok(P.res_out))) &&
+                   (P.quant ? (reinterpret_cast<uintptr_t>(P.out) & 7u) == 0
+                            : P.os * es % 16 == 0 && ok(P.out));
+  if (!vec)
+    return launch_chained(norm_any_kernel<T>, dim3(static_cast<unsigned>(P.rows)),
+                          dim3(kAnyThreads), 0, stream, P);
+  const int nvec = P.d / 8;
+  const int kvec = nvec <= 1024 ? 1 : nvec <= 2048 ? 2 : 4;
+  const int wpr = (nvec + 32 * kvec - 1) / (32 * kvec);
+  const int per_block = wpr >= 4 ? 1 : 4 / wpr;
+  switch (kvec) {
+    case 1: return launch_vec<T, 1>(P, wpr, per_block, stream);
+    case 2: return launch_vec<T, 2>(P, wpr, per_block, stream);
+    default: return launch_vec<T, 4>(P, wpr, per_block, stream);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_norm(const NormParams &P, int num_sms, cudaStream_t stream) {
+  (void)num_sms;
+  switch (P.dtype) {
+    case SV_BF16: return launch_typed<__nv_bfloat16>(P, stream);
+    case SV_FP16: return launch_typed<__half>(P, stream);
+    default: return launch_typed<float>(P, stream);
+  }
+}
+
+}  // namespace sv
