@@ -19,8 +19,10 @@ INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 SOURCES = ["sv_api.cu", "sv_lmhead_tc.cu", "sv_lmhead_simt.cu", "sv_tail.cu", "sv_noalloc.cu",
            "sv_trunc.cu",
            "sv_ngram.cu",
-           "sv_target_api.cu", "sv_norm.cu", "sv_rope.cu", "sv_matmul8.cu", "sv_attn.cu"]
-HEADERS = ["sv_internal.cuh", "sv_kernels.h", "sv_target.cuh", "sv_attn.cuh"]
+           "sv_target_api.cu", "sv_norm.cu", "sv_rope.cu", "sv_matmul8.cu", "sv_attn.cu",
+           "sv_attn_tc.cu"]
+HEADERS = ["sv_internal.cuh", "sv_kernels.h", "sv_target.cuh", "sv_attn.cuh",
+           "sv_tmem.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
          "--expt-relaxed-constexpr", "-I", INCLUDE]

@@ -1,0 +1,977 @@
+// sv_attn_tc.cu -- attention of new tokens over the pages on the tensor
+// cores (bf16, fp16): tcgen05 products with the scores, the weights and the
+// output in tensor memory, K and V brought page by page by TMA.
+//
+//   o = sum_j softmax_j(scale q . k_j) v_j
+//
+// in one pass over the keys with a running maximum m and sum l of each row:
+// a tile of 128 keys gives S = Q K^T, P = 2^((S - m) scale log2 e), and
+// O += P V.  m only moves when a row's maximum has grown by more than 2^8, so
+// that O is rarely rescaled; P is at most 2^8 and l and O stay exact relative
+// to the m they were summed with.
+//
+//  * The rows of one cache head are its new tokens times the G = Hq / Hkv
+//    query heads that share it, so each K and V tile serves all of them.  An
+//    item is one (sequence, cache head, block of rows): up to 128 rows
+//    ("narrow": a verification round, single tokens) or 256 ("wide").
+//  * Two slots (S, P and O in tensor memory, one warpgroup for the softmax)
+//    work in turn, so that one slot's products run under the other's softmax.
+//    Wide: a slot holds 128 of the rows and both take every K and V tile.
+//    Narrow: both hold the same rows, slot 0 takes the even tiles and slot 1
+//    the odd ones, and their sums are joined at the end.
+//  * A persistent grid, one CTA per SM; the (item, tile) units of the whole
+//    call are cut into equal runs, so ragged lengths and few sequences fill
+//    all SMs alike.  An item that is cut leaves its parts' (m, l, O) in the
+//    handle's scratch and a second launch joins them in a fixed order.  The
+//    lengths are read on the device: no host plan, a graph replays with new
+//    ones.
+//  * Warps 0-3 and 4-7: softmax of the two slots, one row a thread; warp 8:
+//    TMA into a ring of 16 or 32 KB tiles; warp 9: the products.
+//
+// What is masked must not count even where it is not finite: keys past the
+// sequence are zeroed in V's tile, and a row whose output is not finite is
+// taken again by attend_row, which multiplies only what the row sees.
+#include <cudaTypedefs.h>
+
+#include "sv_attn.cuh"
+#include "sv_tmem.cuh"
+
+namespace sv {
+namespace {
+
+constexpr int kKeys = 128;     // keys of a tile
+constexpr int kRows = 128;     // rows of a slot
+constexpr int kThreads = 320;
+constexpr int kSoftmaxWarps = 8;
+constexpr int kRingBytes = 160 * 1024;
+constexpr int kMaxSlots = 10;
+constexpr uint64_t kCleanupLimitNs = 2000000000ull;
+constexpr float kRescale = 8.0f;  // log2 of the growth of m that rescales O
+
+template <int DPAD>
+struct Shape {
+  static constexpr int kSlabs = DPAD / 64;          // 128-byte columns of a tile
+  static constexpr int kTileBytes = kKeys * DPAD * 2;
+  static constexpr int kSlots = kRingBytes / kTileBytes;
+  static constexpr int kQBytes = kRows * DPAD * 2;
+  static constexpr int kSmem = 1024 + 2 * kQBytes + kRingBytes;  // + Ctl
+};
+
+struct Ctl {
+  uint64_t full[kMaxSlots], empty[kMaxSlots];
+  uint64_t q_ready, s_full[2], p_ready[2], o_full, x_full, x_free, teardown;
+  uint32_t tmem;
+  int abort;
+  int slow;           // a softmax warp is in attend_row: waits go on
+  int issued, consumed;
+  int start_b;
+  int64_t start_off;
+  int64_t scan[kThreads / 32];
+  float xm[kRows], xl[kRows];
+};
+
+// A cut item's parts: where they lie and which rows they hold.
+struct Desc {
+  int64_t ub, total;  // first unit of the item, units of the call
+  int parts;          // CTAs the item's tiles are spread over (0: none)
+  int cost, ntiles;   // units of a tile, tiles of the item
+  int b, h, r0, rows;
+};
+
+// The parts of one CTA: [2][256 rows], (m, l) and then O.  Slot 0: the part
+// of an item that began in an earlier CTA; slot 1: of one that begins here.
+constexpr int kPartRows = 256;
+template <int DPAD>
+__host__ __device__ constexpr size_t part_floats() {
+  return static_cast<size_t>(kPartRows) * (DPAD + 2);
+}
+constexpr size_t kDescBytes = 64 * 1024;  // start of the scratch
+
+__device__ __forceinline__ int64_t cut_at(int64_t total, int c, int grid) {
+  return total * c / grid;
+}
+
+// Walks the items of a call from a unit on.
+struct Items {
+  const sv_attention_t &a;
+  int G;
+  SeqGeom s;
+  int b, h, m, nm;
+  int64_t ub;       // first unit of the current item
+  int cost, ntiles, tile_lo, r0, rows;
+
+  __device__ explicit Items(const sv_attention_t &arg) : a(arg), G(arg.Hq / arg.Hkv) {}
+
+  __device__ void item() {
+    const int total = s.n * G;
+    const int per = total > kRows ? 2 * kRows : kRows;
+    r0 = m * per;
+    rows = min(per, total - r0);
+    cost = rows > kRows ? 2 : 1;
+    int lo, hi, x;
+    key_range(a, s, r0 / G, lo, x);
+    key_range(a, s, (r0 + rows - 1) / G, x, hi);
+    tile_lo = lo / kKeys;
+    ntiles = max(1, (hi + kKeys - 1) / kKeys - tile_lo);
+  }
+  __device__ void sequence() {
+    const int total = s.n * G;
+    nm = total > kRows ? (total + 2 * kRows - 1) / (2 * kRows) : 1;
+  }
+  // Units of one cache head of the sequence.
+  __device__ int64_t head_units() {
+    int64_t u = 0;
+    if (s.n == 0) return 0;
+    sequence();
+    for (m = 0; m < nm; ++m) {
+      item();
+      u += static_cast<int64_t>(ntiles) * cost;
+    }
+    return u;
+  }
+  __device__ void seek(int b0, int64_t off, int64_t u) {
+    bool bad;
+    b = b0;
+    s = seq_geom(a, b, &bad);
+    const int64_t per = head_units();
+    h = static_cast<int>(off / per);
+    off -= h * per;
+    for (m = 0;; ++m) {
+      item();
+      const int64_t n = static_cast<int64_t>(ntiles) * cost;
+      if (off < n) break;
+      off -= n;
+    }
+    ub = u - off;
+  }
+  // The next item; its units follow the current ones.  False: none left.
+  __device__ bool next() {
+    ub += static_cast<int64_t>(ntiles) * cost;
+    if (++m == nm) {
+      m = 0;
+      if (++h == a.Hkv) {
+        h = 0;
+        do {
+          if (++b >= a.B) return false;
+          bool bad;
+          s = seq_geom(a, b, &bad);
+        } while (s.n == 0);
+        sequence();
+      }
+    }
+    item();
+    return true;
+  }
+};
+
+// The tiles of an item in the units [u0, u1).
+__device__ __forceinline__ void tile_run(int64_t ub, int cost, int ntiles, int64_t u0, int64_t u1,
+                                         int &tb, int &te) {
+  const int64_t lo = u0 > ub ? (u0 - ub + cost - 1) / cost : 0;
+  const int64_t hi = u1 > ub ? (u1 - ub + cost - 1) / cost : 0;
+  tb = static_cast<int>(lo < ntiles ? lo : ntiles);
+  te = static_cast<int>(hi < ntiles ? hi : ntiles);
+}
+
+// Ring positions of an item's K and V tiles (n tiles): wide K0 V0 K1 V1 ...,
+// narrow K0 K1 V0 K2 V1 ... K(n-1) V(n-2) V(n-1), the order of their use.
+__device__ __forceinline__ int k_pos(bool wide, int t) {
+  return wide ? 2 * t : (t < 2 ? t : 2 * t - 1);
+}
+__device__ __forceinline__ int v_pos(bool wide, int t, int n) {
+  return wide ? 2 * t + 1 : min(2 * t + 2, 2 * n - 1);
+}
+// The inverse: which tile, K or V, comes at position p.
+__device__ __forceinline__ int tile_at(bool wide, int p, int n, bool &is_v) {
+  if (wide) {
+    is_v = p & 1;
+    return p >> 1;
+  }
+  if (p == 2 * n - 1) {
+    is_v = true;
+    return n - 1;
+  }
+  if (p < 2) {
+    is_v = false;
+    return p;
+  }
+  is_v = (p & 1) == 0;
+  return is_v ? (p - 2) / 2 : (p + 1) / 2;
+}
+
+// Waits on a barrier with the whole warp; false (and the abort flag) when the
+// limit ran out or another role gave up.  A softmax warp in attend_row holds
+// the others up for as long as it takes, so the limit starts over then.
+__device__ __forceinline__ bool wait_warp(Ctl *ctl, uint64_t *bar, uint32_t parity,
+                                          uint64_t limit_ns, int *status) {
+  const uint32_t at = smem_u32(bar);
+  const volatile int *abort = &ctl->abort, *slow = &ctl->slow;
+  bool ok;
+  do {
+    ok = mbar_wait(at, parity, limit_ns, abort);
+  } while (!ok && !*abort && *slow > 0);
+  if (__all_sync(0xffffffffu, ok)) return true;
+  if ((threadIdx.x & 31) == 0) {
+    *reinterpret_cast<volatile int *>(&ctl->abort) = 1;
+    set_status(status, SV_ERR_TIMEOUT);
+  }
+  __syncwarp();
+  return false;
+}
+
+// 32 bits of a tree row from bit s on (s may be negative): the context before
+// the new tokens is seen, what lies past the words is not.
+__device__ __forceinline__ uint32_t tree_bits(const int32_t *row, int words, int s) {
+  const int w = s >> 5;
+  auto word = [&](int i) {
+    return i < 0 ? 0xffffffffu : i < words ? static_cast<uint32_t>(__ldg(row + i)) : 0u;
+  };
+  return __funnelshift_r(word(w), word(w + 1), s & 31);
+}
+// Bits i of [lo, hi) of a group of 32 keys.
+__device__ __forceinline__ uint32_t range_bits(int lo, int hi) {
+  const uint32_t below = hi >= 32 ? 0xffffffffu : hi <= 0 ? 0u : (1u << hi) - 1u;
+  const uint32_t under = lo >= 32 ? 0xffffffffu : lo <= 0 ? 0u : (1u << lo) - 1u;
+  return below & ~under;
+}
+
+template <class T>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi);
+template <>
+__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t *>(&v);
+}
+template <>
+__device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+struct TcArgs {
+  sv_attention_t a;
+  float *scratch;
+  int *status;
+  uint64_t wait_limit_ns;
+  float c;       // |scale| log2 e, kept above zero
+  int negate;    // scale < 0: the queries are negated
+  int pow_page;  // log2 of the page size
+};
+
+// Stores one row of the output; `fast`: 16-byte aligned rows and D a multiple
+// of 8.
+template <class T, int DPAD>
+__device__ __forceinline__ void store_row(const sv_attention_t &a, T *o, int d0, const float *x,
+                                          bool fast) {
+#pragma unroll
+  for (int v = 0; v < 32; v += 8) {
+    if (d0 + v >= a.D) break;
+    if (fast) {
+      uint4 q;
+      q.x = pack2<T>(x[v], x[v + 1]);
+      q.y = pack2<T>(x[v + 2], x[v + 3]);
+      q.z = pack2<T>(x[v + 4], x[v + 5]);
+      q.w = pack2<T>(x[v + 6], x[v + 7]);
+      *reinterpret_cast<uint4 *>(o + d0 + v) = q;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) o[d0 + v + e] = from_float<T>(x[v + e]);
+    }
+  }
+}
+
+template <class T, int DPAD>
+__global__ void __launch_bounds__(kThreads, 1)
+    attention_tc_kernel(const __grid_constant__ CUtensorMap tmK,
+                        const __grid_constant__ CUtensorMap tmV,
+                        const __grid_constant__ TcArgs args) {
+  using Sh = Shape<DPAD>;
+  constexpr bool kBf16 = sizeof(T) == 2 && !__is_same(T, __half);
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t *smem = smem_raw + (base - raw);
+  Ctl *ctl = reinterpret_cast<Ctl *>(smem + 2 * Sh::kQBytes + kRingBytes);
+  const uint32_t ring = base + 2 * Sh::kQBytes;
+  const sv_attention_t &a = args.a;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  Desc *desc = reinterpret_cast<Desc *>(args.scratch) + blockIdx.x;
+  float *parts = args.scratch + kDescBytes / 4;
+
+  if (tid == 0) {
+    for (int i = 0; i < Sh::kSlots; ++i) {
+      mbar_init(smem_u32(&ctl->full[i]), 1);
+      mbar_init(smem_u32(&ctl->empty[i]), 1);
+    }
+    mbar_init(smem_u32(&ctl->q_ready), kSoftmaxWarps);
+    for (int w = 0; w < 2; ++w) {
+      mbar_init(smem_u32(&ctl->s_full[w]), 1);
+      mbar_init(smem_u32(&ctl->p_ready[w]), kSoftmaxWarps / 2);
+    }
+    mbar_init(smem_u32(&ctl->o_full), 1);
+    mbar_init(smem_u32(&ctl->x_full), kSoftmaxWarps / 2);
+    mbar_init(smem_u32(&ctl->x_free), kSoftmaxWarps / 2);
+    mbar_init(smem_u32(&ctl->teardown), 1);
+    ctl->abort = ctl->slow = ctl->issued = ctl->consumed = 0;
+    ctl->start_b = -1;
+    mbar_fence_init();
+  }
+  if (warp == 8 && lane == 0) {
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
+  }
+  if (warp == 9) {
+    tmem_alloc(smem_u32(&ctl->tmem), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ctl->tmem;
+  pdl_wait();
+  pdl_launch_dependents();
+
+  // ---- this CTA's run of units ----
+  Items it(a);
+  int64_t mine = 0;  // units of sequence tid (the only one where B is small)
+  int64_t sum = 0;
+  for (int b = tid; b < a.B; b += kThreads) {
+    bool bad;
+    it.s = seq_geom(a, b, &bad);
+    if (bad && blockIdx.x == 0) set_status(args.status, SV_ERR_CACHE);
+    const int64_t u = it.head_units() * a.Hkv;
+    if (b == tid) mine = u;
+    sum += u;
+  }
+  auto warp_sum64 = [](int64_t x) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+  };
+  sum = warp_sum64(sum);
+  if (lane == 0) ctl->scan[warp] = sum;
+  __syncthreads();
+  int64_t total = 0;
+  for (int i = 0; i < kThreads / 32; ++i) total += ctl->scan[i];
+  const int64_t u0 = cut_at(total, blockIdx.x, gridDim.x);
+  const int64_t u1 = cut_at(total, blockIdx.x + 1, gridDim.x);
+  int64_t before = 0;
+  for (int b0 = 0; b0 < a.B; b0 += kThreads) {  // where u0 falls
+    const int b = b0 + tid;
+    int64_t u = mine;
+    if (b0 > 0) {
+      u = 0;
+      if (b < a.B) {
+        bool bad;
+        it.s = seq_geom(a, b, &bad);
+        u = it.head_units() * a.Hkv;
+      }
+    }
+    int64_t incl = u;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    __syncthreads();
+    if (lane == 31) ctl->scan[warp] = incl;
+    __syncthreads();
+    int64_t pre = before;
+    for (int i = 0; i < kThreads / 32; ++i) {
+      if (i < warp) pre += ctl->scan[i];
+      before += ctl->scan[i];
+    }
+    if (u > 0 && u0 < u1 && u0 >= pre + incl - u && u0 < pre + incl) {
+      ctl->start_b = b;
+      ctl->start_off = u0 - (pre + incl - u);
+    }
+  }
+  __syncthreads();
+  const int b_first = ctl->start_b;
+  const bool some = b_first >= 0;
+  if (some) it.seek(b_first, ctl->start_off, u0);
+  if (tid == 0) desc->parts = 0;
+
+  if (warp == 8) {
+    // ---------------- TMA ----------------
+    const uint64_t policy = policy_evict_normal();
+    const int page_keys = min(kKeys, a.page_size);
+    const uint32_t box_bytes = static_cast<uint32_t>(page_keys) * 128u;
+    int pos = 0;
+    bool ok = true;
+    for (bool more = some; more && ok && it.ub < u1; more = it.next()) {
+      int tb, te;
+      tile_run(it.ub, it.cost, it.ntiles, u0, u1, tb, te);
+      const int n = te - tb;
+      const bool wide = it.cost == 2;
+      const int32_t *pages = a.page_table + it.b * a.table_stride;
+      // lane i brings box i of a tile: page i / slabs, slab i % slabs (at most 32
+      // boxes, as a page holds 8 keys or more)
+      auto page_of = [&](int p) {
+        bool is_v;
+        const int k0 = (it.tile_lo + tb + tile_at(wide, p, n, is_v)) * kKeys;
+        const int key = k0 + lane / Sh::kSlabs * page_keys;
+        return lane / Sh::kSlabs < kKeys / page_keys && key < it.s.kv ? pages[key >> args.pow_page]
+                                                                      : 0;
+      };
+      int page = n > 0 ? page_of(0) : 0;
+      for (int p = 0; p < 2 * n; ++p, ++pos) {
+        const int slot = pos % Sh::kSlots;
+        bool is_v;
+        const int k0 = (it.tile_lo + tb + tile_at(wide, p, n, is_v)) * kKeys;
+        const int next = p + 1 < 2 * n ? page_of(p + 1) : 0;
+        const int boxes = max(0, (min(it.s.kv - k0, kKeys) + page_keys - 1) / page_keys);
+        if (!wait_warp(ctl, &ctl->empty[slot], ((pos / Sh::kSlots) & 1) ^ 1, args.wait_limit_ns,
+                       args.status)) {
+          ok = false;
+          break;
+        }
+        const uint32_t full = smem_u32(&ctl->full[slot]);
+        if (lane == 0) mbar_arrive_expect_tx(full, boxes * box_bytes * Sh::kSlabs);
+        __syncwarp();
+        if (lane < boxes * Sh::kSlabs) {
+          const int box = lane / Sh::kSlabs, slab = lane % Sh::kSlabs;
+          const int key = k0 + box * page_keys;
+          if (static_cast<uint32_t>(page) >= a.num_pages) set_status(args.status, SV_ERR_CACHE);
+          tma_load_4d(ring + slot * Sh::kTileBytes + slab * (kKeys * 128) + box * box_bytes,
+                      is_v ? &tmV : &tmK, slab * 64, it.h, key & (a.page_size - 1), page, full,
+                      policy);
+        }
+        page = next;
+        __syncwarp();
+        if (lane == 0) ctl->issued = pos + 1;
+      }
+    }
+  } else if (warp == 9) {
+    // ---------------- products ----------------
+    constexpr uint32_t idesc_s = idesc_16(kBf16, kRows, kKeys, false);
+    constexpr uint32_t idesc_o = idesc_16(kBf16, kRows, DPAD, true);
+    int pos0 = 0, items = 0, cnt[2] = {0, 0};
+    bool ok = true;
+    for (bool more = some; more && ok && it.ub < u1; more = it.next()) {
+      int tb, te;
+      tile_run(it.ub, it.cost, it.ntiles, u0, u1, tb, te);
+      const int n = te - tb;
+      if (n <= 0) continue;
+      const bool wide = it.cost == 2;
+      const int steps = wide ? 2 * n : n;
+      auto wait_tile = [&](int p) {
+        const int pos = pos0 + p;
+        const bool r = wait_warp(ctl, &ctl->full[pos % Sh::kSlots], (pos / Sh::kSlots) & 1,
+                                 args.wait_limit_ns, args.status);
+        if (r && lane == 0) ctl->consumed = max(ctl->consumed, pos + 1);
+        return r;
+      };
+      auto release = [&](int p) {
+        umma_commit(smem_u32(&ctl->empty[(pos0 + p) % Sh::kSlots]));
+      };
+      auto scores = [&](int i) {
+        const int w = i & 1, p = k_pos(wide, wide ? i >> 1 : i);
+        if ((!wide || w == 0) && !wait_tile(p)) return false;
+        tc_fence_after();
+        const uint64_t q = sw128_desc(base + (wide ? w : 0) * Sh::kQBytes);
+        const uint64_t k = sw128_desc(ring + (pos0 + p) % Sh::kSlots * Sh::kTileBytes);
+        if (elect_one()) {
+#pragma unroll
+          for (int e = 0; e < DPAD / 16; ++e) {
+            const uint32_t at = (e / 4) * (kKeys * 128 >> 4) + 2 * (e % 4);
+            umma_16(tmem + w * kKeys, q + at, k + at, idesc_s, e > 0);
+          }
+          umma_commit(smem_u32(&ctl->s_full[w]));
+          if (!wide || w == 1) release(p);
+        }
+        __syncwarp();
+        return true;
+      };
+      if (!wait_warp(ctl, &ctl->q_ready, items & 1, args.wait_limit_ns, args.status)) {
+        ok = false;
+        break;
+      }
+      ++items;
+      for (int i = 0; i < min(2, steps) && ok; ++i) ok = scores(i);
+      for (int i = 0; i < steps && ok; ++i) {
+        const int w = i & 1, t = wide ? i >> 1 : i, p = v_pos(wide, t, n);
+        if (!wide || w == 0) {
+          if (!(ok = wait_tile(p))) break;
+          // rows of V past the sequence hold anything: they get weight zero,
+          // which has to give zero
+          const int live = it.s.kv - (it.tile_lo + tb + t) * kKeys;
+          if (live < kKeys) {
+            uint8_t *v = smem + 2 * Sh::kQBytes + (pos0 + p) % Sh::kSlots * Sh::kTileBytes;
+            const int first = max(live, 0), count = (kKeys - first) * 8;
+            for (int x = lane; x < count * Sh::kSlabs; x += 32) {
+              const int slab = x / count, y = x - slab * count;
+              *reinterpret_cast<uint4 *>(v + slab * (kKeys * 128) + first * 128 + y * 16) =
+                  make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
+        }
+        if (!(ok = wait_warp(ctl, &ctl->p_ready[w], cnt[w] & 1, args.wait_limit_ns, args.status)))
+          break;
+        ++cnt[w];
+        tc_fence_after();
+        const uint64_t v =
+            sw128_desc_mn(ring + (pos0 + p) % Sh::kSlots * Sh::kTileBytes, kKeys * 128);
+        if (elect_one()) {
+#pragma unroll
+          for (int e = 0; e < kKeys / 16; ++e)
+            umma_16_ta(tmem + 256 + w * 128, tmem + w * kKeys + e * 8, v + e * (2048 >> 4),
+                       idesc_o, i > 1 || e > 0);
+          if (!wide || w == 1) release(p);
+        }
+        __syncwarp();
+        if (i + 2 < steps) ok = scores(i + 2);
+      }
+      if (!ok) break;
+      if (elect_one()) umma_commit(smem_u32(&ctl->o_full));
+      __syncwarp();
+      pos0 += 2 * n;
+    }
+    if (elect_one()) {
+      umma_commit(smem_u32(&ctl->teardown));
+      const int never = 0;
+      mbar_wait(smem_u32(&ctl->teardown), 0u, kCleanupLimitNs, &never);
+    }
+    __syncwarp();
+  } else {
+    // ---------------- softmax and output ----------------
+    const int w = warp >> 2;
+    const int row = tid & 127;
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + lanes + w * kKeys, tO = tmem + lanes + 256 + w * 128;
+    const bool out_fast = (reinterpret_cast<uintptr_t>(a.out) & 15u) == 0 &&
+                          ((a.o_token | a.o_head) & 7) == 0;
+    int items = 0, cnt = 0, narrow = 0;
+    bool ok = true;
+    for (bool more = some; more && ok && it.ub < u1; more = it.next()) {
+      int tb, te;
+      tile_run(it.ub, it.cost, it.ntiles, u0, u1, tb, te);
+      const int n = te - tb;
+      if (n <= 0) continue;
+      const bool wide = it.cost == 2;
+      // ---- this thread's row ----
+      const int r = wide ? w * kRows + row : row;
+      const bool valid = r < it.rows;
+      const int tok = valid ? (it.r0 + r) / it.G : 0;
+      const int head = it.h * it.G + (it.r0 + r) - tok * it.G;
+      const int64_t t = it.s.t0 + tok;
+      int lo = 0, hi = 0;
+      const int32_t *tree = nullptr;
+      if (valid) {
+        key_range(a, it.s, tok, lo, hi);
+        if (a.tree_mask) tree = a.tree_mask + t * a.tree_words;
+      }
+      if (wide || w == 0) {
+        const T *q = static_cast<const T *>(a.q) + t * a.q_token + head * a.q_head;
+        uint8_t *dst = smem + (wide ? w : 0) * Sh::kQBytes + row * 128;
+#pragma unroll
+        for (int v = 0; v < DPAD / 8; ++v) {
+          uint4 x = make_uint4(0, 0, 0, 0);
+          if (valid && 8 * v < a.D) x = *reinterpret_cast<const uint4 *>(q + 8 * v);
+          if (args.negate) {
+            x.x ^= 0x80008000u;
+            x.y ^= 0x80008000u;
+            x.z ^= 0x80008000u;
+            x.w ^= 0x80008000u;
+          }
+          *reinterpret_cast<uint4 *>(dst + (v / 8) * (kRows * 128) +
+                                     (((v % 8) ^ (row & 7)) << 4)) = x;
+        }
+        fence_proxy_async_smem();
+      }
+      tc_fence_before();  // the last item's reads of O come before its products
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&ctl->q_ready));
+
+      const bool live = __any_sync(0xffffffffu, valid);
+      const int steps = wide ? n : (n + 1 - w) / 2;
+      float m = -INFINITY, l = 0.0f;
+      for (int st = 0; st < steps; ++st) {
+        const int k0 = (it.tile_lo + tb + (wide ? st : 2 * st + w)) * kKeys;
+        if (!wait_warp(ctl, &ctl->s_full[w], cnt & 1, args.wait_limit_ns, args.status)) {
+          ok = false;
+          break;
+        }
+        ++cnt;
+        tc_fence_after();
+        if (live) {
+          uint32_t sr[128];
+#pragma unroll
+          for (int g = 0; g < 4; ++g) tmem_ld32(tS + 32 * g, sr + 32 * g);
+          tmem_ld_wait();
+#pragma unroll
+          for (int g = 0; g < 4; ++g) tmem_reg_fence32(sr + 32 * g);
+          float *x = reinterpret_cast<float *>(sr);
+          const bool whole = !valid || (lo <= k0 && hi >= k0 + kKeys &&
+                                        (!tree || k0 + kKeys <= it.s.ctx));
+          if (!__all_sync(0xffffffffu, whole)) {
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+              uint32_t keep = range_bits(lo - k0 - 32 * g, hi - k0 - 32 * g);
+              if (tree) keep &= tree_bits(tree, a.tree_words, k0 + 32 * g - it.s.ctx);
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (!(keep & (1u << i))) x[32 * g + i] = -INFINITY;
+            }
+          }
+          float top = -INFINITY;
+          {
+            float t8[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) t8[i] = fmaxf(x[i], x[i + 8]);
+#pragma unroll
+            for (int g = 16; g < 128; g += 8)
+#pragma unroll
+              for (int i = 0; i < 8; ++i) t8[i] = fmaxf(t8[i], x[g + i]);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) top = fmaxf(top, t8[i]);
+          }
+          const bool grow = m == -INFINITY ? top > -INFINITY : (top - m) * args.c > kRescale;
+          if (__any_sync(0xffffffffu, grow)) {
+            const float to = grow ? top : m;
+            const float f = grow ? (m == -INFINITY ? 0.0f : ex2((m - to) * args.c)) : 1.0f;
+            m = to;
+            l *= f;
+            if (st > 0) {
+              // the products of the last step are complete: they precede the
+              // scores of this one
+#pragma unroll
+              for (int g = 0; g < DPAD / 32; ++g) {
+                uint32_t o[32];
+                tmem_ld32(tO + 32 * g, o);
+                tmem_ld_wait();
+                tmem_reg_fence32(o);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                tmem_st32(tO + 32 * g, o);
+              }
+            }
+          }
+          const float off = m == -INFINITY ? 0.0f : -m * args.c;
+          float ls[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const int j = 64 * g + 2 * i;
+              const float p0 = ex2(fmaf(x[j], args.c, off));
+              const float p1 = ex2(fmaf(x[j + 1], args.c, off));
+              ls[i & 3] += p0 + p1;
+              sr[32 * g + i] = pack2<T>(p0, p1);
+            }
+            tmem_st32(tS + 32 * g, sr + 32 * g);
+          }
+          l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+          tmem_st_wait();
+          tc_fence_before();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&ctl->p_ready[w]));
+      }
+      if (!ok) break;
+      if (!wait_warp(ctl, &ctl->o_full, items & 1, args.wait_limit_ns, args.status)) {
+        ok = false;
+        break;
+      }
+      ++items;
+      tc_fence_after();
+
+      // ---- the item's result, or this CTA's part of it ----
+      float f0 = 1.0f, f1 = 0.0f;
+      const bool join = !wide && n > 1;
+      if (!wide) {
+        // slot 1 hands its m and l to slot 0, which reads both outputs
+        if (w == 1) {
+          if (narrow > 0 && !(ok = wait_warp(ctl, &ctl->x_free, (narrow - 1) & 1,
+                                             args.wait_limit_ns, args.status)))
+            break;
+          ctl->xm[row] = m;
+          ctl->xl[row] = l;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&ctl->x_full));
+        } else {
+          if (!(ok = wait_warp(ctl, &ctl->x_full, narrow & 1, args.wait_limit_ns, args.status)))
+            break;
+          const float m1 = ctl->xm[row], l1 = ctl->xl[row];
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&ctl->x_free));
+          if (join) {
+            const float to = fmaxf(m, m1);
+            f0 = m == -INFINITY ? 0.0f : ex2((m - to) * args.c);
+            f1 = m1 == -INFINITY ? 0.0f : ex2((m1 - to) * args.c);
+            l = l * f0 + l1 * f1;
+            m = to;
+          }
+        }
+        ++narrow;
+      }
+      if ((wide || w == 0) && live) {
+        const bool all = tb == 0 && te == it.ntiles;
+        const int slot = tb > 0 ? 0 : 1;
+        float *part = parts + (static_cast<size_t>(blockIdx.x) * 2 + slot) * part_floats<DPAD>();
+        const float inv = l != 0.0f ? 1.0f / l : 0.0f;
+        T *o = static_cast<T *>(a.out) + t * a.o_token + head * a.o_head;
+        bool fine = true;
+#pragma unroll
+        for (int g = 0; g < DPAD / 32; ++g) {
+          uint32_t y[32], z[32];
+          tmem_ld32(tO + 32 * g, y);
+          if (join) tmem_ld32(tO + 128 + 32 * g, z);
+          tmem_ld_wait();
+          tmem_reg_fence32(y);
+          tmem_reg_fence32(z);
+          float x[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            // a slot that saw nothing has nothing to add
+            x[i] = __uint_as_float(y[i]);
+            if (join) {
+              x[i] = f0 != 0.0f ? x[i] * f0 : 0.0f;
+              if (f1 != 0.0f) x[i] = fmaf(__uint_as_float(z[i]), f1, x[i]);
+            }
+          }
+          if (all) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              x[i] = l != 0.0f ? x[i] * inv : 0.0f;
+              fine &= fabsf(x[i]) < INFINITY;
+            }
+            if (valid) store_row<T, DPAD>(a, o, 32 * g, x, out_fast);
+          } else if (valid) {
+            float4 *d = reinterpret_cast<float4 *>(part + 2 * kPartRows +
+                                                   static_cast<size_t>(r) * DPAD + 32 * g);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              d[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+          }
+        }
+        if (valid) {
+          if (all) {
+            if (a.lse)
+              a.lse[t * a.Hq + head] =
+                  l != 0.0f ? m * (args.c * 0.69314718055994531f) + logf(l) : -INFINITY;
+          } else {
+            reinterpret_cast<float2 *>(part)[r] = make_float2(m, l);
+          }
+        }
+        if (!all && slot == 1 && tid == 0) {
+          const int64_t ue = it.ub + static_cast<int64_t>(it.ntiles) * it.cost;
+          // the CTA that holds the item's last unit
+          const int last = static_cast<int>((ue * gridDim.x + total - 1) / total) - 1;
+          Desc d;
+          d.ub = it.ub;
+          d.total = total;
+          d.parts = last - static_cast<int>(blockIdx.x) + 1;
+          d.cost = it.cost;
+          d.ntiles = it.ntiles;
+          d.b = it.b;
+          d.h = it.h;
+          d.r0 = it.r0;
+          d.rows = it.rows;
+          *desc = d;
+        }
+        unsigned again = __ballot_sync(0xffffffffu, all && valid && !fine);
+        if (again) {
+          if (lane == 0) atomicAdd(&ctl->slow, 1);
+          __syncwarp();
+          while (again) {
+            const int src = __ffs(again) - 1;
+            again &= again - 1;
+            attend_row<T>(a, it.s, it.b, __shfl_sync(0xffffffffu, tok, src),
+                          __shfl_sync(0xffffffffu, head, src), lane, args.status);
+          }
+          __syncwarp();
+          if (lane == 0) atomicSub(&ctl->slow, 1);
+        }
+      }
+    }
+  }
+
+  // ---------------- teardown ----------------
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 8 && lane == 0) {
+    // only after an abort can copies still be in flight
+    const int never = 0;
+    for (int p = ctl->consumed; p < ctl->issued; ++p)
+      mbar_wait(smem_u32(&ctl->full[p % Sh::kSlots]),
+                static_cast<uint32_t>((p / Sh::kSlots) & 1), kCleanupLimitNs, &never);
+  }
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Joins the parts of the items that were cut: block (c, y) takes rows of the
+// item that begins in CTA c, a warp a row, the parts in order.
+constexpr int kJoinWarps = 8, kJoinBlocks = 4;
+template <class T, int DPAD>
+__global__ void __launch_bounds__(32 * kJoinWarps)
+    attention_join_kernel(const __grid_constant__ TcArgs args, int grid) {
+  const sv_attention_t &a = args.a;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  pdl_wait();
+  pdl_launch_dependents();
+  const Desc d = reinterpret_cast<const Desc *>(args.scratch)[blockIdx.x];
+  if (d.parts == 0) return;
+  const float *parts = args.scratch + kDescBytes / 4;
+  const int G = a.Hq / a.Hkv;
+  bool bad;
+  const SeqGeom s = seq_geom(a, d.b, &bad);
+  constexpr int kPer = DPAD / 32;
+  for (int r = blockIdx.y * kJoinWarps + warp; r < d.rows; r += kJoinBlocks * kJoinWarps) {
+    // (m, l) of 32 parts at a time, one a lane
+    float top = -INFINITY, sum = 0.0f, acc[kPer] = {};
+    for (int k0 = 0; k0 < d.parts; k0 += 32) {
+      const int k = k0 + lane, c = blockIdx.x + k;
+      const float *part = nullptr;
+      float2 ml = make_float2(-INFINITY, 0.0f);
+      if (k < d.parts) {
+        int tb, te;
+        tile_run(d.ub, d.cost, d.ntiles, cut_at(d.total, c, grid), cut_at(d.total, c + 1, grid),
+                 tb, te);
+        if (tb < te) {
+          part = parts + (static_cast<size_t>(c) * 2 + (k > 0 ? 0 : 1)) * part_floats<DPAD>();
+          ml = __ldcg(reinterpret_cast<const float2 *>(part) + r);
+        }
+      }
+      const float to = fmaxf(top, warp_max(ml.x));
+      const float keep = top == -INFINITY ? 0.0f : ex2((top - to) * args.c);
+      const float f = ml.x == -INFINITY ? 0.0f : ex2((ml.x - to) * args.c);
+      sum = sum * keep + warp_sum(ml.y * f);
+      top = to;
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) acc[e] = keep != 0.0f ? acc[e] * keep : 0.0f;
+      const int many = min(32, d.parts - k0);
+#pragma unroll 4
+      for (int j = 0; j < many; ++j) {
+        const float fj = __shfl_sync(0xffffffffu, f, j);
+        const float *pj = reinterpret_cast<const float *>(
+            __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(part), j));
+        if (fj == 0.0f) continue;  // nothing there, or nothing seen
+        const float *o = pj + 2 * kPartRows + static_cast<size_t>(r) * DPAD;
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) acc[e] = fmaf(__ldcg(o + lane + 32 * e), fj, acc[e]);
+      }
+    }
+    const int tok = (d.r0 + r) / G, head = d.h * G + (d.r0 + r) - tok * G;
+    const int64_t t = s.t0 + tok;
+    const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;
+    T *o = static_cast<T *>(a.out) + t * a.o_token + head * a.o_head;
+    bool fine = true;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) {
+      const float x = sum != 0.0f ? acc[e] * inv : 0.0f;
+      fine &= fabsf(x) < INFINITY;
+      if (lane + 32 * e < a.D) o[lane + 32 * e] = from_float<T>(x);
+    }
+    if (a.lse && lane == 0)
+      a.lse[t * a.Hq + head] =
+          sum != 0.0f ? top * (args.c * 0.69314718055994531f) + logf(sum) : -INFINITY;
+    if (__any_sync(0xffffffffu, !fine)) attend_row<T>(a, s, d.b, tok, head, lane, args.status);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void *p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                         &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  }();
+  return fn;
+}
+
+// Map of a cache [page, token, head, D]: box of 64 elements of up to 128
+// tokens of one page and head.
+bool encode_cache(CUtensorMap *map, const sv_attention_t &a, const void *base, int64_t page,
+                  int64_t token, int64_t head) {
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(a.D), static_cast<cuuint64_t>(a.Hkv),
+                              static_cast<cuuint64_t>(a.page_size),
+                              static_cast<cuuint64_t>(a.num_pages)};
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(head) * 2,
+                                 static_cast<cuuint64_t>(token) * 2,
+                                 static_cast<cuuint64_t>(page) * 2};
+  const cuuint32_t box[4] = {64, 1, static_cast<cuuint32_t>(a.page_size < kKeys ? a.page_size
+                                                                                : kKeys),
+                             1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  return encode_fn()(map,
+                     a.dtype == SV_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                        : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                     4, const_cast<void *>(base), dims, strides, box, estr,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <class T, int DPAD>
+int launch_typed(const spec_target &h, const TcArgs &args, const CUtensorMap &tmK,
+                 const CUtensorMap &tmV, cudaStream_t stream) {
+  constexpr int smem = Shape<DPAD>::kSmem + static_cast<int>(sizeof(Ctl));
+  static_assert(smem <= 232448, "shared memory of one SM");
+  // per device; a cheap call, so it is not remembered
+  if (cudaFuncSetAttribute(attention_tc_kernel<T, DPAD>,
+                           cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+    return SV_ERR_CUDA;
+  const int grid = h.num_sms;
+  if (kDescBytes + sizeof(float) * part_floats<DPAD>() * 2 * grid > h.scratch_bytes ||
+      sizeof(Desc) * grid > kDescBytes)
+    return SV_ERR_CUDA;
+  if (launch_chained(attention_tc_kernel<T, DPAD>, dim3(grid), dim3(kThreads), smem, stream, tmK,
+                     tmV, args) != cudaSuccess)
+    return SV_ERR_CUDA;
+  return launch_chained(attention_join_kernel<T, DPAD>, dim3(grid, kJoinBlocks),
+                        dim3(32 * kJoinWarps), 0, stream, args, grid) == cudaSuccess
+             ? SV_OK
+             : SV_ERR_CUDA;
+}
+
+}  // namespace
+
+int launch_attention_tc(const spec_target &h, const sv_attention_t &a, cudaStream_t stream) {
+  auto ok = [](const void *p, int64_t s0, int64_t s1, int64_t s2) {
+    return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ((s0 | s1 | s2) & 7) == 0;
+  };
+  // TMA takes positive strides below 2^40 bytes
+  auto span = [](int64_t s) { return s > 0 && s < (int64_t(1) << 38); };
+  if ((a.dtype != SV_BF16 && a.dtype != SV_FP16) || a.D % 8 != 0 || a.D > 128 ||
+      a.page_size < 8 || (a.page_size & (a.page_size - 1)) != 0 ||
+      !ok(a.q, a.q_token, a.q_head, 0) || !ok(a.k_cache, a.kc_page, a.kc_token, a.kc_head) ||
+      !ok(a.v_cache, a.vc_page, a.vc_token, a.vc_head) || !span(a.kc_page) ||
+      !span(a.kc_token) || !span(a.kc_head) || !span(a.vc_page) || !span(a.vc_token) ||
+      !span(a.vc_head))
+    return kNotTaken;
+  CUtensorMap tmK, tmV;
+  if (!encode_fn()) return SV_ERR_CUDA;
+  if (!encode_cache(&tmK, a, a.k_cache, a.kc_page, a.kc_token, a.kc_head) ||
+      !encode_cache(&tmV, a, a.v_cache, a.vc_page, a.vc_token, a.vc_head))
+    return kNotTaken;
+  TcArgs args{};
+  args.a = a;
+  args.scratch = h.scratch;
+  args.status = h.status;
+  args.wait_limit_ns = h.wait_limit_ns;
+  // a scale of zero becomes one too small to matter, so that -inf stays -inf
+  const float c = fabsf(a.scale) * 1.4426950408889634f;
+  args.c = c > 1e-37f ? c : 1e-37f;
+  args.negate = a.scale < 0.0f;
+  while ((1 << args.pow_page) < a.page_size) ++args.pow_page;
+  if (a.dtype == SV_BF16)
+    return a.D <= 64 ? launch_typed<__nv_bfloat16, 64>(h, args, tmK, tmV, stream)
+                     : launch_typed<__nv_bfloat16, 128>(h, args, tmK, tmV, stream);
+  return a.D <= 64 ? launch_typed<__half, 64>(h, args, tmK, tmV, stream)
+                   : launch_typed<__half, 128>(h, args, tmK, tmV, stream);
+}
+
+}  // namespace sv
