@@ -26,7 +26,9 @@
 //    lengths are read on the device: no host plan, a graph replays with new
 //    ones.
 //  * Warps 0-3 and 4-7: softmax of the two slots, one row a thread; warp 8:
-//    TMA into a ring of 16 or 32 KB tiles; warp 9: the products.
+//    TMA into a ring of 16 or 32 KB tiles; warp 9: the products; warp 10
+//    hands out the items; warp 11 completes the warpgroup that gives its
+//    registers to the others.
 //
 // What is masked must not count even where it is not finite: keys past the
 // sequence are zeroed in V's tile, and a row whose output is not finite is
@@ -41,7 +43,10 @@ namespace {
 
 constexpr int kKeys = 128;     // keys of a tile
 constexpr int kRows = 128;     // rows of a slot
-constexpr int kThreads = 320;
+constexpr int kThreads = 384;
+// Registers a thread: 168 at launch; the softmax warpgroups take what the
+// third one gives back (256 * 216 + 128 * 72 = 384 * 168).
+constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
 constexpr int kSoftmaxWarps = 8;
 constexpr int kRingBytes = 160 * 1024;
 constexpr int kMaxSlots = 10;
@@ -57,7 +62,21 @@ struct Shape {
   static constexpr int kSmem = 1024 + 2 * kQBytes + kRingBytes;  // + Ctl
 };
 
+// One item of this CTA's run, as the scheduling warp hands it to the others.
+struct Run {
+  int n;            // tiles of it in this run; 0: no more items
+  int tile0;        // its first tile
+  int wide;         // 256 rows rather than 128
+  int whole;        // all of the item's tiles are here
+  int part;         // where its part goes: 0 it began earlier, 1 it begins here
+  int b, h, r0, rows;
+  SeqGeom s;
+};
+constexpr int kRuns = 4;
+
 struct Ctl {
+  Run run[kRuns];
+  uint64_t run_full[kRuns], run_empty[kRuns];
   uint64_t full[kMaxSlots], empty[kMaxSlots];
   uint64_t q_ready, s_full[2], p_ready[2], o_full, x_full, x_free, teardown;
   uint32_t tmem;
@@ -258,13 +277,13 @@ struct TcArgs {
   int pow_page;  // log2 of the page size
 };
 
-// Stores one row of the output; `fast`: 16-byte aligned rows and D a multiple
+// Stores 16 elements of a row of the output; `fast`: 16-byte aligned rows and D a multiple
 // of 8.
 template <class T, int DPAD>
 __device__ __forceinline__ void store_row(const sv_attention_t &a, T *o, int d0, const float *x,
                                           bool fast) {
 #pragma unroll
-  for (int v = 0; v < 32; v += 8) {
+  for (int v = 0; v < 16; v += 8) {
     if (d0 + v >= a.D) break;
     if (fast) {
       uint4 q;
@@ -302,6 +321,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < Sh::kSlots; ++i) {
       mbar_init(smem_u32(&ctl->full[i]), 1);
       mbar_init(smem_u32(&ctl->empty[i]), 1);
+    }
+    for (int i = 0; i < kRuns; ++i) {
+      mbar_init(smem_u32(&ctl->run_full[i]), 1);
+      mbar_init(smem_u32(&ctl->run_empty[i]), kSoftmaxWarps + 2);
     }
     mbar_init(smem_u32(&ctl->q_ready), kSoftmaxWarps);
     for (int w = 0; w < 2; ++w) {
@@ -388,174 +411,41 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   __syncthreads();
   const int b_first = ctl->start_b;
-  const bool some = b_first >= 0;
-  if (some) it.seek(b_first, ctl->start_off, u0);
-  if (tid == 0) desc->parts = 0;
-
-  if (warp == 8) {
-    // ---------------- TMA ----------------
-    const uint64_t policy = policy_evict_normal();
-    const int page_keys = min(kKeys, a.page_size);
-    const uint32_t box_bytes = static_cast<uint32_t>(page_keys) * 128u;
-    int pos = 0;
-    bool ok = true;
-    for (bool more = some; more && ok && it.ub < u1; more = it.next()) {
-      int tb, te;
-      tile_run(it.ub, it.cost, it.ntiles, u0, u1, tb, te);
-      const int n = te - tb;
-      const bool wide = it.cost == 2;
-      const int32_t *pages = a.page_table + it.b * a.table_stride;
-      // lane i brings box i of a tile: page i / slabs, slab i % slabs (at most 32
-      // boxes, as a page holds 8 keys or more)
-      auto page_of = [&](int p) {
-        bool is_v;
-        const int k0 = (it.tile_lo + tb + tile_at(wide, p, n, is_v)) * kKeys;
-        const int key = k0 + lane / Sh::kSlabs * page_keys;
-        return lane / Sh::kSlabs < kKeys / page_keys && key < it.s.kv ? pages[key >> args.pow_page]
-                                                                      : 0;
-      };
-      int page = n > 0 ? page_of(0) : 0;
-      for (int p = 0; p < 2 * n; ++p, ++pos) {
-        const int slot = pos % Sh::kSlots;
-        bool is_v;
-        const int k0 = (it.tile_lo + tb + tile_at(wide, p, n, is_v)) * kKeys;
-        const int next = p + 1 < 2 * n ? page_of(p + 1) : 0;
-        const int boxes = max(0, (min(it.s.kv - k0, kKeys) + page_keys - 1) / page_keys);
-        if (!wait_warp(ctl, &ctl->empty[slot], ((pos / Sh::kSlots) & 1) ^ 1, args.wait_limit_ns,
-                       args.status)) {
-          ok = false;
-          break;
-        }
-        const uint32_t full = smem_u32(&ctl->full[slot]);
-        if (lane == 0) mbar_arrive_expect_tx(full, boxes * box_bytes * Sh::kSlabs);
-        __syncwarp();
-        if (lane < boxes * Sh::kSlabs) {
-          const int box = lane / Sh::kSlabs, slab = lane % Sh::kSlabs;
-          const int key = k0 + box * page_keys;
-          if (static_cast<uint32_t>(page) >= a.num_pages) set_status(args.status, SV_ERR_CACHE);
-          tma_load_4d(ring + slot * Sh::kTileBytes + slab * (kKeys * 128) + box * box_bytes,
-                      is_v ? &tmV : &tmK, slab * 64, it.h, key & (a.page_size - 1), page, full,
-                      policy);
-        }
-        page = next;
-        __syncwarp();
-        if (lane == 0) ctl->issued = pos + 1;
-      }
-    }
-  } else if (warp == 9) {
-    // ---------------- products ----------------
-    constexpr uint32_t idesc_s = idesc_16(kBf16, kRows, kKeys, false);
-    constexpr uint32_t idesc_o = idesc_16(kBf16, kRows, DPAD, true);
-    int pos0 = 0, items = 0, cnt[2] = {0, 0};
-    bool ok = true;
-    for (bool more = some; more && ok && it.ub < u1; more = it.next()) {
-      int tb, te;
-      tile_run(it.ub, it.cost, it.ntiles, u0, u1, tb, te);
-      const int n = te - tb;
-      if (n <= 0) continue;
-      const bool wide = it.cost == 2;
-      const int steps = wide ? 2 * n : n;
-      auto wait_tile = [&](int p) {
-        const int pos = pos0 + p;
-        const bool r = wait_warp(ctl, &ctl->full[pos % Sh::kSlots], (pos / Sh::kSlots) & 1,
-                                 args.wait_limit_ns, args.status);
-        if (r && lane == 0) ctl->consumed = max(ctl->consumed, pos + 1);
-        return r;
-      };
-      auto release = [&](int p) {
-        umma_commit(smem_u32(&ctl->empty[(pos0 + p) % Sh::kSlots]));
-      };
-      auto scores = [&](int i) {
-        const int w = i & 1, p = k_pos(wide, wide ? i >> 1 : i);
-        if ((!wide || w == 0) && !wait_tile(p)) return false;
-        tc_fence_after();
-        const uint64_t q = sw128_desc(base + (wide ? w : 0) * Sh::kQBytes);
-        const uint64_t k = sw128_desc(ring + (pos0 + p) % Sh::kSlots * Sh::kTileBytes);
-        if (elect_one()) {
-#pragma unroll
-          for (int e = 0; e < DPAD / 16; ++e) {
-            const uint32_t at = (e / 4) * (kKeys * 128 >> 4) + 2 * (e % 4);
-            umma_16(tmem + w * kKeys, q + at, k + at, idesc_s, e > 0);
-          }
-          umma_commit(smem_u32(&ctl->s_full[w]));
-          if (!wide || w == 1) release(p);
-        }
-        __syncwarp();
-        return true;
-      };
-      if (!wait_warp(ctl, &ctl->q_ready, items & 1, args.wait_limit_ns, args.status)) {
-        ok = false;
-        break;
-      }
-      ++items;
-      for (int i = 0; i < min(2, steps) && ok; ++i) ok = scores(i);
-      for (int i = 0; i < steps && ok; ++i) {
-        const int w = i & 1, t = wide ? i >> 1 : i, p = v_pos(wide, t, n);
-        if (!wide || w == 0) {
-          if (!(ok = wait_tile(p))) break;
-          // rows of V past the sequence hold anything: they get weight zero,
-          // which has to give zero
-          const int live = it.s.kv - (it.tile_lo + tb + t) * kKeys;
-          if (live < kKeys) {
-            uint8_t *v = smem + 2 * Sh::kQBytes + (pos0 + p) % Sh::kSlots * Sh::kTileBytes;
-            const int first = max(live, 0), count = (kKeys - first) * 8;
-            for (int x = lane; x < count * Sh::kSlabs; x += 32) {
-              const int slab = x / count, y = x - slab * count;
-              *reinterpret_cast<uint4 *>(v + slab * (kKeys * 128) + first * 128 + y * 16) =
-                  make_uint4(0, 0, 0, 0);
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-          }
-        }
-        if (!(ok = wait_warp(ctl, &ctl->p_ready[w], cnt[w] & 1, args.wait_limit_ns, args.status)))
-          break;
-        ++cnt[w];
-        tc_fence_after();
-        const uint64_t v =
-            sw128_desc_mn(ring + (pos0 + p) % Sh::kSlots * Sh::kTileBytes, kKeys * 128);
-        if (elect_one()) {
-#pragma unroll
-          for (int e = 0; e < kKeys / 16; ++e)
-            umma_16_ta(tmem + 256 + w * 128, tmem + w * kKeys + e * 8, v + e * (2048 >> 4),
-                       idesc_o, i > 1 || e > 0);
-          if (!wide || w == 1) release(p);
-        }
-        __syncwarp();
-        if (i + 2 < steps) ok = scores(i + 2);
-      }
-      if (!ok) break;
-      if (elect_one()) umma_commit(smem_u32(&ctl->o_full));
-      __syncwarp();
-      pos0 += 2 * n;
-    }
-    if (elect_one()) {
-      umma_commit(smem_u32(&ctl->teardown));
-      const int never = 0;
-      mbar_wait(smem_u32(&ctl->teardown), 0u, kCleanupLimitNs, &never);
-    }
+  // The next item for a role's warp; false: none left, or the call is given up.
+  int runs = 0;
+  auto take = [&]() {
+    const int i = runs % kRuns;
+    if (!wait_warp(ctl, &ctl->run_full[i], (runs / kRuns) & 1, args.wait_limit_ns, args.status))
+      return false;
+    ++runs;
+    return ctl->run[i].n > 0;
+  };
+  auto give_back = [&]() {
     __syncwarp();
-  } else {
+    if (lane == 0) mbar_arrive(smem_u32(&ctl->run_empty[(runs - 1) % kRuns]));
+  };
+
+  if (warp < kSoftmaxWarps) {
     // ---------------- softmax and output ----------------
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     const int w = warp >> 2;
     const int row = tid & 127;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + lanes + w * kKeys, tO = tmem + lanes + 256 + w * 128;
     const bool out_fast = (reinterpret_cast<uintptr_t>(a.out) & 15u) == 0 &&
                           ((a.o_token | a.o_head) & 7) == 0;
+    const int G = a.Hq / a.Hkv;
     int items = 0, cnt = 0, narrow = 0;
     bool ok = true;
-    for (bool more = some; more && ok && it.ub < u1; more = it.next()) {
-      int tb, te;
-      tile_run(it.ub, it.cost, it.ntiles, u0, u1, tb, te);
-      const int n = te - tb;
-      if (n <= 0) continue;
-      const bool wide = it.cost == 2;
+    while (ok && take()) {
+      const Run &it = ctl->run[(runs - 1) % kRuns];
+      const int n = it.n;
+      const bool wide = it.wide;
       // ---- this thread's row ----
       const int r = wide ? w * kRows + row : row;
       const bool valid = r < it.rows;
-      const int tok = valid ? (it.r0 + r) / it.G : 0;
-      const int head = it.h * it.G + (it.r0 + r) - tok * it.G;
+      const int tok = valid ? (it.r0 + r) / G : 0;
+      const int head = it.h * G + (it.r0 + r) - tok * G;
       const int64_t t = it.s.t0 + tok;
       int lo = 0, hi = 0;
       const int32_t *tree = nullptr;
@@ -589,7 +479,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int steps = wide ? n : (n + 1 - w) / 2;
       float m = -INFINITY, l = 0.0f;
       for (int st = 0; st < steps; ++st) {
-        const int k0 = (it.tile_lo + tb + (wide ? st : 2 * st + w)) * kKeys;
+        const int k0 = (it.tile0 + (wide ? st : 2 * st + w)) * kKeys;
         if (!wait_warp(ctl, &ctl->s_full[w], cnt & 1, args.wait_limit_ns, args.status)) {
           ok = false;
           break;
@@ -638,14 +528,14 @@ __global__ void __launch_bounds__(kThreads, 1)
               // the products of the last step are complete: they precede the
               // scores of this one
 #pragma unroll
-              for (int g = 0; g < DPAD / 32; ++g) {
-                uint32_t o[32];
-                tmem_ld32(tO + 32 * g, o);
+              for (int g = 0; g < DPAD / 16; ++g) {
+                uint32_t o[16];
+                tmem_ld16(tO + 16 * g, o);
                 tmem_ld_wait();
-                tmem_reg_fence32(o);
+                tmem_reg_fence(o);
 #pragma unroll
-                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                tmem_st32(tO + 32 * g, o);
+                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                tmem_st16(tO + 16 * g, o);
               }
             }
           }
@@ -708,23 +598,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++narrow;
       }
       if ((wide || w == 0) && live) {
-        const bool all = tb == 0 && te == it.ntiles;
-        const int slot = tb > 0 ? 0 : 1;
-        float *part = parts + (static_cast<size_t>(blockIdx.x) * 2 + slot) * part_floats<DPAD>();
+        const bool all = it.whole;
+        float *part =
+            parts + (static_cast<size_t>(blockIdx.x) * 2 + it.part) * part_floats<DPAD>();
         const float inv = l != 0.0f ? 1.0f / l : 0.0f;
         T *o = static_cast<T *>(a.out) + t * a.o_token + head * a.o_head;
         bool fine = true;
 #pragma unroll
-        for (int g = 0; g < DPAD / 32; ++g) {
-          uint32_t y[32], z[32];
-          tmem_ld32(tO + 32 * g, y);
-          if (join) tmem_ld32(tO + 128 + 32 * g, z);
+        for (int g = 0; g < DPAD / 16; ++g) {
+          uint32_t y[16], z[16];
+          tmem_ld16(tO + 16 * g, y);
+          if (join) tmem_ld16(tO + 128 + 16 * g, z);
           tmem_ld_wait();
-          tmem_reg_fence32(y);
-          tmem_reg_fence32(z);
-          float x[32];
+          tmem_reg_fence(y);
+          tmem_reg_fence(z);
+          float x[16];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
+          for (int i = 0; i < 16; ++i) {
             // a slot that saw nothing has nothing to add
             x[i] = __uint_as_float(y[i]);
             if (join) {
@@ -734,16 +624,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (all) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
+            for (int i = 0; i < 16; ++i) {
               x[i] = l != 0.0f ? x[i] * inv : 0.0f;
               fine &= fabsf(x[i]) < INFINITY;
             }
-            if (valid) store_row<T, DPAD>(a, o, 32 * g, x, out_fast);
+            if (valid) store_row<T, DPAD>(a, o, 16 * g, x, out_fast);
           } else if (valid) {
             float4 *d = reinterpret_cast<float4 *>(part + 2 * kPartRows +
-                                                   static_cast<size_t>(r) * DPAD + 32 * g);
+                                                   static_cast<size_t>(r) * DPAD + 16 * g);
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
+            for (int i = 0; i < 4; ++i)
               d[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
           }
         }
@@ -755,22 +645,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           } else {
             reinterpret_cast<float2 *>(part)[r] = make_float2(m, l);
           }
-        }
-        if (!all && slot == 1 && tid == 0) {
-          const int64_t ue = it.ub + static_cast<int64_t>(it.ntiles) * it.cost;
-          // the CTA that holds the item's last unit
-          const int last = static_cast<int>((ue * gridDim.x + total - 1) / total) - 1;
-          Desc d;
-          d.ub = it.ub;
-          d.total = total;
-          d.parts = last - static_cast<int>(blockIdx.x) + 1;
-          d.cost = it.cost;
-          d.ntiles = it.ntiles;
-          d.b = it.b;
-          d.h = it.h;
-          d.r0 = it.r0;
-          d.rows = it.rows;
-          *desc = d;
         }
         unsigned again = __ballot_sync(0xffffffffu, all && valid && !fine);
         if (again) {
@@ -786,6 +660,195 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) atomicSub(&ctl->slow, 1);
         }
       }
+      give_back();
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp == 10) {
+      // ---------------- items ----------------
+      if (lane == 0) desc->parts = 0;
+      if (b_first >= 0) it.seek(b_first, ctl->start_off, u0);
+      bool more = b_first >= 0;
+      while (true) {
+        Run r{};
+        while (more && it.ub < u1) {
+          int tb, te;
+          tile_run(it.ub, it.cost, it.ntiles, u0, u1, tb, te);
+          if (te > tb) {
+            r.n = te - tb;
+            r.tile0 = it.tile_lo + tb;
+            r.wide = it.cost == 2;
+            r.whole = tb == 0 && te == it.ntiles;
+            r.part = tb > 0 ? 0 : 1;
+            r.b = it.b;
+            r.h = it.h;
+            r.r0 = it.r0;
+            r.rows = it.rows;
+            r.s = it.s;
+            if (!r.whole && r.part == 1 && lane == 0) {
+              // the CTA that holds the item's last unit
+              const int64_t ue = it.ub + static_cast<int64_t>(it.ntiles) * it.cost;
+              const int last = static_cast<int>((ue * gridDim.x + total - 1) / total) - 1;
+              *desc = Desc{it.ub, total, last - static_cast<int>(blockIdx.x) + 1, it.cost,
+                           it.ntiles, it.b, it.h, it.r0, it.rows};
+            }
+          }
+          more = it.next();
+          if (r.n > 0) break;
+        }
+        const int i = runs % kRuns;
+        if (!wait_warp(ctl, &ctl->run_empty[i], ((runs / kRuns) & 1) ^ 1, args.wait_limit_ns,
+                       args.status))
+          break;
+        if (lane == 0) {
+          ctl->run[i] = r;
+          mbar_arrive(smem_u32(&ctl->run_full[i]));
+        }
+        __syncwarp();
+        ++runs;
+        if (r.n == 0) break;
+      }
+    } else if (warp == 8) {
+      // ---------------- TMA ----------------
+      const uint64_t policy = policy_evict_normal();
+      const int page_keys = min(kKeys, a.page_size);
+      const uint32_t box_bytes = static_cast<uint32_t>(page_keys) * 128u;
+      int pos = 0;
+      bool ok = true;
+      while (ok && take()) {
+        const Run &it = ctl->run[(runs - 1) % kRuns];
+        const int n = it.n;
+        const bool wide = it.wide;
+        const int32_t *pages = a.page_table + it.b * a.table_stride;
+        // lane i brings box i of a tile: page i / slabs, slab i % slabs (at most 32
+        // boxes, as a page holds 8 keys or more)
+        auto page_of = [&](int p) {
+          bool is_v;
+          const int k0 = (it.tile0 + tile_at(wide, p, n, is_v)) * kKeys;
+          const int key = k0 + lane / Sh::kSlabs * page_keys;
+          const bool in = lane / Sh::kSlabs < kKeys / page_keys && key < it.s.kv;
+          return in ? pages[key >> args.pow_page] : 0;
+        };
+        int page = page_of(0);
+        for (int p = 0; p < 2 * n; ++p, ++pos) {
+          const int slot = pos % Sh::kSlots;
+          bool is_v;
+          const int k0 = (it.tile0 + tile_at(wide, p, n, is_v)) * kKeys;
+          const int next = p + 1 < 2 * n ? page_of(p + 1) : 0;
+          const int boxes = max(0, (min(it.s.kv - k0, kKeys) + page_keys - 1) / page_keys);
+          if (!wait_warp(ctl, &ctl->empty[slot], ((pos / Sh::kSlots) & 1) ^ 1, args.wait_limit_ns,
+                         args.status)) {
+            ok = false;
+            break;
+          }
+          const uint32_t full = smem_u32(&ctl->full[slot]);
+          if (lane == 0) mbar_arrive_expect_tx(full, boxes * box_bytes * Sh::kSlabs);
+          __syncwarp();
+          if (lane < boxes * Sh::kSlabs) {
+            const int box = lane / Sh::kSlabs, slab = lane % Sh::kSlabs;
+            const int key = k0 + box * page_keys;
+            if (static_cast<uint32_t>(page) >= a.num_pages) set_status(args.status, SV_ERR_CACHE);
+            tma_load_4d(ring + slot * Sh::kTileBytes + slab * (kKeys * 128) + box * box_bytes,
+                        is_v ? &tmV : &tmK, slab * 64, it.h, key & (a.page_size - 1), page, full,
+                        policy);
+          }
+          page = next;
+          __syncwarp();
+          if (lane == 0) ctl->issued = pos + 1;
+        }
+        give_back();
+      }
+    } else if (warp == 9) {
+      // ---------------- products ----------------
+      constexpr uint32_t idesc_s = idesc_16(kBf16, kRows, kKeys, false);
+      constexpr uint32_t idesc_o = idesc_16(kBf16, kRows, DPAD, true);
+      int pos0 = 0, items = 0, cnt[2] = {0, 0};
+      bool ok = true;
+      while (ok && take()) {
+        const Run &it = ctl->run[(runs - 1) % kRuns];
+        const int n = it.n;
+        const bool wide = it.wide;
+        const int steps = wide ? 2 * n : n;
+        auto wait_tile = [&](int p) {
+          const int pos = pos0 + p;
+          const bool r = wait_warp(ctl, &ctl->full[pos % Sh::kSlots], (pos / Sh::kSlots) & 1,
+                                   args.wait_limit_ns, args.status);
+          if (r && lane == 0) ctl->consumed = max(ctl->consumed, pos + 1);
+          return r;
+        };
+        auto release = [&](int p) {
+          umma_commit(smem_u32(&ctl->empty[(pos0 + p) % Sh::kSlots]));
+        };
+        auto scores = [&](int i) {
+          const int w = i & 1, p = k_pos(wide, wide ? i >> 1 : i);
+          if ((!wide || w == 0) && !wait_tile(p)) return false;
+          tc_fence_after();
+          const uint64_t q = sw128_desc(base + (wide ? w : 0) * Sh::kQBytes);
+          const uint64_t k = sw128_desc(ring + (pos0 + p) % Sh::kSlots * Sh::kTileBytes);
+          if (elect_one()) {
+#pragma unroll
+            for (int e = 0; e < DPAD / 16; ++e) {
+              const uint32_t at = (e / 4) * (kKeys * 128 >> 4) + 2 * (e % 4);
+              umma_16(tmem + w * kKeys, q + at, k + at, idesc_s, e > 0);
+            }
+            umma_commit(smem_u32(&ctl->s_full[w]));
+            if (!wide || w == 1) release(p);
+          }
+          __syncwarp();
+          return true;
+        };
+        if (!wait_warp(ctl, &ctl->q_ready, items & 1, args.wait_limit_ns, args.status)) {
+          ok = false;
+          break;
+        }
+        ++items;
+        for (int i = 0; i < min(2, steps) && ok; ++i) ok = scores(i);
+        for (int i = 0; i < steps && ok; ++i) {
+          const int w = i & 1, t = wide ? i >> 1 : i, p = v_pos(wide, t, n);
+          if (!wide || w == 0) {
+            if (!(ok = wait_tile(p))) break;
+            // rows of V past the sequence hold anything: they get weight zero,
+            // which has to give zero
+            const int live = it.s.kv - (it.tile0 + t) * kKeys;
+            if (live < kKeys) {
+              uint8_t *v = smem + 2 * Sh::kQBytes + (pos0 + p) % Sh::kSlots * Sh::kTileBytes;
+              const int first = max(live, 0), count = (kKeys - first) * 8;
+              for (int x = lane; x < count * Sh::kSlabs; x += 32) {
+                const int slab = x / count, y = x - slab * count;
+                *reinterpret_cast<uint4 *>(v + slab * (kKeys * 128) + first * 128 + y * 16) =
+                    make_uint4(0, 0, 0, 0);
+              }
+              fence_proxy_async_smem();
+              __syncwarp();
+            }
+          }
+          if (!(ok = wait_warp(ctl, &ctl->p_ready[w], cnt[w] & 1, args.wait_limit_ns, args.status)))
+            break;
+          ++cnt[w];
+          tc_fence_after();
+          const uint64_t v =
+              sw128_desc_mn(ring + (pos0 + p) % Sh::kSlots * Sh::kTileBytes, kKeys * 128);
+          if (elect_one()) {
+#pragma unroll
+            for (int e = 0; e < kKeys / 16; ++e)
+              umma_16_ta(tmem + 256 + w * 128, tmem + w * kKeys + e * 8, v + e * (2048 >> 4),
+                         idesc_o, i > 1 || e > 0);
+            if (!wide || w == 1) release(p);
+          }
+          __syncwarp();
+          if (i + 2 < steps) ok = scores(i + 2);
+        }
+        if (!ok) break;
+        if (elect_one()) umma_commit(smem_u32(&ctl->o_full));
+        give_back();
+        pos0 += 2 * n;
+      }
+      if (elect_one()) {
+        umma_commit(smem_u32(&ctl->teardown));
+        const int never = 0;
+        mbar_wait(smem_u32(&ctl->teardown), 0u, kCleanupLimitNs, &never);
+      }
+      __syncwarp();
     }
   }
 
