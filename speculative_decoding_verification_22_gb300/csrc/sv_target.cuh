@@ -16,6 +16,7 @@ struct spec_target {
   int *status = nullptr;   // device: first error since it was last read
   float *scratch = nullptr;  // device: partial results
   size_t scratch_bytes = 0;
+  int clusters[9] = {};    // the product's clusters of 1..8 CTAs that run at once
 };
 
 namespace sv {
@@ -89,6 +90,8 @@ struct MatmulParams {
   int64_t os;
   int M, N, K, kb, out_dtype;
 };
+// Fills h.clusters.
+cudaError_t plan_matmul_fp8(spec_target &h);
 int launch_matmul_fp8(const spec_target &h, const MatmulParams &P, cudaStream_t stream);
 
 int launch_attention(const spec_target &h, const sv_attention_t &a, cudaStream_t stream);

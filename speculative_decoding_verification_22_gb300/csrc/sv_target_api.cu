@@ -66,7 +66,8 @@ int spec_target_create(spec_target_t **out) {
       cudaMalloc(&h->scratch, h->scratch_bytes) != cudaSuccess ||
       cudaMemset(h->status, 0, sizeof(int)) != cudaSuccess ||
       cudaMemset(h->scratch, 0, h->scratch_bytes) != cudaSuccess ||
-      cudaStreamSynchronize(nullptr) != cudaSuccess) {
+      cudaStreamSynchronize(nullptr) != cudaSuccess ||
+      sv::plan_matmul_fp8(*h) != cudaSuccess) {
     spec_target_destroy(h);
     return SV_ERR_CUDA;
   }
