@@ -5,7 +5,7 @@
 //   o = sum_j softmax_j(scale q . k_j) v_j
 //
 // in one pass over the keys with a running maximum m and sum l of each row:
-// a tile of 128 keys gives S = Q K^T, P = 2^((S - m) scale log2 e), and
+// a tile of keys gives S = Q K^T, P = 2^((S - m) scale log2 e), and
 // O += P V.  m only moves when a row's maximum has grown by more than 2^8, so
 // that O is rarely rescaled; P is at most 2^8 and l and O stay exact relative
 // to the m they were summed with.
@@ -16,9 +16,11 @@
 //    ("narrow": a verification round, single tokens) or 256 ("wide").
 //  * Two slots (S, P and O in tensor memory, one warpgroup for the softmax)
 //    work in turn, so that one slot's products run under the other's softmax.
-//    Wide: a slot holds 128 of the rows and both take every K and V tile.
-//    Narrow: both hold the same rows, slot 0 takes the even tiles and slot 1
-//    the odd ones, and their sums are joined at the end.
+//    Wide: a slot holds 128 of the rows and both take every K and V tile of
+//    128 keys.  Narrow: both hold the same rows, slot 0 takes the even tiles
+//    of 64 keys and slot 1 the odd ones, and their sums are joined at the end.
+//    (Narrow is bound by the cache's bytes: with tiles of 128 keys the two
+//    slots held four fifths of the ring while it should have been loading.)
 //  * A persistent grid, one CTA per SM; the (item, tile) units of the whole
 //    call are cut into equal runs, so ragged lengths and few sequences fill
 //    all SMs alike.  An item that is cut leaves its parts' (m, l, O) in the
@@ -26,7 +28,7 @@
 //    lengths are read on the device: no host plan, a graph replays with new
 //    ones.
 //  * Warps 0-3 and 4-7: softmax of the two slots, one row a thread; warp 8:
-//    TMA into a ring of 16 or 32 KB tiles; warp 9: the products; warp 10
+//    TMA into a ring of 160 KB; warp 9: the products; warp 10
 //    hands out the items; warp 11 completes the warpgroup that gives its
 //    registers to the others.
 //
@@ -35,13 +37,15 @@
 // taken again by attend_row, which multiplies only what the row sees.
 #include <cudaTypedefs.h>
 
+#include <type_traits>
+
 #include "sv_attn.cuh"
 #include "sv_tmem.cuh"
 
 namespace sv {
 namespace {
 
-constexpr int kKeys = 128;     // keys of a tile
+constexpr int kWideKeys = 128, kNarrowKeys = 64;  // keys of a tile
 constexpr int kRows = 128;     // rows of a slot
 constexpr int kThreads = 384;
 // Registers a thread: 168 at launch; the softmax warpgroups take what the
@@ -56,8 +60,9 @@ constexpr float kRescale = 8.0f;  // log2 of the growth of m that rescales O
 template <int DPAD>
 struct Shape {
   static constexpr int kSlabs = DPAD / 64;          // 128-byte columns of a tile
-  static constexpr int kTileBytes = kKeys * DPAD * 2;
-  static constexpr int kSlots = kRingBytes / kTileBytes;
+  // A slot of the ring: a wide tile of K or V, or a narrow tile's K and V.
+  static constexpr int kSlotBytes = kWideKeys * DPAD * 2;
+  static constexpr int kSlots = kRingBytes / kSlotBytes;
   static constexpr int kQBytes = kRows * DPAD * 2;
   static constexpr int kSmem = 1024 + 2 * kQBytes + kRingBytes;  // + Ctl
 };
@@ -130,8 +135,9 @@ struct Items {
     int lo, hi, x;
     key_range(a, s, r0 / G, lo, x);
     key_range(a, s, (r0 + rows - 1) / G, x, hi);
-    tile_lo = lo / kKeys;
-    ntiles = max(1, (hi + kKeys - 1) / kKeys - tile_lo);
+    const int keys = cost == 2 ? kWideKeys : kNarrowKeys;
+    tile_lo = lo / keys;
+    ntiles = max(1, (hi + keys - 1) / keys - tile_lo);
   }
   __device__ void sequence() {
     const int total = s.n * G;
@@ -192,50 +198,35 @@ __device__ __forceinline__ void tile_run(int64_t ub, int cost, int ntiles, int64
   te = static_cast<int>(hi < ntiles ? hi : ntiles);
 }
 
-// Ring positions of an item's K and V tiles (n tiles): wide K0 V0 K1 V1 ...,
-// narrow K0 K1 V0 K2 V1 ... K(n-1) V(n-2) V(n-1), the order of their use.
-__device__ __forceinline__ int k_pos(bool wide, int t) {
-  return wide ? 2 * t : (t < 2 ? t : 2 * t - 1);
-}
-__device__ __forceinline__ int v_pos(bool wide, int t, int n) {
-  return wide ? 2 * t + 1 : min(2 * t + 2, 2 * n - 1);
-}
-// The inverse: which tile, K or V, comes at position p.
-__device__ __forceinline__ int tile_at(bool wide, int p, int n, bool &is_v) {
-  if (wide) {
-    is_v = p & 1;
-    return p >> 1;
-  }
-  if (p == 2 * n - 1) {
-    is_v = true;
-    return n - 1;
-  }
-  if (p < 2) {
-    is_v = false;
-    return p;
-  }
-  is_v = (p & 1) == 0;
-  return is_v ? (p - 2) / 2 : (p + 1) / 2;
-}
-
-// Waits on a barrier with the whole warp; false (and the abort flag) when the
-// limit ran out or another role gave up.  A softmax warp in attend_row holds
-// the others up for as long as it takes, so the limit starts over then.
-__device__ __forceinline__ bool wait_warp(Ctl *ctl, uint64_t *bar, uint32_t parity,
-                                          uint64_t limit_ns, int *status) {
-  const uint32_t at = smem_u32(bar);
+// Whether a waiting warp has to give up: its limit ran out, or another role
+// gave up.  A softmax warp in attend_row holds the others up for as long as it
+// takes, so the limit starts over then.
+__device__ __noinline__ bool give_up(Ctl *ctl, uint64_t &since, uint64_t limit_ns, int *status) {
   const volatile int *abort = &ctl->abort, *slow = &ctl->slow;
-  bool ok;
-  do {
-    ok = mbar_wait(at, parity, limit_ns, abort);
-  } while (!ok && !*abort && *slow > 0);
-  if (__all_sync(0xffffffffu, ok)) return true;
+  const uint64_t now = globaltimer();
+  if (since == 0 || *slow > 0) since = now;
+  const bool out = now - since >= limit_ns;
+  if (!__any_sync(0xffffffffu, out || *abort)) return false;
   if ((threadIdx.x & 31) == 0) {
     *reinterpret_cast<volatile int *>(&ctl->abort) = 1;
     set_status(status, SV_ERR_TIMEOUT);
   }
   __syncwarp();
-  return false;
+  return true;
+}
+// Waits on a barrier with the whole warp; false: given up.  Few instructions
+// where the barrier is ready, as the warp that issues the products pays for
+// each (about 5 cycles).
+__device__ __forceinline__ bool wait_warp(Ctl *ctl, uint64_t *bar, uint32_t parity,
+                                          uint64_t limit_ns, int *status) {
+  const uint32_t at = smem_u32(bar);
+  if (__all_sync(0xffffffffu, mbar_try_wait(at, parity))) return true;
+  uint64_t since = 0;
+  while (true) {
+    for (int i = 0; i < 16; ++i)
+      if (__all_sync(0xffffffffu, mbar_try_wait(at, parity))) return true;
+    if (give_up(ctl, since, limit_ns, status)) return false;
+  }
 }
 
 // 32 bits of a tree row from bit s on (s may be negative): the context before
@@ -313,7 +304,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   Ctl *ctl = reinterpret_cast<Ctl *>(smem + 2 * Sh::kQBytes + kRingBytes);
   const uint32_t ring = base + 2 * Sh::kQBytes;
   const sv_attention_t &a = args.a;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // uniform to the compiler
   Desc *desc = reinterpret_cast<Desc *>(args.scratch) + blockIdx.x;
   float *parts = args.scratch + kDescBytes / 4;
 
@@ -350,7 +342,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = ctl->tmem;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, ctl->tmem, 0);
   pdl_wait();
   pdl_launch_dependents();
 
@@ -431,7 +423,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int w = warp >> 2;
     const int row = tid & 127;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t tS = tmem + lanes + w * kKeys, tO = tmem + lanes + 256 + w * 128;
+    const uint32_t tS = tmem + lanes + w * 128, tO = tmem + lanes + 256 + w * 128;
     const bool out_fast = (reinterpret_cast<uintptr_t>(a.out) & 15u) == 0 &&
                           ((a.o_token | a.o_head) & 7) == 0;
     const int G = a.Hq / a.Hkv;
@@ -478,8 +470,86 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool live = __any_sync(0xffffffffu, valid);
       const int steps = wide ? n : (n + 1 - w) / 2;
       float m = -INFINITY, l = 0.0f;
+      // One tile of NK keys for this warp's rows.
+      auto tile = [&](auto nk, int k0, bool first) {
+        constexpr int NK = decltype(nk)::value;
+        uint32_t sr[NK];
+#pragma unroll
+        for (int g = 0; g < NK / 32; ++g) tmem_ld32(tS + 32 * g, sr + 32 * g);
+        tmem_ld_wait();
+#pragma unroll
+        for (int g = 0; g < NK / 32; ++g) tmem_reg_fence32(sr + 32 * g);
+        float *x = reinterpret_cast<float *>(sr);
+        const bool whole =
+            !valid || (lo <= k0 && hi >= k0 + NK && (!tree || k0 + NK <= it.s.ctx));
+        if (!__all_sync(0xffffffffu, whole)) {
+#pragma unroll
+          for (int g = 0; g < NK / 32; ++g) {
+            uint32_t keep = range_bits(lo - k0 - 32 * g, hi - k0 - 32 * g);
+            if (tree) keep &= tree_bits(tree, a.tree_words, k0 + 32 * g - it.s.ctx);
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (!(keep & (1u << i))) x[32 * g + i] = -INFINITY;
+          }
+        }
+        float top;
+        {
+          float t4[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) t4[i] = max3(x[i], x[i + 4], x[i + 8]);
+#pragma unroll
+          for (int g = 12; g + 8 <= NK; g += 8)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) t4[i] = max3(t4[i], x[g + i], x[g + 4 + i]);
+          constexpr int rest = 12 + (NK - 12) / 8 * 8;
+#pragma unroll
+          for (int i = rest; i < NK; ++i) t4[i & 3] = fmaxf(t4[i & 3], x[i]);
+          top = fmaxf(max3(t4[0], t4[1], t4[2]), t4[3]);
+        }
+        const bool grow = m == -INFINITY ? top > -INFINITY : (top - m) * args.c > kRescale;
+        if (__any_sync(0xffffffffu, grow)) {
+          const float to = grow ? top : m;
+          const float f = grow ? (m == -INFINITY ? 0.0f : ex2((m - to) * args.c)) : 1.0f;
+          m = to;
+          l *= f;
+          if (!first) {
+            // the products of the last step are complete: they precede the
+            // scores of this one
+#pragma unroll
+            for (int g = 0; g < DPAD / 16; ++g) {
+              uint32_t o[16];
+              tmem_ld16(tO + 16 * g, o);
+              tmem_ld_wait();
+              tmem_reg_fence(o);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+              tmem_st16(tO + 16 * g, o);
+            }
+          }
+        }
+        const float off = m == -INFINITY ? 0.0f : -m * args.c;
+        const float2 c2 = make_float2(args.c, args.c), off2 = make_float2(off, off);
+        float2 ls[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+#pragma unroll
+        for (int g = 0; g < NK / 64; ++g) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const int j = 64 * g + 2 * i;
+            const float2 y = fma2(make_float2(x[j], x[j + 1]), c2, off2);
+            const float2 p = make_float2(ex2(y.x), ex2(y.y));
+            ls[i & 1] = add2(ls[i & 1], p);
+            sr[32 * g + i] = pack2<T>(p.x, p.y);
+          }
+          tmem_st32(tS + 32 * g, sr + 32 * g);
+        }
+        ls[0] = add2(ls[0], ls[1]);
+        l += ls[0].x + ls[0].y;
+        tmem_st_wait();
+        tc_fence_before();
+      };
+      const int keys = wide ? kWideKeys : kNarrowKeys;
       for (int st = 0; st < steps; ++st) {
-        const int k0 = (it.tile0 + (wide ? st : 2 * st + w)) * kKeys;
+        const int k0 = (it.tile0 + (wide ? st : 2 * st + w)) * keys;
         if (!wait_warp(ctl, &ctl->s_full[w], cnt & 1, args.wait_limit_ns, args.status)) {
           ok = false;
           break;
@@ -487,75 +557,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++cnt;
         tc_fence_after();
         if (live) {
-          uint32_t sr[128];
-#pragma unroll
-          for (int g = 0; g < 4; ++g) tmem_ld32(tS + 32 * g, sr + 32 * g);
-          tmem_ld_wait();
-#pragma unroll
-          for (int g = 0; g < 4; ++g) tmem_reg_fence32(sr + 32 * g);
-          float *x = reinterpret_cast<float *>(sr);
-          const bool whole = !valid || (lo <= k0 && hi >= k0 + kKeys &&
-                                        (!tree || k0 + kKeys <= it.s.ctx));
-          if (!__all_sync(0xffffffffu, whole)) {
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-              uint32_t keep = range_bits(lo - k0 - 32 * g, hi - k0 - 32 * g);
-              if (tree) keep &= tree_bits(tree, a.tree_words, k0 + 32 * g - it.s.ctx);
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (!(keep & (1u << i))) x[32 * g + i] = -INFINITY;
-            }
-          }
-          float top = -INFINITY;
-          {
-            float t8[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) t8[i] = fmaxf(x[i], x[i + 8]);
-#pragma unroll
-            for (int g = 16; g < 128; g += 8)
-#pragma unroll
-              for (int i = 0; i < 8; ++i) t8[i] = fmaxf(t8[i], x[g + i]);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) top = fmaxf(top, t8[i]);
-          }
-          const bool grow = m == -INFINITY ? top > -INFINITY : (top - m) * args.c > kRescale;
-          if (__any_sync(0xffffffffu, grow)) {
-            const float to = grow ? top : m;
-            const float f = grow ? (m == -INFINITY ? 0.0f : ex2((m - to) * args.c)) : 1.0f;
-            m = to;
-            l *= f;
-            if (st > 0) {
-              // the products of the last step are complete: they precede the
-              // scores of this one
-#pragma unroll
-              for (int g = 0; g < DPAD / 16; ++g) {
-                uint32_t o[16];
-                tmem_ld16(tO + 16 * g, o);
-                tmem_ld_wait();
-                tmem_reg_fence(o);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                tmem_st16(tO + 16 * g, o);
-              }
-            }
-          }
-          const float off = m == -INFINITY ? 0.0f : -m * args.c;
-          float ls[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-          for (int g = 0; g < 2; ++g) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const int j = 64 * g + 2 * i;
-              const float p0 = ex2(fmaf(x[j], args.c, off));
-              const float p1 = ex2(fmaf(x[j + 1], args.c, off));
-              ls[i & 3] += p0 + p1;
-              sr[32 * g + i] = pack2<T>(p0, p1);
-            }
-            tmem_st32(tS + 32 * g, sr + 32 * g);
-          }
-          l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
-          tmem_st_wait();
-          tc_fence_before();
+          if (wide)
+            tile(std::integral_constant<int, kWideKeys>{}, k0, st == 0);
+          else
+            tile(std::integral_constant<int, kNarrowKeys>{}, k0, st == 0);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&ctl->p_ready[w]));
@@ -711,138 +716,190 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 8) {
       // ---------------- TMA ----------------
       const uint64_t policy = policy_evict_normal();
-      const int page_keys = min(kKeys, a.page_size);
+      const int page_keys = min(64, a.page_size);
       const uint32_t box_bytes = static_cast<uint32_t>(page_keys) * 128u;
-      int pos = 0;
+      int slot = 0, issued = 0;
+      uint32_t phase = 0;
       bool ok = true;
       while (ok && take()) {
         const Run &it = ctl->run[(runs - 1) % kRuns];
-        const int n = it.n;
+        const int n = it.n, tile0 = it.tile0, kv = it.s.kv, head = it.h;
         const bool wide = it.wide;
+        const int keys = wide ? kWideKeys : kNarrowKeys;
         const int32_t *pages = a.page_table + it.b * a.table_stride;
-        // lane i brings box i of a tile: page i / slabs, slab i % slabs (at most 32
-        // boxes, as a page holds 8 keys or more)
-        auto page_of = [&](int p) {
-          bool is_v;
-          const int k0 = (it.tile0 + tile_at(wide, p, n, is_v)) * kKeys;
-          const int key = k0 + lane / Sh::kSlabs * page_keys;
-          const bool in = lane / Sh::kSlabs < kKeys / page_keys && key < it.s.kv;
-          return in ? pages[key >> args.pow_page] : 0;
+        // lane i brings box i of a tile: box i / slabs of its keys, slab i %
+        // slabs (at most 32 boxes, as a page holds 8 keys or more)
+        const int slab = lane % Sh::kSlabs, key_in = lane / Sh::kSlabs * page_keys;
+        const uint32_t offset = static_cast<uint32_t>(slab * keys * 128 + key_in * 128);
+        auto page_of = [&](int t) {
+          const int key = (tile0 + t) * keys + key_in;
+          return t < n && key_in < keys && key < kv ? pages[key >> args.pow_page] : 0;
         };
         int page = page_of(0);
-        for (int p = 0; p < 2 * n; ++p, ++pos) {
-          const int slot = pos % Sh::kSlots;
-          bool is_v;
-          const int k0 = (it.tile0 + tile_at(wide, p, n, is_v)) * kKeys;
-          const int next = p + 1 < 2 * n ? page_of(p + 1) : 0;
-          const int boxes = max(0, (min(it.s.kv - k0, kKeys) + page_keys - 1) / page_keys);
-          if (!wait_warp(ctl, &ctl->empty[slot], ((pos / Sh::kSlots) & 1) ^ 1, args.wait_limit_ns,
-                         args.status)) {
-            ok = false;
-            break;
-          }
-          const uint32_t full = smem_u32(&ctl->full[slot]);
-          if (lane == 0) mbar_arrive_expect_tx(full, boxes * box_bytes * Sh::kSlabs);
-          __syncwarp();
-          if (lane < boxes * Sh::kSlabs) {
-            const int box = lane / Sh::kSlabs, slab = lane % Sh::kSlabs;
-            const int key = k0 + box * page_keys;
-            if (static_cast<uint32_t>(page) >= a.num_pages) set_status(args.status, SV_ERR_CACHE);
-            tma_load_4d(ring + slot * Sh::kTileBytes + slab * (kKeys * 128) + box * box_bytes,
-                        is_v ? &tmV : &tmK, slab * 64, it.h, key & (a.page_size - 1), page, full,
-                        policy);
+        for (int t = 0; t < n && ok; ++t) {
+          const int next = page_of(t + 1);
+          const int k0 = (tile0 + t) * keys;
+          const bool mine = key_in < keys && k0 + key_in < kv;
+          const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, mine)) * box_bytes;
+          if (mine && static_cast<uint32_t>(page) >= a.num_pages)
+            set_status(args.status, SV_ERR_CACHE);
+          const int in_page = (k0 + key_in) & (a.page_size - 1);
+          for (int v = 0; v < (wide ? 2 : 1); ++v) {
+            if (!(ok = wait_warp(ctl, &ctl->empty[slot], phase ^ 1, args.wait_limit_ns,
+                                 args.status)))
+              break;
+            const uint32_t full = smem_u32(&ctl->full[slot]);
+            if (lane == 0) mbar_arrive_expect_tx(full, wide ? bytes : 2 * bytes);
+            __syncwarp();
+            const uint32_t at = ring + slot * Sh::kSlotBytes + offset;
+            if (mine) {
+              tma_load_4d(at, v ? &tmV : &tmK, slab * 64, head, in_page, page, full, policy);
+              if (!wide)
+                tma_load_4d(at + Sh::kSlotBytes / 2, &tmV, slab * 64, head, in_page, page, full,
+                            policy);
+            }
+            __syncwarp();
+            ++issued;
+            if (++slot == Sh::kSlots) {
+              slot = 0;
+              phase ^= 1;
+            }
           }
           page = next;
-          __syncwarp();
-          if (lane == 0) ctl->issued = pos + 1;
         }
         give_back();
       }
+      if (lane == 0) ctl->issued = issued;
     } else if (warp == 9) {
       // ---------------- products ----------------
-      constexpr uint32_t idesc_s = idesc_16(kBf16, kRows, kKeys, false);
       constexpr uint32_t idesc_o = idesc_16(kBf16, kRows, DPAD, true);
-      int pos0 = 0, items = 0, cnt[2] = {0, 0};
+      int slot = 0, consumed = 0;
+      uint32_t phase = 0, q_phase = 0, p_phase = 0;
       bool ok = true;
+      // the next slot of the ring, once it is full; -1: given up
+      auto next_slot = [&]() {
+        if (!wait_warp(ctl, &ctl->full[slot], phase, args.wait_limit_ns, args.status)) return -1;
+        const int s = slot;
+        ++consumed;
+        if (++slot == Sh::kSlots) {
+          slot = 0;
+          phase ^= 1;
+        }
+        return s;
+      };
+      // Both of a slot's weights flip together with p_phase's bits.
+      auto wait_p = [&](int w) {
+        const bool r = wait_warp(ctl, &ctl->p_ready[w], (p_phase >> w) & 1, args.wait_limit_ns,
+                                 args.status);
+        p_phase ^= 1u << w;
+        tc_fence_after();
+        return r;
+      };
+      const uint64_t q0 = sw128_desc(base), k_base = sw128_desc(ring);
+      constexpr uint32_t kSlot16 = Sh::kSlotBytes >> 4, kQ16 = Sh::kQBytes >> 4;
+      // S of slot w: `keys` keys from ring slot s on; then commits s_full and,
+      // if `last`, frees the slot
+      auto scores = [&](int w, uint64_t q, int s, auto keys, bool last) {
+        constexpr uint32_t slab16 = keys * 128 >> 4;
+        constexpr uint32_t idesc = idesc_16(kBf16, kRows, keys, false);
+        const uint64_t k = k_base + static_cast<uint32_t>(s) * kSlot16;
+        if (elect_one()) {
+#pragma unroll
+          for (int e = 0; e < DPAD / 16; ++e)
+            umma_16(tmem + w * 128, q + (e / 4) * (kRows * 128 >> 4) + 2 * (e % 4),
+                    k + (e / 4) * slab16 + 2 * (e % 4), idesc, e > 0);
+          umma_commit(smem_u32(&ctl->s_full[w]));
+          if (last) umma_commit(smem_u32(&ctl->empty[s]));
+        }
+        __syncwarp();
+      };
+      // O of slot w += P V, V at `at` in the ring, 16 keys a product
+      auto outputs = [&](int w, uint32_t at, int s, auto keys, bool more, bool last) {
+        const uint64_t v = sw128_desc_mn(at, keys * 128);
+        if (elect_one()) {
+#pragma unroll
+          for (int e = 0; e < keys / 16; ++e)
+            umma_16_ta(tmem + 256 + w * 128, tmem + w * 128 + e * 8, v + e * (2048 >> 4), idesc_o,
+                       more || e > 0);
+          if (last) umma_commit(smem_u32(&ctl->empty[s]));
+        }
+        __syncwarp();
+      };
+      // Rows of V past the sequence hold anything: they get weight zero, which
+      // has to give zero.
+      auto zero_tail = [&](uint32_t at, int live, int keys) {
+        uint8_t *v = smem + (at - base);
+        const int first = max(live, 0), count = (keys - first) * 8;
+        for (int x = lane; x < count * Sh::kSlabs; x += 32) {
+          const int slab = x / count, y = x - slab * count;
+          *reinterpret_cast<uint4 *>(v + slab * (keys * 128) + first * 128 + y * 16) =
+              make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+      };
+      constexpr std::integral_constant<int, kWideKeys> wide_keys{};
+      constexpr std::integral_constant<int, kNarrowKeys> narrow_keys{};
       while (ok && take()) {
         const Run &it = ctl->run[(runs - 1) % kRuns];
-        const int n = it.n;
-        const bool wide = it.wide;
-        const int steps = wide ? 2 * n : n;
-        auto wait_tile = [&](int p) {
-          const int pos = pos0 + p;
-          const bool r = wait_warp(ctl, &ctl->full[pos % Sh::kSlots], (pos / Sh::kSlots) & 1,
-                                   args.wait_limit_ns, args.status);
-          if (r && lane == 0) ctl->consumed = max(ctl->consumed, pos + 1);
-          return r;
-        };
-        auto release = [&](int p) {
-          umma_commit(smem_u32(&ctl->empty[(pos0 + p) % Sh::kSlots]));
-        };
-        auto scores = [&](int i) {
-          const int w = i & 1, p = k_pos(wide, wide ? i >> 1 : i);
-          if ((!wide || w == 0) && !wait_tile(p)) return false;
-          tc_fence_after();
-          const uint64_t q = sw128_desc(base + (wide ? w : 0) * Sh::kQBytes);
-          const uint64_t k = sw128_desc(ring + (pos0 + p) % Sh::kSlots * Sh::kTileBytes);
-          if (elect_one()) {
-#pragma unroll
-            for (int e = 0; e < DPAD / 16; ++e) {
-              const uint32_t at = (e / 4) * (kKeys * 128 >> 4) + 2 * (e % 4);
-              umma_16(tmem + w * kKeys, q + at, k + at, idesc_s, e > 0);
+        const int n = __shfl_sync(0xffffffffu, it.n, 0);
+        const int live = __shfl_sync(0xffffffffu, it.s.kv, 0) -
+                         __shfl_sync(0xffffffffu, it.tile0, 0) * (it.wide ? kWideKeys
+                                                                          : kNarrowKeys);
+        if (!(ok = wait_warp(ctl, &ctl->q_ready, q_phase, args.wait_limit_ns, args.status))) break;
+        q_phase ^= 1;
+        int s = next_slot();
+        if (!(ok = s >= 0)) break;
+        tc_fence_after();
+        if (__shfl_sync(0xffffffffu, it.wide, 0)) {
+          scores(0, q0, s, wide_keys, false);
+          scores(1, q0 + kQ16, s, wide_keys, true);
+          for (int t = 0; t < n; ++t) {
+            const int v = next_slot();
+            if (!(ok = v >= 0)) break;
+            const uint32_t at = ring + v * Sh::kSlotBytes;
+            if (live < (t + 1) * kWideKeys) zero_tail(at, live - t * kWideKeys, kWideKeys);
+            if (!(ok = wait_p(0))) break;
+            outputs(0, at, v, wide_keys, t > 0, false);
+            if (t + 1 < n) {
+              s = next_slot();
+              if (!(ok = s >= 0)) break;
+              tc_fence_after();
+              scores(0, q0, s, wide_keys, false);
             }
-            umma_commit(smem_u32(&ctl->s_full[w]));
-            if (!wide || w == 1) release(p);
+            if (!(ok = wait_p(1))) break;
+            outputs(1, at, v, wide_keys, t > 0, true);
+            if (t + 1 < n) scores(1, q0 + kQ16, s, wide_keys, true);
           }
-          __syncwarp();
-          return true;
-        };
-        if (!wait_warp(ctl, &ctl->q_ready, items & 1, args.wait_limit_ns, args.status)) {
-          ok = false;
-          break;
-        }
-        ++items;
-        for (int i = 0; i < min(2, steps) && ok; ++i) ok = scores(i);
-        for (int i = 0; i < steps && ok; ++i) {
-          const int w = i & 1, t = wide ? i >> 1 : i, p = v_pos(wide, t, n);
-          if (!wide || w == 0) {
-            if (!(ok = wait_tile(p))) break;
-            // rows of V past the sequence hold anything: they get weight zero,
-            // which has to give zero
-            const int live = it.s.kv - (it.tile0 + t) * kKeys;
-            if (live < kKeys) {
-              uint8_t *v = smem + 2 * Sh::kQBytes + (pos0 + p) % Sh::kSlots * Sh::kTileBytes;
-              const int first = max(live, 0), count = (kKeys - first) * 8;
-              for (int x = lane; x < count * Sh::kSlabs; x += 32) {
-                const int slab = x / count, y = x - slab * count;
-                *reinterpret_cast<uint4 *>(v + slab * (kKeys * 128) + first * 128 + y * 16) =
-                    make_uint4(0, 0, 0, 0);
-              }
-              fence_proxy_async_smem();
-              __syncwarp();
+        } else {
+          scores(0, q0, s, narrow_keys, false);
+          int s1 = s;
+          if (n > 1) {
+            s1 = next_slot();
+            if (!(ok = s1 >= 0)) break;
+            tc_fence_after();
+            scores(1, q0, s1, narrow_keys, false);
+          }
+          for (int t = 0; t < n; ++t) {
+            const int w = t & 1, v = s;
+            const uint32_t at = ring + v * Sh::kSlotBytes + Sh::kSlotBytes / 2;
+            if (live < (t + 1) * kNarrowKeys) zero_tail(at, live - t * kNarrowKeys, kNarrowKeys);
+            if (!(ok = wait_p(w))) break;
+            outputs(w, at, v, narrow_keys, t > 1, true);
+            s = s1;
+            if (t + 2 < n) {
+              s1 = next_slot();
+              if (!(ok = s1 >= 0)) break;
+              tc_fence_after();
+              scores(w, q0, s1, narrow_keys, false);
             }
           }
-          if (!(ok = wait_warp(ctl, &ctl->p_ready[w], cnt[w] & 1, args.wait_limit_ns, args.status)))
-            break;
-          ++cnt[w];
-          tc_fence_after();
-          const uint64_t v =
-              sw128_desc_mn(ring + (pos0 + p) % Sh::kSlots * Sh::kTileBytes, kKeys * 128);
-          if (elect_one()) {
-#pragma unroll
-            for (int e = 0; e < kKeys / 16; ++e)
-              umma_16_ta(tmem + 256 + w * 128, tmem + w * kKeys + e * 8, v + e * (2048 >> 4),
-                         idesc_o, i > 1 || e > 0);
-            if (!wide || w == 1) release(p);
-          }
-          __syncwarp();
-          if (i + 2 < steps) ok = scores(i + 2);
         }
         if (!ok) break;
         if (elect_one()) umma_commit(smem_u32(&ctl->o_full));
         give_back();
-        pos0 += 2 * n;
       }
+      if (lane == 0) ctl->consumed = consumed;
       if (elect_one()) {
         umma_commit(smem_u32(&ctl->teardown));
         const int never = 0;
@@ -955,7 +1012,7 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-// Map of a cache [page, token, head, D]: box of 64 elements of up to 128
+// Map of a cache [page, token, head, D]: box of 64 elements of up to 64
 // tokens of one page and head.
 bool encode_cache(CUtensorMap *map, const sv_attention_t &a, const void *base, int64_t page,
                   int64_t token, int64_t head) {
@@ -965,8 +1022,7 @@ bool encode_cache(CUtensorMap *map, const sv_attention_t &a, const void *base, i
   const cuuint64_t strides[3] = {static_cast<cuuint64_t>(head) * 2,
                                  static_cast<cuuint64_t>(token) * 2,
                                  static_cast<cuuint64_t>(page) * 2};
-  const cuuint32_t box[4] = {64, 1, static_cast<cuuint32_t>(a.page_size < kKeys ? a.page_size
-                                                                                : kKeys),
+  const cuuint32_t box[4] = {64, 1, static_cast<cuuint32_t>(a.page_size < 64 ? a.page_size : 64),
                              1};
   const cuuint32_t estr[4] = {1, 1, 1, 1};
   return encode_fn()(map,

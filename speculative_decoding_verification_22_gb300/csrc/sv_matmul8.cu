@@ -87,18 +87,6 @@ __device__ __forceinline__ void store_remote(uint32_t smem_addr, uint32_t rank, 
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(x) : "memory");
 }
 
-// (a.x, a.y) = (x * s.x + a.x, y * s.y + a.y)
-__device__ __forceinline__ void fma2(float2 &a, float x, float y, float2 s) {
-  asm("{\n\t.reg .b64 ra, rx, rs;\n\t"
-      "mov.b64 ra, {%0, %1};\n\t"
-      "mov.b64 rx, {%2, %3};\n\t"
-      "mov.b64 rs, {%4, %5};\n\t"
-      "fma.rn.f32x2 ra, rx, rs, ra;\n\t"
-      "mov.b64 {%0, %1}, ra;\n\t}"
-      : "+f"(a.x), "+f"(a.y)
-      : "f"(x), "f"(y), "f"(s.x), "f"(s.y));
-}
-
 __device__ __forceinline__ void store_one(const MatmulParams &p, int64_t at, float x) {
   if (p.out_dtype == SV_BF16)
     static_cast<__nv_bfloat16 *>(p.out)[at] = __float2bfloat16_rn(x);
@@ -242,10 +230,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 sc = *reinterpret_cast<const float4 *>(
                     &ctl->scale[sslot][half * kHalf + g * kChunk + i]);
               const int j = (g * kChunk + i) / 2;
-              fma2(acc[j], __uint_as_float(x[i]), __uint_as_float(x[i + 1]),
-                   make_float2(sc.x, sc.y));
-              fma2(acc[j + 1], __uint_as_float(x[i + 2]), __uint_as_float(x[i + 3]),
-                   make_float2(sc.z, sc.w));
+              acc[j] = fma2(make_float2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])),
+                            make_float2(sc.x, sc.y), acc[j]);
+              acc[j + 1] = fma2(make_float2(__uint_as_float(x[i + 2]), __uint_as_float(x[i + 3])),
+                                make_float2(sc.z, sc.w), acc[j + 1]);
             }
           }
         }
