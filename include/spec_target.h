@@ -169,7 +169,7 @@ int spec_target_rope_freqs(const sv_rope_t *cfg, double *freqs, double *magnitud
  *   k_cache, v_cache  device, dtype [num_pages, page_size, Hkv, D] with page,
  *               token and head strides
  * T == 0 is a no-op.  Errors: SV_ERR_ARG, SV_ERR_SHAPE (D outside 1..256,
- * rot_dim odd or outside 0..D, sizes), SV_ERR_ALIGN, SV_ERR_CUDA. */
+ * rot_dim odd or outside 0..D, more than 4096 heads, sizes), SV_ERR_ALIGN, SV_ERR_CUDA. */
 typedef struct {
   const void *q, *k, *v;
   int64_t q_token, q_head, k_token, k_head, v_token, v_head;

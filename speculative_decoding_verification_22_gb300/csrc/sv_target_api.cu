@@ -206,7 +206,7 @@ int spec_target_rope_freqs(const sv_rope_t *cfg, double *freqs, double *magnitud
 
 int spec_target_rope_append(spec_target_t *h, const sv_rope_append_t *a, void *stream) {
   if (!h || !a || !float_type(a->dtype) || !std::isfinite(a->magnitude)) return SV_ERR_ARG;
-  if (a->T < 0 || a->Hq < 1 || a->Hkv < 1 || a->Hq > 65536 || a->Hkv > 65536 || a->D < 1 ||
+  if (a->T < 0 || a->Hq < 1 || a->Hkv < 1 || a->Hq > 4096 || a->Hkv > 4096 || a->D < 1 ||
       a->D > SV_MAX_HEAD_DIM || a->rot_dim < 0 || a->rot_dim > a->D || a->rot_dim % 2 != 0 ||
       a->page_size < 1 || a->num_pages < 1)
     return SV_ERR_SHAPE;
