@@ -89,21 +89,22 @@ struct Ctl {
   int slow;           // a softmax warp is in attend_row: waits go on
   int issued, consumed;
   int start_b;
-  int64_t start_off;
+  int64_t start_off, start_per;
   int64_t scan[kThreads / 32];
   float xm[kRows], xl[kRows];
 };
 
-// A cut item's parts: where they lie and which rows they hold.
+// A cut item's parts: which CTAs of its walk hold some, and whose rows.
+constexpr int kMaxWalks = 160;
 struct Desc {
-  int64_t ub, total;  // first unit of the item, units of the call
-  int parts;          // CTAs the item's tiles are spread over (0: none)
-  int cost, ntiles;   // units of a tile, tiles of the item
-  int b, h, r0, rows;
+  uint32_t held[kMaxWalks / 32];  // bit k: the walk's k-th CTA from here on
+  int parts;                      // CTAs it may be spread over (0: no cut item)
+  int b, h, r0, rows, t0;
 };
 
-// The parts of one CTA: [2][256 rows], (m, l) and then O.  Slot 0: the part
-// of an item that began in an earlier CTA; slot 1: of one that begins here.
+// The parts of one CTA: per part m, l and O as [2 + DPAD][256 rows], so that a
+// warp's rows lie side by side.  Part 0 is of an item that began in an earlier
+// CTA, part 1 of one that begins here.
 constexpr int kPartRows = 256;
 template <int DPAD>
 __host__ __device__ constexpr size_t part_floats() {
@@ -111,70 +112,147 @@ __host__ __device__ constexpr size_t part_floats() {
 }
 constexpr size_t kDescBytes = 64 * 1024;  // start of the scratch
 
-__device__ __forceinline__ int64_t cut_at(int64_t total, int c, int grid) {
-  return total * c / grid;
+struct TcArgs {
+  sv_attention_t a;
+  float *scratch;
+  int *status;
+  uint64_t wait_limit_ns;
+  uint64_t by_walks;  // 2^64 / walks
+  uint32_t by_group;  // 2^32 / G, rounded up (0: G is 1)
+  float c;       // |scale| log2 e, kept above zero
+  int negate;    // scale < 0: the queries are negated
+  int pow_page;  // log2 of the page size
+  int side;      // cache heads walked side by side
+  int walks;     // grid / side
+};
+
+// `side` CTAs, for as many neighbouring cache heads, walk the same items and
+// tiles at the same time, as the heads of a cached token lie side by side in
+// the usual layout (256 bytes each).  The walk's units are cut into equal runs
+// (any monotone rule will do, so this one takes no division), but of two units
+// at least: the two slots take two narrow tiles in the time of one, and each
+// run more is a part to be joined.
+__device__ __forceinline__ int64_t cut_at(const TcArgs &args, int64_t total, int c) {
+  if (total < 2 * args.walks) return 2 * c < total ? 2 * c : total;
+  return c >= args.walks ? total
+                         : static_cast<int64_t>(__umul64hi(total, args.by_walks * c));
 }
 
-// Walks the items of a call from a unit on.
+// r / G for a row.
+__device__ __forceinline__ int group_div(const TcArgs &args, int G, int r) {
+  if (!args.by_group) return r;
+  const int q = static_cast<int>(__umulhi(static_cast<uint32_t>(r), args.by_group));
+  return q * G > r ? q - 1 : q;  // the reciprocal is rounded up: at most one too many
+}
+
+// Walks the items of every side-th cache head (h counts those) from a unit on.
+// Divisions and long arithmetic are kept out: the first tile waits for this.
 struct Items {
+  const TcArgs &args;
   const sv_attention_t &a;
-  int G;
+  int G, heads;
   SeqGeom s;
   int b, h, m, nm;
-  int64_t ub;       // first unit of the current item
-  int cost, ntiles, tile_lo, r0, rows;
+  int64_t ub;  // first unit of the current item
+  int shift;   // 0: narrow, a tile is one unit; 1: wide, two
+  int ntiles, tile_lo, r0, rows;
 
-  __device__ explicit Items(const sv_attention_t &arg) : a(arg), G(arg.Hq / arg.Hkv) {}
+  __device__ explicit Items(const TcArgs &t)
+      : args(t), a(t.a), G(t.a.Hq / t.a.Hkv), heads(t.a.Hkv / t.side) {}
 
-  __device__ void item() {
-    const int total = s.n * G;
-    const int per = total > kRows ? 2 * kRows : kRows;
-    r0 = m * per;
-    rows = min(per, total - r0);
-    cost = rows > kRows ? 2 : 1;
-    int lo, hi, x;
-    key_range(a, s, r0 / G, lo, x);
-    key_range(a, s, (r0 + rows - 1) / G, x, hi);
-    const int keys = cost == 2 ? kWideKeys : kNarrowKeys;
-    tile_lo = lo / keys;
-    ntiles = max(1, (hi + keys - 1) / keys - tile_lo);
-  }
   __device__ void sequence() {
     const int total = s.n * G;
     nm = total > kRows ? (total + 2 * kRows - 1) / (2 * kRows) : 1;
   }
-  // Units of one cache head of the sequence.
-  __device__ int64_t head_units() {
+  __device__ void item() {
+    const int total = s.n * G;
+    r0 = m * (2 * kRows);
+    rows = nm == 1 ? total : min(2 * kRows, total - r0);
+    shift = rows > kRows ? 1 : 0;
+    int lo, hi, x;
+    key_range(a, s, nm == 1 ? 0 : group_div(args, G, r0), lo, x);
+    key_range(a, s, nm == 1 ? s.n - 1 : group_div(args, G, r0 + rows - 1), x, hi);
+    const int bits = shift ? 7 : 6;
+    static_assert(kWideKeys == 128 && kNarrowKeys == 64, "bits");
+    tile_lo = lo >> bits;
+    ntiles = max(1, ((hi + (1 << bits) - 1) >> bits) - tile_lo);
+  }
+  __device__ int64_t units() const { return static_cast<int64_t>(ntiles) << shift; }
+
+  // Units of one cache head of each lane's sequence (whole warp; n may be 0).
+  __device__ int64_t head_units(int lane) {
     int64_t u = 0;
-    if (s.n == 0) return 0;
     sequence();
-    for (m = 0; m < nm; ++m) {
+    if (s.n > 0 && nm == 1) {
+      m = 0;
       item();
-      u += static_cast<int64_t>(ntiles) * cost;
+      u = units();
     }
+    // sequences of several items: the warp takes one at a time, an item a lane
+    const SeqGeom mine = s;
+    unsigned many = __ballot_sync(0xffffffffu, s.n > 0 && nm > 1);
+    while (many) {
+      const int src = __ffs(many) - 1;
+      many &= many - 1;
+      s.t0 = __shfl_sync(0xffffffffu, mine.t0, src);
+      s.n = __shfl_sync(0xffffffffu, mine.n, src);
+      s.kv = __shfl_sync(0xffffffffu, mine.kv, src);
+      s.ctx = __shfl_sync(0xffffffffu, mine.ctx, src);
+      sequence();
+      int64_t sum = 0;
+      for (m = lane; m < nm; m += 32) {
+        item();
+        sum += units();
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      if (lane == src) u = sum;
+    }
+    s = mine;
     return u;
   }
-  __device__ void seek(int b0, int64_t off, int64_t u) {
-    bool bad;
-    b = b0;
-    s = seq_geom(a, b, &bad);
-    const int64_t per = head_units();
-    h = static_cast<int>(off / per);
-    off -= h * per;
-    for (m = 0;; ++m) {
-      item();
-      const int64_t n = static_cast<int64_t>(ntiles) * cost;
-      if (off < n) break;
-      off -= n;
+  // To the item of sequence b (s is set, `per` units a head) that holds its unit
+  // `off`, which is unit u of the walk.
+  __device__ void seek(int64_t per, int64_t off, int64_t u, int lane) {
+    sequence();
+    h = 0;
+    if (off >= 16 * per) {
+      h = static_cast<int>(off / per);
+      off -= h * per;
     }
+    for (; off >= per; ++h) off -= per;
+    m = 0;
+    for (int m0 = 0; nm > 1 && m0 < nm; m0 += 32) {
+      m = m0 + lane;
+      int64_t mine = 0;
+      if (m < nm) {
+        item();
+        mine = units();
+      }
+      int64_t incl = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+      }
+      const unsigned here = __ballot_sync(0xffffffffu, off < incl);
+      if (here) {
+        const int src = __ffs(here) - 1;
+        off -= __shfl_sync(0xffffffffu, incl - mine, src);
+        m = m0 + src;
+        break;
+      }
+      off -= __shfl_sync(0xffffffffu, incl, 31);
+    }
+    item();
     ub = u - off;
   }
   // The next item; its units follow the current ones.  False: none left.
   __device__ bool next() {
-    ub += static_cast<int64_t>(ntiles) * cost;
+    ub += units();
     if (++m == nm) {
       m = 0;
-      if (++h == a.Hkv) {
+      if (++h == heads) {
         h = 0;
         do {
           if (++b >= a.B) return false;
@@ -190,10 +268,10 @@ struct Items {
 };
 
 // The tiles of an item in the units [u0, u1).
-__device__ __forceinline__ void tile_run(int64_t ub, int cost, int ntiles, int64_t u0, int64_t u1,
+__device__ __forceinline__ void tile_run(int64_t ub, int shift, int ntiles, int64_t u0, int64_t u1,
                                          int &tb, int &te) {
-  const int64_t lo = u0 > ub ? (u0 - ub + cost - 1) / cost : 0;
-  const int64_t hi = u1 > ub ? (u1 - ub + cost - 1) / cost : 0;
+  const int64_t lo = u0 > ub ? (u0 - ub + shift) >> shift : 0;
+  const int64_t hi = u1 > ub ? (u1 - ub + shift) >> shift : 0;
   tb = static_cast<int>(lo < ntiles ? lo : ntiles);
   te = static_cast<int>(hi < ntiles ? hi : ntiles);
 }
@@ -258,23 +336,17 @@ __device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
   return *reinterpret_cast<const uint32_t *>(&v);
 }
 
-struct TcArgs {
-  sv_attention_t a;
-  float *scratch;
-  int *status;
-  uint64_t wait_limit_ns;
-  float c;       // |scale| log2 e, kept above zero
-  int negate;    // scale < 0: the queries are negated
-  int pow_page;  // log2 of the page size
-};
-
-// Stores 16 elements of a row of the output; `fast`: 16-byte aligned rows and D a multiple
-// of 8.
-template <class T, int DPAD>
+__device__ __forceinline__ bool fast_output(const sv_attention_t &a) {
+  return (reinterpret_cast<uintptr_t>(a.out) & 15u) == 0 && ((a.o_token | a.o_head) & 7) == 0;
+}
+// Stores N elements of a row of the output from d0 on; `fast`: 16-byte aligned
+// rows.  D is a multiple of 8.
+template <class T, int N = 32>
 __device__ __forceinline__ void store_row(const sv_attention_t &a, T *o, int d0, const float *x,
                                           bool fast) {
+  static_assert(N % 8 == 0, "16-byte stores");
 #pragma unroll
-  for (int v = 0; v < 16; v += 8) {
+  for (int v = 0; v < N; v += 8) {
     if (d0 + v >= a.D) break;
     if (fast) {
       uint4 q;
@@ -347,62 +419,57 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_launch_dependents();
 
   // ---- this CTA's run of units ----
-  Items it(a);
-  int64_t mine = 0;  // units of sequence tid (the only one where B is small)
-  int64_t sum = 0;
-  for (int b = tid; b < a.B; b += kThreads) {
-    bool bad;
-    it.s = seq_geom(a, b, &bad);
+  // With up to 32 sequences the warp that hands out the items finds it alone;
+  // with more the block does.
+  const int walk = blockIdx.x / args.side;
+  Items it(args);
+  // units of sequence b (one a lane), and of one head of it
+  auto sequence_units = [&](int b, int64_t &per) {
+    bool bad = false;
+    it.s = SeqGeom{0, 0, 0, 0};
+    if (b < a.B) it.s = seq_geom(a, b, &bad);
     if (bad && blockIdx.x == 0) set_status(args.status, SV_ERR_CACHE);
-    const int64_t u = it.head_units() * a.Hkv;
-    if (b == tid) mine = u;
-    sum += u;
-  }
-  auto warp_sum64 = [](int64_t x) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-    return x;
+    per = it.head_units(lane);
+    return per * it.heads;
   };
-  sum = warp_sum64(sum);
-  if (lane == 0) ctl->scan[warp] = sum;
-  __syncthreads();
-  int64_t total = 0;
-  for (int i = 0; i < kThreads / 32; ++i) total += ctl->scan[i];
-  const int64_t u0 = cut_at(total, blockIdx.x, gridDim.x);
-  const int64_t u1 = cut_at(total, blockIdx.x + 1, gridDim.x);
-  int64_t before = 0;
-  for (int b0 = 0; b0 < a.B; b0 += kThreads) {  // where u0 falls
-    const int b = b0 + tid;
-    int64_t u = mine;
-    if (b0 > 0) {
-      u = 0;
-      if (b < a.B) {
-        bool bad;
-        it.s = seq_geom(a, b, &bad);
-        u = it.head_units() * a.Hkv;
-      }
-    }
-    int64_t incl = u;
+  auto scan32 = [&](int64_t x) {
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += y;
+      const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    return x;
+  };
+  int64_t total = 0, u0 = 0, u1 = 0;
+  if (a.B > 32) {
+    int64_t before = 0, per;
+    for (int pass = 0; pass < 2; ++pass) {  // the total, then where u0 lies
+      for (int b0 = 0; b0 < a.B; b0 += kThreads) {
+        const int64_t u = sequence_units(b0 + tid, per);
+        const int64_t incl = scan32(u);
+        __syncthreads();  // the last sums have been read
+        if (lane == 31) ctl->scan[warp] = incl;
+        __syncthreads();
+        int64_t pre = before;
+        for (int i = 0; i < kThreads / 32; ++i) {
+          if (i < warp) pre += ctl->scan[i];
+          before += ctl->scan[i];
+        }
+        if (pass == 1 && u > 0 && u0 < u1 && u0 >= pre + incl - u && u0 < pre + incl) {
+          ctl->start_b = b0 + tid;
+          ctl->start_off = u0 - (pre + incl - u);
+          ctl->start_per = per;
+        }
+      }
+      if (pass == 0) {
+        total = before;
+        before = 0;
+        u0 = cut_at(args, total, walk);
+        u1 = cut_at(args, total, walk + 1);
+      }
     }
     __syncthreads();
-    if (lane == 31) ctl->scan[warp] = incl;
-    __syncthreads();
-    int64_t pre = before;
-    for (int i = 0; i < kThreads / 32; ++i) {
-      if (i < warp) pre += ctl->scan[i];
-      before += ctl->scan[i];
-    }
-    if (u > 0 && u0 < u1 && u0 >= pre + incl - u && u0 < pre + incl) {
-      ctl->start_b = b;
-      ctl->start_off = u0 - (pre + incl - u);
-    }
   }
-  __syncthreads();
-  const int b_first = ctl->start_b;
   // The next item for a role's warp; false: none left, or the call is given up.
   int runs = 0;
   auto take = [&]() {
@@ -424,8 +491,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int row = tid & 127;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + lanes + w * 128, tO = tmem + lanes + 256 + w * 128;
-    const bool out_fast = (reinterpret_cast<uintptr_t>(a.out) & 15u) == 0 &&
-                          ((a.o_token | a.o_head) & 7) == 0;
+    const bool out_fast = fast_output(a);
     const int G = a.Hq / a.Hkv;
     int items = 0, cnt = 0, narrow = 0;
     bool ok = true;
@@ -436,7 +502,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---- this thread's row ----
       const int r = wide ? w * kRows + row : row;
       const bool valid = r < it.rows;
-      const int tok = valid ? (it.r0 + r) / G : 0;
+      const int tok = valid ? group_div(args, G, it.r0 + r) : 0;
       const int head = it.h * G + (it.r0 + r) - tok * G;
       const int64_t t = it.s.t0 + tok;
       int lo = 0, hi = 0;
@@ -609,37 +675,34 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float inv = l != 0.0f ? 1.0f / l : 0.0f;
         T *o = static_cast<T *>(a.out) + t * a.o_token + head * a.o_head;
         bool fine = true;
-#pragma unroll
-        for (int g = 0; g < DPAD / 16; ++g) {
-          uint32_t y[16], z[16];
-          tmem_ld16(tO + 16 * g, y);
-          if (join) tmem_ld16(tO + 128 + 16 * g, z);
+        // (written out once: code that runs once an item is not unrolled further)
+#pragma unroll 1
+        for (int g = 0; g < DPAD / 32; ++g) {
+          uint32_t y[32], z[32];
+          tmem_ld32(tO + 32 * g, y);
+          if (join) tmem_ld32(tO + 128 + 32 * g, z);
           tmem_ld_wait();
-          tmem_reg_fence(y);
-          tmem_reg_fence(z);
-          float x[16];
+          tmem_reg_fence32(y);
+          tmem_reg_fence32(z);
+          float *x = reinterpret_cast<float *>(y);
+          if (join) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            // a slot that saw nothing has nothing to add
-            x[i] = __uint_as_float(y[i]);
-            if (join) {
+            for (int i = 0; i < 32; ++i) {
+              // a slot that saw nothing has nothing to add
               x[i] = f0 != 0.0f ? x[i] * f0 : 0.0f;
               if (f1 != 0.0f) x[i] = fmaf(__uint_as_float(z[i]), f1, x[i]);
             }
           }
           if (all) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
+            for (int i = 0; i < 32; ++i) {
               x[i] = l != 0.0f ? x[i] * inv : 0.0f;
               fine &= fabsf(x[i]) < INFINITY;
             }
-            if (valid) store_row<T, DPAD>(a, o, 16 * g, x, out_fast);
+            if (valid) store_row<T>(a, o, 32 * g, x, out_fast);
           } else if (valid) {
-            float4 *d = reinterpret_cast<float4 *>(part + 2 * kPartRows +
-                                                   static_cast<size_t>(r) * DPAD + 16 * g);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              d[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+            for (int i = 0; i < 32; ++i) part[(2 + 32 * g + i) * kPartRows + r] = x[i];
           }
         }
         if (valid) {
@@ -648,7 +711,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               a.lse[t * a.Hq + head] =
                   l != 0.0f ? m * (args.c * 0.69314718055994531f) + logf(l) : -INFINITY;
           } else {
-            reinterpret_cast<float2 *>(part)[r] = make_float2(m, l);
+            part[r] = m;
+            part[kPartRows + r] = l;
           }
         }
         unsigned again = __ballot_sync(0xffffffffu, all && valid && !fine);
@@ -672,34 +736,52 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 10) {
       // ---------------- items ----------------
       if (lane == 0) desc->parts = 0;
-      if (b_first >= 0) it.seek(b_first, ctl->start_off, u0);
-      bool more = b_first >= 0;
+      bool more = false;
+      if (a.B > 32) {
+        it.b = ctl->start_b;
+        more = it.b >= 0;
+        if (more) {
+          bool bad;
+          it.s = seq_geom(a, it.b, &bad);
+          it.seek(ctl->start_per, ctl->start_off, u0, lane);
+        }
+      } else {
+        int64_t per;
+        const int64_t u = sequence_units(lane, per), incl = scan32(u);
+        total = __shfl_sync(0xffffffffu, incl, 31);
+        u0 = cut_at(args, total, walk);
+        u1 = cut_at(args, total, walk + 1);
+        const unsigned here = __ballot_sync(0xffffffffu, u0 < u1 && u0 < incl);
+        more = here != 0;
+        if (more) {
+          const int src = __ffs(here) - 1;
+          it.b = src;
+          it.s.t0 = __shfl_sync(0xffffffffu, it.s.t0, src);
+          it.s.n = __shfl_sync(0xffffffffu, it.s.n, src);
+          it.s.kv = __shfl_sync(0xffffffffu, it.s.kv, src);
+          it.s.ctx = __shfl_sync(0xffffffffu, it.s.ctx, src);
+          it.seek(__shfl_sync(0xffffffffu, per, src),
+                  u0 - __shfl_sync(0xffffffffu, incl - u, src), u0, lane);
+        }
+      }
       while (true) {
         Run r{};
-        while (more && it.ub < u1) {
-          int tb, te;
-          tile_run(it.ub, it.cost, it.ntiles, u0, u1, tb, te);
+        int tb, te;
+        for (; more && it.ub < u1; more = it.next()) {
+          tile_run(it.ub, it.shift, it.ntiles, u0, u1, tb, te);
           if (te > tb) {
             r.n = te - tb;
             r.tile0 = it.tile_lo + tb;
-            r.wide = it.cost == 2;
+            r.wide = it.shift;
             r.whole = tb == 0 && te == it.ntiles;
             r.part = tb > 0 ? 0 : 1;
             r.b = it.b;
-            r.h = it.h;
+            r.h = it.h * args.side + blockIdx.x % args.side;
             r.r0 = it.r0;
             r.rows = it.rows;
             r.s = it.s;
-            if (!r.whole && r.part == 1 && lane == 0) {
-              // the CTA that holds the item's last unit
-              const int64_t ue = it.ub + static_cast<int64_t>(it.ntiles) * it.cost;
-              const int last = static_cast<int>((ue * gridDim.x + total - 1) / total) - 1;
-              *desc = Desc{it.ub, total, last - static_cast<int>(blockIdx.x) + 1, it.cost,
-                           it.ntiles, it.b, it.h, it.r0, it.rows};
-            }
+            break;
           }
-          more = it.next();
-          if (r.n > 0) break;
         }
         const int i = runs % kRuns;
         if (!wait_warp(ctl, &ctl->run_empty[i], ((runs / kRuns) & 1) ^ 1, args.wait_limit_ns,
@@ -712,6 +794,31 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         ++runs;
         if (r.n == 0) break;
+        // the others are at work: what the join needs, and the next item
+        if (!r.whole && r.part == 1) {
+          // the CTAs of the walk from here on that hold tiles of it
+          const int64_t ue = it.ub + it.units();
+          int n = 0;
+          for (int k0 = 0;; k0 += 32) {
+            const int c = walk + k0 + lane;
+            const int64_t c0 = cut_at(args, total, c);
+            int kb, ke;
+            tile_run(it.ub, it.shift, it.ntiles, c0, cut_at(args, total, c + 1), kb, ke);
+            const unsigned held = __ballot_sync(0xffffffffu, c < args.walks && kb < ke);
+            if (lane == 0) desc->held[k0 / 32] = held;
+            if (held) n = k0 + 32 - __clz(held);
+            if (!__all_sync(0xffffffffu, c < args.walks && c0 < ue)) break;
+          }
+          if (lane == 0) {
+            desc->b = r.b;
+            desc->h = r.h;
+            desc->r0 = r.r0;
+            desc->rows = r.rows;
+            desc->t0 = r.s.t0;
+            desc->parts = n;
+          }
+        }
+        more = it.next();
       }
     } else if (warp == 8) {
       // ---------------- TMA ----------------
@@ -849,21 +956,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!(ok = wait_warp(ctl, &ctl->q_ready, q_phase, args.wait_limit_ns, args.status))) break;
         q_phase ^= 1;
         int s = next_slot();
-        if (!(ok = s >= 0)) break;
+        ok = s >= 0;
+        if (!ok) break;
         tc_fence_after();
         if (__shfl_sync(0xffffffffu, it.wide, 0)) {
           scores(0, q0, s, wide_keys, false);
           scores(1, q0 + kQ16, s, wide_keys, true);
           for (int t = 0; t < n; ++t) {
             const int v = next_slot();
-            if (!(ok = v >= 0)) break;
+            ok = v >= 0;
+            if (!ok) break;
             const uint32_t at = ring + v * Sh::kSlotBytes;
             if (live < (t + 1) * kWideKeys) zero_tail(at, live - t * kWideKeys, kWideKeys);
             if (!(ok = wait_p(0))) break;
             outputs(0, at, v, wide_keys, t > 0, false);
             if (t + 1 < n) {
               s = next_slot();
-              if (!(ok = s >= 0)) break;
+              ok = s >= 0;
+              if (!ok) break;
               tc_fence_after();
               scores(0, q0, s, wide_keys, false);
             }
@@ -876,7 +986,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           int s1 = s;
           if (n > 1) {
             s1 = next_slot();
-            if (!(ok = s1 >= 0)) break;
+            ok = s1 >= 0;
+            if (!ok) break;
             tc_fence_after();
             scores(1, q0, s1, narrow_keys, false);
           }
@@ -889,7 +1000,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             s = s1;
             if (t + 2 < n) {
               s1 = next_slot();
-              if (!(ok = s1 >= 0)) break;
+              ok = s1 >= 0;
+            if (!ok) break;
               tc_fence_after();
               scores(w, q0, s1, narrow_keys, false);
             }
@@ -926,73 +1038,102 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Joins the parts of the items that were cut: block (c, y) takes rows of the
-// item that begins in CTA c, a warp a row, the parts in order.
-constexpr int kJoinWarps = 8, kJoinBlocks = 4;
+// Joins the parts of the items that were cut, in their order.  A warp takes 32
+// rows, one a lane, and eight elements of the head; block (c, y) works on the
+// item that begins in CTA c.
+constexpr int kJoinWarps = 8, kJoinBlocks = 2, kJoinElems = 8, kJoinParts = 4;
 template <class T, int DPAD>
 __global__ void __launch_bounds__(32 * kJoinWarps)
-    attention_join_kernel(const __grid_constant__ TcArgs args, int grid) {
+    attention_join_kernel(const __grid_constant__ TcArgs args) {
   const sv_attention_t &a = args.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_wait();
   pdl_launch_dependents();
-  const Desc d = reinterpret_cast<const Desc *>(args.scratch)[blockIdx.x];
-  if (d.parts == 0) return;
-  const float *parts = args.scratch + kDescBytes / 4;
-  const int G = a.Hq / a.Hkv;
-  bool bad;
-  const SeqGeom s = seq_geom(a, d.b, &bad);
-  constexpr int kPer = DPAD / 32;
-  for (int r = blockIdx.y * kJoinWarps + warp; r < d.rows; r += kJoinBlocks * kJoinWarps) {
-    // (m, l) of 32 parts at a time, one a lane
-    float top = -INFINITY, sum = 0.0f, acc[kPer] = {};
-    for (int k0 = 0; k0 < d.parts; k0 += 32) {
-      const int k = k0 + lane, c = blockIdx.x + k;
-      const float *part = nullptr;
-      float2 ml = make_float2(-INFINITY, 0.0f);
-      if (k < d.parts) {
-        int tb, te;
-        tile_run(d.ub, d.cost, d.ntiles, cut_at(d.total, c, grid), cut_at(d.total, c + 1, grid),
-                 tb, te);
-        if (tb < te) {
-          part = parts + (static_cast<size_t>(c) * 2 + (k > 0 ? 0 : 1)) * part_floats<DPAD>();
-          ml = __ldcg(reinterpret_cast<const float2 *>(part) + r);
-        }
+  const Desc &d = reinterpret_cast<const Desc *>(args.scratch)[blockIdx.x];
+  const int count = d.parts;
+  if (count == 0) return;
+  const int rows = d.rows, G = a.Hq / a.Hkv;
+  const size_t pitch = 2 * part_floats<DPAD>() * args.side;  // from CTA to CTA of the walk
+  const float *parts = args.scratch + kDescBytes / 4 +
+                       blockIdx.x * (2 * part_floats<DPAD>());
+  auto part_of = [&](int k) { return parts + k * pitch + (k > 0 ? 0 : part_floats<DPAD>()); };
+  uint32_t held[kMaxWalks / 32];
+#pragma unroll
+  for (int i = 0; i < kMaxWalks / 32; ++i) held[i] = 32 * i < count ? d.held[i] : 0u;
+  const int b = d.b, h = d.h, r0 = d.r0, t0 = d.t0;
+  constexpr int kGroups = DPAD / kJoinElems;
+  const int tasks = (rows + 31) / 32 * kGroups;
+  for (int i = blockIdx.y * kJoinWarps + warp; i < tasks; i += kJoinBlocks * kJoinWarps) {
+    const int r = i / kGroups * 32 + lane, d0 = i % kGroups * kJoinElems;
+    if (d0 >= a.D) continue;
+    const bool valid = r < rows;
+    const int row = valid ? r : 0;
+    float top = -INFINITY, sum = 0.0f, acc[kJoinElems] = {};
+    for (int k0 = 0; k0 < count; k0 += kJoinParts) {
+      // all of the round's loads first: the parts were written by other SMs
+      float m[kJoinParts], l[kJoinParts], x[kJoinParts][kJoinElems];
+      uint32_t word = held[0];
+#pragma unroll
+      for (int i = 1; i < kMaxWalks / 32; ++i)
+        if (k0 >= 32 * i) word = held[i];
+      word >>= k0 & 31;
+#pragma unroll
+      for (int j = 0; j < kJoinParts; ++j) {
+        const float *p = part_of(min(k0 + j, count - 1)) + row;
+        m[j] = __ldcg(p);
+        l[j] = __ldcg(p + kPartRows);
+#pragma unroll
+        for (int e = 0; e < kJoinElems; ++e) x[j][e] = __ldcg(p + (2 + d0 + e) * kPartRows);
       }
-      const float to = fmaxf(top, warp_max(ml.x));
+      float to = top;
+#pragma unroll
+      for (int j = 0; j < kJoinParts; ++j) {
+        if (!((word >> j) & 1u)) m[j] = -INFINITY;  // none there
+        to = fmaxf(to, m[j]);
+      }
       const float keep = top == -INFINITY ? 0.0f : ex2((top - to) * args.c);
-      const float f = ml.x == -INFINITY ? 0.0f : ex2((ml.x - to) * args.c);
-      sum = sum * keep + warp_sum(ml.y * f);
+      sum *= keep;
+#pragma unroll
+      for (int e = 0; e < kJoinElems; ++e) acc[e] = keep != 0.0f ? acc[e] * keep : 0.0f;
       top = to;
 #pragma unroll
-      for (int e = 0; e < kPer; ++e) acc[e] = keep != 0.0f ? acc[e] * keep : 0.0f;
-      const int many = min(32, d.parts - k0);
-#pragma unroll 4
-      for (int j = 0; j < many; ++j) {
-        const float fj = __shfl_sync(0xffffffffu, f, j);
-        const float *pj = reinterpret_cast<const float *>(
-            __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(part), j));
-        if (fj == 0.0f) continue;  // nothing there, or nothing seen
-        const float *o = pj + 2 * kPartRows + static_cast<size_t>(r) * DPAD;
+      for (int j = 0; j < kJoinParts; ++j) {
+        // a part that saw nothing adds nothing
+        const float f = m[j] == -INFINITY ? 0.0f : ex2((m[j] - top) * args.c);
+        sum = f != 0.0f ? fmaf(l[j], f, sum) : sum;
 #pragma unroll
-        for (int e = 0; e < kPer; ++e) acc[e] = fmaf(__ldcg(o + lane + 32 * e), fj, acc[e]);
+        for (int e = 0; e < kJoinElems; ++e)
+          acc[e] = f != 0.0f ? fmaf(x[j][e], f, acc[e]) : acc[e];
       }
     }
-    const int tok = (d.r0 + r) / G, head = d.h * G + (d.r0 + r) - tok * G;
-    const int64_t t = s.t0 + tok;
-    const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;
-    T *o = static_cast<T *>(a.out) + t * a.o_token + head * a.o_head;
+    const int tok = valid ? group_div(args, G, r0 + r) : 0;
+    const int head = h * G + r0 + r - tok * G;
+    const int64_t t = t0 + tok;
     bool fine = true;
+    if (valid) {
+      const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;
 #pragma unroll
-    for (int e = 0; e < kPer; ++e) {
-      const float x = sum != 0.0f ? acc[e] * inv : 0.0f;
-      fine &= fabsf(x) < INFINITY;
-      if (lane + 32 * e < a.D) o[lane + 32 * e] = from_float<T>(x);
+      for (int e = 0; e < kJoinElems; ++e) {
+        acc[e] = sum != 0.0f ? acc[e] * inv : 0.0f;
+        fine &= fabsf(acc[e]) < INFINITY;
+      }
+      store_row<T, kJoinElems>(a, static_cast<T *>(a.out) + t * a.o_token + head * a.o_head, d0,
+                               acc, fast_output(a));
+      if (a.lse && d0 == 0)
+        a.lse[t * a.Hq + head] =
+            sum != 0.0f ? top * (args.c * 0.69314718055994531f) + logf(sum) : -INFINITY;
     }
-    if (a.lse && lane == 0)
-      a.lse[t * a.Hq + head] =
-          sum != 0.0f ? top * (args.c * 0.69314718055994531f) + logf(sum) : -INFINITY;
-    if (__any_sync(0xffffffffu, !fine)) attend_row<T>(a, s, d.b, tok, head, lane, args.status);
+    unsigned again = __ballot_sync(0xffffffffu, !fine);
+    if (again) {
+      bool bad;
+      const SeqGeom s = seq_geom(a, b, &bad);
+      while (again) {
+        const int src = __ffs(again) - 1;
+        again &= again - 1;
+        attend_row<T>(a, s, b, __shfl_sync(0xffffffffu, tok, src),
+                      __shfl_sync(0xffffffffu, head, src), lane, args.status);
+      }
+    }
   }
 }
 
@@ -1039,19 +1180,18 @@ int launch_typed(const spec_target &h, const TcArgs &args, const CUtensorMap &tm
                  const CUtensorMap &tmV, cudaStream_t stream) {
   constexpr int smem = Shape<DPAD>::kSmem + static_cast<int>(sizeof(Ctl));
   static_assert(smem <= 232448, "shared memory of one SM");
-  // per device; a cheap call, so it is not remembered
   if (cudaFuncSetAttribute(attention_tc_kernel<T, DPAD>,
                            cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return SV_ERR_CUDA;
   const int grid = h.num_sms;
   if (kDescBytes + sizeof(float) * part_floats<DPAD>() * 2 * grid > h.scratch_bytes ||
-      sizeof(Desc) * grid > kDescBytes)
+      sizeof(Desc) * grid > kDescBytes || args.walks > kMaxWalks)
     return SV_ERR_CUDA;
   if (launch_chained(attention_tc_kernel<T, DPAD>, dim3(grid), dim3(kThreads), smem, stream, tmK,
                      tmV, args) != cudaSuccess)
     return SV_ERR_CUDA;
   return launch_chained(attention_join_kernel<T, DPAD>, dim3(grid, kJoinBlocks),
-                        dim3(32 * kJoinWarps), 0, stream, args, grid) == cudaSuccess
+                        dim3(32 * kJoinWarps), 0, stream, args) == cudaSuccess
              ? SV_OK
              : SV_ERR_CUDA;
 }
@@ -1086,6 +1226,13 @@ int launch_attention_tc(const spec_target &h, const sv_attention_t &a, cudaStrea
   args.c = c > 1e-37f ? c : 1e-37f;
   args.negate = a.scale < 0.0f;
   while ((1 << args.pow_page) < a.page_size) ++args.pow_page;
+  args.side = 1;
+  while (args.side < 8 && a.Hkv % (2 * args.side) == 0 && h.num_sms % (2 * args.side) == 0)
+    args.side *= 2;
+  args.walks = h.num_sms / args.side;
+  args.by_walks = args.walks > 1 ? ~uint64_t(0) / args.walks : 0;
+  const uint64_t G = a.Hq / a.Hkv;
+  args.by_group = G > 1 ? static_cast<uint32_t>(((uint64_t(1) << 32) + G - 1) / G) : 0;
   if (a.dtype == SV_BF16)
     return a.D <= 64 ? launch_typed<__nv_bfloat16, 64>(h, args, tmK, tmV, stream)
                      : launch_typed<__nv_bfloat16, 128>(h, args, tmK, tmV, stream);
