@@ -594,22 +594,22 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         const float off = m == -INFINITY ? 0.0f : -m * args.c;
-        const float2 c2 = make_float2(args.c, args.c), off2 = make_float2(off, off);
-        float2 ls[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+        const uint64_t c2 = pair2(args.c, args.c), off2 = pair2(off, off);
+        uint64_t ls[2] = {0, 0};
 #pragma unroll
         for (int g = 0; g < NK / 64; ++g) {
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
             const int j = 64 * g + 2 * i;
-            const float2 y = fma2(make_float2(x[j], x[j + 1]), c2, off2);
-            const float2 p = make_float2(ex2(y.x), ex2(y.y));
-            ls[i & 1] = add2(ls[i & 1], p);
-            sr[32 * g + i] = pack2<T>(p.x, p.y);
+            const float2 y = unpair2(fma2(pair2(x[j], x[j + 1]), c2, off2));
+            const float p0 = ex2(y.x), p1 = ex2(y.y);
+            ls[i & 1] = add2(ls[i & 1], pair2(p0, p1));
+            sr[32 * g + i] = pack2<T>(p0, p1);
           }
           tmem_st32(tS + 32 * g, sr + 32 * g);
         }
-        ls[0] = add2(ls[0], ls[1]);
-        l += ls[0].x + ls[0].y;
+        const float2 sum2 = unpair2(add2(ls[0], ls[1]));
+        l += sum2.x + sum2.y;
         tmem_st_wait();
         tc_fence_before();
       };

@@ -16,8 +16,8 @@
 //  * Fewer tiles than SMs: a cluster of up to eight CTAs shares a tile, each
 //    takes a part of K, and the parts are added through distributed shared
 //    memory in the order of K (repeatable, no scratch, no second launch).
-//  * Warps 0-7: scale and add (two warpgroups, half of the columns each);
-//    warp 8: TMA; warp 9: products; warps 10, 11: the columns' scales.
+//  * Warps 0-15: scale and add (four warpgroups, a quarter of the columns
+//    each); warp 16: TMA; warp 17: products; warps 18, 19: the columns' scales.
 #include <cudaTypedefs.h>
 
 #include "sv_target.cuh"
@@ -26,9 +26,15 @@
 namespace sv {
 namespace {
 
-constexpr int kThreads = 384;
-constexpr int kAddWarps = 8;
-constexpr int kAddRegs = 216, kOtherRegs = 72;  // see the attention's kernel
+#ifndef ADDW
+#define ADDW 8
+#endif
+constexpr int kAddWarps = ADDW;
+constexpr int kThreads = 32 * kAddWarps + 128;
+// Registers a thread: 168 at launch; the adding warps take what the others give
+// back (256 * 216 + 128 * 72 = 384 * 168).
+constexpr int kAddRegs = ADDW == 8 ? 216 : 104, kOtherRegs = ADDW == 8 ? 72 : 64;
+constexpr int kLoadWarp = kAddWarps, kMmaWarp = kAddWarps + 1, kScaleWarp = kAddWarps + 2;
 constexpr int kLanes = 128;      // rows of a tile
 constexpr int kBlk = 128;        // K elements (bytes) of a block
 constexpr int kRingBytes = 192 * 1024;
@@ -46,6 +52,7 @@ struct Args {
   int split;              // CTAs of a tile
   int stages, stage_bytes;
   int fast;               // 16-byte stores of the output's rows
+  int fast_scales;        // 16-byte loads of four scales of a row
 };
 
 struct Ctl {
@@ -58,16 +65,30 @@ struct Ctl {
   int abort, issued, consumed;
 };
 
-__device__ __forceinline__ bool wait_warp(Ctl *ctl, uint64_t *bar, uint32_t parity,
-                                          const Args &a) {
-  const bool ok = mbar_wait(smem_u32(bar), parity, a.wait_limit_ns, &ctl->abort);
-  if (__all_sync(0xffffffffu, ok)) return true;
+__device__ __noinline__ bool give_up(Ctl *ctl, uint64_t &since, const Args &a) {
+  const volatile int *abort = &ctl->abort;
+  const uint64_t now = globaltimer();
+  if (since == 0) since = now;
+  if (!__any_sync(0xffffffffu, now - since >= a.wait_limit_ns || *abort)) return false;
   if ((threadIdx.x & 31) == 0) {
     *reinterpret_cast<volatile int *>(&ctl->abort) = 1;
     set_status(a.status, SV_ERR_TIMEOUT);
   }
   __syncwarp();
-  return false;
+  return true;
+}
+// Waits on a barrier with the whole warp; false: the limit ran out, or another
+// role gave up.
+__device__ __forceinline__ bool wait_warp(Ctl *ctl, uint64_t *bar, uint32_t parity,
+                                          const Args &a) {
+  const uint32_t at = smem_u32(bar);
+  if (__all_sync(0xffffffffu, mbar_try_wait(at, parity))) return true;
+  uint64_t since = 0;
+  while (true) {
+    for (int i = 0; i < 16; ++i)
+      if (__all_sync(0xffffffffu, mbar_try_wait(at, parity))) return true;
+    if (give_up(ctl, since, a)) return false;
+  }
 }
 
 // All threads of the cluster.
@@ -81,10 +102,30 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
-__device__ __forceinline__ void store_remote(uint32_t smem_addr, uint32_t rank, float x) {
+// The address of another CTA's shared memory in the cluster, and a store there.
+__device__ __forceinline__ uint32_t remote_smem(uint32_t smem_addr, uint32_t rank) {
   uint32_t at;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_addr), "r"(rank));
+  return at;
+}
+__device__ __forceinline__ void store_remote(uint32_t at, float x) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(x) : "memory");
+}
+
+template <int kChunk>
+__device__ __forceinline__ void read_columns(uint32_t at, uint32_t *x) {
+  if constexpr (kChunk == 32)
+    tmem_ld32(at, x);
+  else
+    tmem_ld16(at, *reinterpret_cast<uint32_t(*)[16]>(x));
+}
+template <int kChunk>
+__device__ __forceinline__ void columns_arrived(uint32_t *x) {
+  tmem_ld_wait();
+  if constexpr (kChunk == 32)
+    tmem_reg_fence32(x);
+  else
+    tmem_reg_fence(*reinterpret_cast<uint32_t(*)[16]>(x));
 }
 
 __device__ __forceinline__ void store_one(const MatmulParams &p, int64_t at, float x) {
@@ -131,7 +172,8 @@ template <int kCols, bool kSwap>
 __global__ void __launch_bounds__(kThreads, 1)
     matmul8_kernel(const __grid_constant__ CUtensorMap tmLane,
                    const __grid_constant__ CUtensorMap tmCol, const __grid_constant__ Args args) {
-  constexpr int kHalf = kCols / 2;                       // columns of a thread
+  constexpr int kParts = kAddWarps / 4;
+  constexpr int kMine = kCols / kParts < 16 ? 16 : kCols / kParts;  // columns of a thread
   constexpr int kSlots = 512 / kCols < 8 ? 512 / kCols : 8;  // blocks in tensor memory
   const MatmulParams &p = args.p;
   extern __shared__ uint8_t smem_raw[];
@@ -139,7 +181,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t *smem = smem_raw + (base - raw);
   Ctl *ctl = reinterpret_cast<Ctl *>(smem + kRingBytes);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // uniform to the compiler
 
   if (tid == 0) {
     for (int i = 0; i < args.stages; ++i) {
@@ -158,18 +201,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     ctl->abort = ctl->issued = ctl->consumed = 0;
     mbar_fence_init();
   }
-  if (warp == 8 && lane == 0) {
+  if (warp == kLoadWarp && lane == 0) {
     tma_prefetch_desc(&tmLane);
     tma_prefetch_desc(&tmCol);
   }
-  if (warp == 9) {
+  if (warp == kMmaWarp) {
     tmem_alloc(smem_u32(&ctl->tmem), 512);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = ctl->tmem;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, ctl->tmem, 0);
   pdl_wait();
   pdl_launch_dependents();
 
@@ -180,68 +223,98 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp < kAddWarps) {
     // ---------------- scale, add, store ----------------
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kAddRegs));
-    const int half = warp >> 2, row = tid & 127;
+    const int own = (warp >> 2) * kMine, row = tid & 127;  // first column, lane
     const uint32_t tacc =
-        tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + half * kHalf;
+        tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + own;
     int slot = 0, sslot = 0;
     uint32_t tphase = 0, sphase = 0;
     bool ok = true;
     for (int tile = first; tile < args.tiles && ok; tile += step) {
       const int l0 = tile % args.lane_tiles * kLanes;
-      const int c0 = tile / args.lane_tiles * args.bn + half * kHalf;
-      float2 acc[kHalf / 2];
+      const int c0 = tile / args.lane_tiles * args.bn + own;
+      uint64_t acc[kMine / 2];  // two columns each
 #pragma unroll
-      for (int i = 0; i < kHalf / 2; ++i) acc[i] = make_float2(0.0f, 0.0f);
-      const bool work = !kSwap || half * kHalf < args.bn;
+      for (int i = 0; i < kMine / 2; ++i) acc[i] = 0;
+      const bool work = own < args.bn;
       // lanes = A's rows: one scale a row and one a 128-column block of W
       const bool in = l0 + row < p.M;
       const float *as = p.as + static_cast<int64_t>(in ? l0 + row : 0) * p.kb;
       const float *ws = p.ws + static_cast<int64_t>(c0 < p.N ? c0 / kBlk : 0) * p.kb;
-      float s_next = 0.0f;
-      if constexpr (!kSwap) s_next = kb0 < kb1 ? __ldg(as + kb0) * __ldg(ws + kb0) : 0.0f;
+      // scales of four blocks at a time, the next four on their way (one 16-byte
+      // load for a row's four: 32 rows are 32 lines, whatever is read of them)
+      float sc[4] = {}, as_next[4] = {}, ws_next[4] = {};
+      auto fetch = [&](int kb) {
+        if (args.fast_scales) {
+          const float4 v = __ldg(reinterpret_cast<const float4 *>(as + kb));
+          const float4 w = __ldg(reinterpret_cast<const float4 *>(ws + kb));
+          as_next[0] = v.x, as_next[1] = v.y, as_next[2] = v.z, as_next[3] = v.w;
+          ws_next[0] = w.x, ws_next[1] = w.y, ws_next[2] = w.z, ws_next[3] = w.w;
+        } else {
+#pragma unroll
+          for (int t = 0; t < 4; ++t)
+            if (kb + t < kb1) {
+              as_next[t] = __ldg(as + kb + t);
+              ws_next[t] = __ldg(ws + kb + t);
+            }
+        }
+      };
+      if (!kSwap && kb0 < kb1) fetch(kb0);
       for (int kb = kb0; kb < kb1; ++kb) {
         float s = 0.0f;
         if constexpr (!kSwap) {
-          s = s_next;
-          if (kb + 1 < kb1) s_next = __ldg(as + kb + 1) * __ldg(ws + kb + 1);
+          const int t = (kb - kb0) & 3;
+          if (t == 0) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sc[i] = as_next[i] * ws_next[i];
+            if (kb + 4 < kb1) fetch(kb + 4);
+          }
+          s = t < 2 ? (t == 0 ? sc[0] : sc[1]) : (t == 2 ? sc[2] : sc[3]);
         } else {
           if (!(ok = wait_warp(ctl, &ctl->sfull[sslot], sphase, args))) break;
         }
         if (!(ok = wait_warp(ctl, &ctl->tfull[slot], tphase, args))) break;
         tc_fence_after();
+        // the slot is free once its last columns have been read
+        auto free_slot = [&]() {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&ctl->tempty[slot]));
+        };
+        const uint64_t s2 = pair2(s, s);
         if (work) {
-          constexpr int kChunk = kHalf < 32 ? 16 : 32;
+          // the next columns are read while these are scaled and added
+          constexpr int kChunk = kMine == 64 || kMine == 32 ? 32 : 16, kChunks = kMine / kChunk;
+          uint32_t x[kChunks > 1 ? 2 : 1][kChunk];
+          read_columns<kChunk>(tacc + slot * kCols, x[0]);
 #pragma unroll
-          for (int g = 0; g < kHalf / kChunk; ++g) {
-            uint32_t x[kChunk];
-            if constexpr (kChunk == 32) {
-              tmem_ld32(tacc + slot * kCols + g * kChunk, x);
-              tmem_ld_wait();
-              tmem_reg_fence32(x);
-            } else {
-              tmem_ld16(tacc + slot * kCols + g * kChunk, x);
-              tmem_ld_wait();
-              tmem_reg_fence(x);
-            }
+          for (int g = 0; g < kChunks; ++g) {
+            uint32_t *y = x[g & 1];
+            columns_arrived<kChunk>(y);
+            if (g + 1 < kChunks)
+              read_columns<kChunk>(tacc + slot * kCols + (g + 1) * kChunk, x[(g + 1) & 1]);
+            else
+              free_slot();
 #pragma unroll
             for (int i = 0; i < kChunk; i += 4) {
-              float4 sc = make_float4(s, s, s, s);
-              if constexpr (kSwap)
-                sc = *reinterpret_cast<const float4 *>(
-                    &ctl->scale[sslot][half * kHalf + g * kChunk + i]);
+              uint64_t s01 = s2, s23 = s2;
+              if constexpr (kSwap) {
+                const ulonglong2 sc = *reinterpret_cast<const ulonglong2 *>(
+                    &ctl->scale[sslot][own + g * kChunk + i]);
+                s01 = sc.x;
+                s23 = sc.y;
+              }
               const int j = (g * kChunk + i) / 2;
-              acc[j] = fma2(make_float2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])),
-                            make_float2(sc.x, sc.y), acc[j]);
-              acc[j + 1] = fma2(make_float2(__uint_as_float(x[i + 2]), __uint_as_float(x[i + 3])),
-                                make_float2(sc.z, sc.w), acc[j + 1]);
+              acc[j] = fma2(pair2(__uint_as_float(y[i]), __uint_as_float(y[i + 1])), s01, acc[j]);
+              acc[j + 1] = fma2(pair2(__uint_as_float(y[i + 2]), __uint_as_float(y[i + 3])), s23,
+                                acc[j + 1]);
             }
           }
+        } else {
+          free_slot();
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(smem_u32(&ctl->tempty[slot]));
-          if (kSwap) mbar_arrive(smem_u32(&ctl->sempty[sslot]));
+        if constexpr (kSwap) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&ctl->sempty[sslot]));
         }
         if (++slot == kSlots) {
           slot = 0;
@@ -252,34 +325,41 @@ __global__ void __launch_bounds__(kThreads, 1)
           sphase ^= 1u;
         }
       }
-      const float *x = reinterpret_cast<const float *>(acc);
-      const int cols = min(args.bn, (kSwap ? p.M : p.N) - (c0 - half * kHalf));  // of the tile
+      float x[kMine];
+#pragma unroll
+      for (int i = 0; i < kMine / 2; ++i) {
+        const float2 v = unpair2(acc[i]);
+        x[2 * i] = v.x;
+        x[2 * i + 1] = v.y;
+      }
+      const int cols = min(args.bn, (kSwap ? p.M : p.N) - (c0 - own));  // of the tile
       if (args.split > 1) {
         // CTA q of the cluster sums the columns [q * per, (q + 1) * per)
         const int per = (args.bn + 8 * args.split - 1) / (8 * args.split) * 8;
         cluster_sync();  // every CTA is done with its ring
         if (ok && work) {
 #pragma unroll
-          for (int i = 0; i < kHalf; ++i) {
-            const int c = half * kHalf + i;
+          for (int i = 0; i < kMine; i += 8) {
+            const int c = own + i;  // eight columns go to one CTA: per is a multiple of 8
             if (c < cols) {
               const int q = c / per;
-              store_remote(base + static_cast<uint32_t>(((rank * per + c - q * per) * kLanes + row)
-                                                        * 4),
-                           q, x[i]);
+              const uint32_t at = remote_smem(
+                  base + static_cast<uint32_t>(((rank * per + c - q * per) * kLanes + row) * 4), q);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) store_remote(at + e * kLanes * 4, x[i + e]);
             }
           }
         }
         cluster_sync();
         const float *in_parts = reinterpret_cast<const float *>(smem);
         const int n = min(per, cols - rank * per);
-        for (int v = 8 * half; v < n; v += 16) {
+        for (int v = 8 * (warp >> 2); v < n; v += 8 * kParts) {
           float y[8] = {};
           for (int q = 0; q < args.split; ++q)
 #pragma unroll
             for (int e = 0; e < 8; ++e)
               if (v + e < n) y[e] += in_parts[(q * per + v + e) * kLanes + row];
-          const int c = c0 - half * kHalf + rank * per + v;
+          const int c = c0 - own + rank * per + v;
           if (l0 + row < (kSwap ? p.N : p.M) && !*const_cast<volatile int *>(&ctl->abort)) {
             if constexpr (kSwap) {
 #pragma unroll
@@ -293,20 +373,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       } else if (ok && work && l0 + row < (kSwap ? p.N : p.M)) {
         if constexpr (kSwap) {
 #pragma unroll
-          for (int i = 0; i < kHalf; ++i)
-            if (half * kHalf + i < cols) store_one(p, (c0 + i) * p.os + l0 + row, x[i]);
+          for (int i = 0; i < kMine; ++i)
+            if (own + i < cols) store_one(p, (c0 + i) * p.os + l0 + row, x[i]);
         } else {
 #pragma unroll
-          for (int i = 0; i < kHalf; i += 8)
-            if (half * kHalf + i < cols)
-              store_eight(p, (l0 + row) * p.os + c0 + i, x + i, cols - half * kHalf - i,
+          for (int i = 0; i < kMine; i += 8)
+            if (own + i < cols)
+              store_eight(p, (l0 + row) * p.os + c0 + i, x + i, cols - own - i,
                           args.fast);
         }
       }
     }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-    if (warp == 8) {
+    if (warp == kLoadWarp) {
       // ---------------- TMA ----------------
       const uint64_t policy = policy_evict_normal();
       const uint32_t tx = static_cast<uint32_t>((kLanes + args.bn) * kBlk);
@@ -332,7 +412,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-    } else if (warp == 9) {
+    } else if (warp == kMmaWarp) {
       // ---------------- products ----------------
       const uint32_t idesc = idesc_e4m3(kLanes, args.bn);
       int stage = 0, slot = 0, consumed = 0;
@@ -371,29 +451,40 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
     } else if (kSwap) {
-      // ---------------- the columns' scales: warps 10 and 11 in turn --------
-      int i = 0;  // block of this CTA's run
+      // ---------------- the columns' scales: the last two warps in turn --------
+      // four blocks at a time, so that one wait for memory serves four
+      int i0 = 0;  // first block of the group in this CTA's run
       bool ok = true;
       for (int tile = first; tile < args.tiles && ok; tile += step) {
         const int lt = tile % args.lane_tiles, c0 = tile / args.lane_tiles * args.bn;
         const float *ws = p.ws + static_cast<int64_t>(lt) * p.kb;
-        for (int kb = kb0; kb < kb1; ++kb, ++i) {
-          if ((i & 1) != warp - 10) continue;
-          float v[kCols / 32];
-          const float w = __ldg(ws + kb);
+        for (int kb = kb0; kb < kb1 && ok; kb += 4) {
+          const int n = min(4, kb1 - kb), i = i0;
+          i0 += n;
+          if (((kb - kb0) >> 2 & 1) != warp - kScaleWarp) continue;
+          constexpr int kE = kCols / 32;
+          float v[kE][4], w[4];
 #pragma unroll
-          for (int e = 0; e < kCols / 32; ++e) {
+          for (int t = 0; t < 4; ++t) w[t] = t < n ? __ldg(ws + kb + t) : 0.0f;
+#pragma unroll
+          for (int e = 0; e < kE; ++e) {
             const int c = c0 + lane + 32 * e;
-            v[e] = lane + 32 * e < args.bn && c < p.M
-                       ? __ldg(p.as + static_cast<int64_t>(c) * p.kb + kb) * w
-                       : 0.0f;
-          }
-          const int s = i % kScaleSlots;
-          if (!(ok = wait_warp(ctl, &ctl->sempty[s], ((i / kScaleSlots) & 1) ^ 1, args))) break;
+            const bool in = lane + 32 * e < args.bn && c < p.M;
+            const float *as = p.as + static_cast<int64_t>(in ? c : 0) * p.kb + kb;
 #pragma unroll
-          for (int e = 0; e < kCols / 32; ++e) ctl->scale[s][lane + 32 * e] = v[e];
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&ctl->sfull[s]));
+            for (int t = 0; t < 4; ++t) v[e][t] = in && t < n ? __ldg(as + t) : 0.0f;
+          }
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {
+            if (t >= n) break;
+            const int s = (i + t) % kScaleSlots;
+            if (!(ok = wait_warp(ctl, &ctl->sempty[s], (((i + t) / kScaleSlots) & 1) ^ 1, args)))
+              break;
+#pragma unroll
+            for (int e = 0; e < kE; ++e) ctl->scale[s][lane + 32 * e] = v[e][t] * w[t];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&ctl->sfull[s]));
+          }
         }
       }
     }
@@ -406,7 +497,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // ---------------- teardown ----------------
   tc_fence_before();
   __syncthreads();
-  if (warp == 8 && lane == 0) {
+  if (warp == kLoadWarp && lane == 0) {
     // only after an abort can copies still be in flight
     const int never = 0;
     for (int i = ctl->consumed; i < ctl->issued; ++i)
@@ -414,7 +505,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 static_cast<uint32_t>((i / args.stages) & 1), kCleanupLimitNs, &never);
   }
   __syncthreads();
-  if (warp == 9) {
+  if (warp == kMmaWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
@@ -522,6 +613,9 @@ int launch_matmul_fp8(const spec_target &h, const MatmulParams &P, cudaStream_t 
   if (args.stages > kMaxStages) args.stages = kMaxStages;
   const int es = P.out_dtype == SV_FP32 ? 4 : 2;
   args.fast = (reinterpret_cast<uintptr_t>(P.out) & 15u) == 0 && P.os * es % 16 == 0;
+  args.fast_scales = P.kb % 4 == 0 && args.split == 1 &&
+                     ((reinterpret_cast<uintptr_t>(P.as) | reinterpret_cast<uintptr_t>(P.ws)) &
+                      15u) == 0;
   CUtensorMap lane, col;
   if (!encode_rows(&lane, swap ? P.w : P.a, P.K, rows, kLanes) ||
       !encode_rows(&col, swap ? P.a : P.w, P.K, other, args.bn))
