@@ -1,4 +1,5 @@
-"""Builds ``libspec_verify.so`` in-tree for sm_103a with nvcc.
+"""Builds ``libspec_verify.so`` in-tree for sm_103a with nvcc, and the compiled
+Python binding of the target-layer operators beside it.
 
 Each CUDA translation unit is compiled in parallel into ``_build/`` and
 linked with the static CUDA runtime, so the library loads on machines
@@ -10,6 +11,7 @@ import concurrent.futures
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -26,6 +28,29 @@ HEADERS = ["sv_internal.cuh", "sv_kernels.h", "sv_target.cuh", "sv_attn.cuh",
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
          "--expt-relaxed-constexpr", "-I", INCLUDE]
+
+
+BIND_SRC = os.path.join(CSRC, "sv_bind.cpp")
+BIND = os.path.join(HERE, "_target_bind.so")
+
+
+def _bind_commands():
+    """(compile, link, object) of the binding for the torch that is installed."""
+    import torch
+    t = os.path.dirname(torch.__file__)
+    cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
+    obj = os.path.join(BUILD, f"sv_bind.{torch.__version__}.o")
+    inc = [os.path.join(t, "include"),
+           os.path.join(t, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], os.path.join(cuda, "include"), INCLUDE]
+    flags = ["-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+             f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+    compile_ = ["g++", *flags, *[x for i in inc for x in ("-I", i)], "-c", BIND_SRC, "-o", obj]
+    lib = os.path.join(t, "lib")
+    link = ["g++", "-shared", obj, "-L", lib, "-lc10", "-lc10_cuda", "-ltorch_cpu",
+            "-ltorch_cuda", "-ltorch_python", "-L", HERE, "-l:libspec_verify.so",
+            "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib}"]
+    return compile_, link, obj
 
 
 def _nvcc():
@@ -58,6 +83,10 @@ def build(force: bool = False, ptxas_verbose: bool = False, verbose: bool = Fals
                 cmd.append("-Xptxas=-v")
             jobs.append(cmd)
 
+    bind_compile, bind_link, bind_obj = _bind_commands()
+    if force or _stale(bind_obj, [BIND_SRC] + hdrs):
+        jobs.insert(0, bind_compile)
+
     def run(cmd):
         r = subprocess.run(cmd, capture_output=True, text=True)
         return cmd, r
@@ -68,8 +97,8 @@ def build(force: bool = False, ptxas_verbose: bool = False, verbose: bool = Fals
                 if verbose or ptxas_verbose or r.returncode != 0:
                     sys.stderr.write(r.stdout + r.stderr)
                 if r.returncode != 0:
-                    raise RuntimeError(f"nvcc failed: {' '.join(cmd)}")
-    if force or jobs or _stale(LIB, objs):
+                    raise RuntimeError(f"compilation failed: {' '.join(cmd)}")
+    if force or _stale(LIB, objs):
         tmp = LIB + f".tmp{os.getpid()}"
         cmd = [nvcc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs,
                "-ldl", "-lpthread", "-lrt"]
@@ -78,6 +107,13 @@ def build(force: bool = False, ptxas_verbose: bool = False, verbose: bool = Fals
             sys.stderr.write(r.stdout + r.stderr)
             raise RuntimeError("link failed")
         os.replace(tmp, LIB)
+    if force or _stale(BIND, [bind_obj, LIB]):
+        tmp = BIND + f".tmp{os.getpid()}"
+        r = subprocess.run([*bind_link, "-o", tmp], capture_output=True, text=True)
+        if r.returncode != 0:
+            sys.stderr.write(r.stdout + r.stderr)
+            raise RuntimeError("link of the binding failed")
+        os.replace(tmp, BIND)
     return LIB
 
 

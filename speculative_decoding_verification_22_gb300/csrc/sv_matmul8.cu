@@ -9,15 +9,15 @@
 // slots.  The scales can be any fp32 number, which the hardware's own block
 // scales (powers of two) cannot.
 //
-//  * Few rows (up to 256): the weight's rows are the 128 lanes of a tile and
+//  * Few rows (up to 96): the weight's rows are the 128 lanes of a tile and
 //    A's rows its columns, so W is streamed once and nothing is padded to
-//    128.  More rows: A's rows are the lanes and a tile is 128 x 256, so a
-//    thread's scale is one number for 128 columns.
+//    128.  More rows: A's rows are the lanes and a tile is 128 x 256 (or 128),
+//    so a thread's scale is one number for its columns.
 //  * Fewer tiles than SMs: a cluster of up to eight CTAs shares a tile, each
 //    takes a part of K, and the parts are added through distributed shared
 //    memory in the order of K (repeatable, no scratch, no second launch).
-//  * Warps 0-15: scale and add (four warpgroups, a quarter of the columns
-//    each); warp 16: TMA; warp 17: products; warps 18, 19: the columns' scales.
+//  * Warps 0-7: scale and add (two warpgroups, half of the columns each);
+//    warp 8: TMA; warp 9: products; warps 10, 11: the columns' scales.
 #include <cudaTypedefs.h>
 
 #include "sv_target.cuh"
@@ -26,14 +26,11 @@
 namespace sv {
 namespace {
 
-#ifndef ADDW
-#define ADDW 8
-#endif
-constexpr int kAddWarps = ADDW;
+constexpr int kAddWarps = 8;
 constexpr int kThreads = 32 * kAddWarps + 128;
 // Registers a thread: 168 at launch; the adding warps take what the others give
 // back (256 * 216 + 128 * 72 = 384 * 168).
-constexpr int kAddRegs = ADDW == 8 ? 216 : 104, kOtherRegs = ADDW == 8 ? 72 : 64;
+constexpr int kAddRegs = 216, kOtherRegs = 72;
 constexpr int kLoadWarp = kAddWarps, kMmaWarp = kAddWarps + 1, kScaleWarp = kAddWarps + 2;
 constexpr int kLanes = 128;      // rows of a tile
 constexpr int kBlk = 128;        // K elements (bytes) of a block
@@ -420,12 +417,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       for (int tile = first; tile < args.tiles && ok; tile += step) {
         for (int kb = kb0; kb < kb1; ++kb) {
-          if (!(ok = wait_warp(ctl, &ctl->tempty[slot], tphase ^ 1u, args))) break;
           if (!(ok = wait_warp(ctl, &ctl->full[stage], phase, args))) break;
           if (lane == 0) ctl->consumed = ++consumed;
-          tc_fence_after();
           const uint32_t at = base + stage * args.stage_bytes;
           const uint64_t ad = sw128_desc(at), bd = sw128_desc(at + kLanes * kBlk);
+          if (!(ok = wait_warp(ctl, &ctl->tempty[slot], tphase ^ 1u, args))) break;
+          tc_fence_after();
           if (elect_one()) {
 #pragma unroll
             for (int k = 0; k < 4; ++k)
@@ -593,19 +590,34 @@ int launch_matmul_fp8(const spec_target &h, const MatmulParams &P, cudaStream_t 
   args.p = P;
   args.status = h.status;
   args.wait_limit_ns = h.wait_limit_ns;
-  const bool swap = P.M <= 256;
+  // Up to 96 rows W's rows are the lanes: 96 x 8192 x 8192 in 17.7 us against
+  // 18.1 the other way, 128 in 18.9 against 18.5.
+  const bool swap = P.M <= 96;
   const int rows = swap ? P.N : P.M, other = swap ? P.M : P.N;
   const int lane_tiles = (rows + kLanes - 1) / kLanes;
-  args.bn = swap ? (P.M + 15) / 16 * 16 : 256;
-  if (!swap && static_cast<int64_t>(lane_tiles) * ((other + 255) / 256) < h.num_sms) args.bn = 128;
-  const int64_t tiles = static_cast<int64_t>(lane_tiles) * ((other + args.bn - 1) / args.bn);
+  // A tile's columns and the CTAs that share it, by the time that its blocks
+  // take (a block of 256 columns about 1000 cycles, of 128 about 600): the
+  // largest cluster of which all tiles' run at once, else one CTA a tile and
+  // whole waves.
+  int64_t tiles = 0, best = INT64_MAX;
+  for (const int bn : {swap ? (P.M + 15) / 16 * 16 : 256, 128}) {
+    const int64_t n = static_cast<int64_t>(lane_tiles) * ((other + bn - 1) / bn);
+    int split = 1;
+    for (int s = 2; s <= kMaxSplit && s <= P.kb; ++s)
+      if (n <= h.clusters[s]) split = s;
+    const int64_t waves = split > 1 ? 1 : (n + h.num_sms - 1) / h.num_sms;
+    const int64_t time = waves * ((P.kb + split - 1) / split) * (bn > 128 ? 10 : 6);
+    if (time < best) {
+      best = time;
+      tiles = n;
+      args.bn = bn;
+      args.split = split;
+    }
+    if (swap) break;
+  }
   if (tiles > INT32_MAX) return SV_ERR_SHAPE;
   args.lane_tiles = lane_tiles;
   args.tiles = static_cast<int>(tiles);
-  args.split = 1;
-  // the largest cluster of which all tiles' run at once
-  for (int s = 2; s <= kMaxSplit && s <= P.kb; ++s)
-    if (tiles <= h.clusters[s]) args.split = s;
   const int grid = args.split > 1 ? args.split * args.tiles
                                   : (args.tiles < h.num_sms ? args.tiles : h.num_sms);
   args.stage_bytes = ((kLanes + args.bn) * kBlk + 1023) / 1024 * 1024;
@@ -628,10 +640,8 @@ int launch_matmul_fp8(const spec_target &h, const MatmulParams &P, cudaStream_t 
     e = launch<32, true>(args, lane, col, grid, stream);
   else if (args.bn <= 64)
     e = launch<64, true>(args, lane, col, grid, stream);
-  else if (args.bn <= 128)
-    e = launch<128, true>(args, lane, col, grid, stream);
   else
-    e = launch<256, true>(args, lane, col, grid, stream);
+    e = launch<128, true>(args, lane, col, grid, stream);
   return e == cudaSuccess ? SV_OK : SV_ERR_CUDA;
 }
 
