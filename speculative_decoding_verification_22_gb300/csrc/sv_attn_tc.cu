@@ -145,6 +145,8 @@ __device__ __forceinline__ int group_div(const TcArgs &args, int G, int r) {
   return q * G > r ? q - 1 : q;  // the reciprocal is rounded up: at most one too many
 }
 
+constexpr int kFewItems = 4;  // items of a sequence that one lane counts by itself
+
 // Walks the items of every side-th cache head (h counts those) from a unit on.
 // Divisions and long arithmetic are kept out: the first tile waits for this.
 struct Items {
@@ -183,14 +185,15 @@ struct Items {
   __device__ int64_t head_units(int lane) {
     int64_t u = 0;
     sequence();
-    if (s.n > 0 && nm == 1) {
-      m = 0;
-      item();
-      u = units();
+    if (s.n > 0 && nm <= kFewItems) {
+      for (m = 0; m < nm; ++m) {
+        item();
+        u += units();
+      }
     }
-    // sequences of several items: the warp takes one at a time, an item a lane
+    // sequences of many items: the warp takes one at a time, an item a lane
     const SeqGeom mine = s;
-    unsigned many = __ballot_sync(0xffffffffu, s.n > 0 && nm > 1);
+    unsigned many = __ballot_sync(0xffffffffu, s.n > 0 && nm > kFewItems);
     while (many) {
       const int src = __ffs(many) - 1;
       many &= many - 1;
@@ -221,8 +224,14 @@ struct Items {
       off -= h * per;
     }
     for (; off >= per; ++h) off -= per;
-    m = 0;
-    for (int m0 = 0; nm > 1 && m0 < nm; m0 += 32) {
+    if (nm <= kFewItems) {
+      for (m = 0; m + 1 < nm; ++m) {
+        item();
+        if (off < units()) break;
+        off -= units();
+      }
+    }
+    for (int m0 = 0; nm > kFewItems && m0 < nm; m0 += 32) {
       m = m0 + lane;
       int64_t mine = 0;
       if (m < nm) {
@@ -1041,7 +1050,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Joins the parts of the items that were cut, in their order.  A warp takes 32
 // rows, one a lane, and eight elements of the head; block (c, y) works on the
 // item that begins in CTA c.
-constexpr int kJoinWarps = 8, kJoinBlocks = 2, kJoinElems = 8, kJoinParts = 4;
+constexpr int kJoinWarps = 8, kJoinElems = 8, kJoinParts = 4;
 template <class T, int DPAD>
 __global__ void __launch_bounds__(32 * kJoinWarps)
     attention_join_kernel(const __grid_constant__ TcArgs args) {
@@ -1063,7 +1072,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
   const int b = d.b, h = d.h, r0 = d.r0, t0 = d.t0;
   constexpr int kGroups = DPAD / kJoinElems;
   const int tasks = (rows + 31) / 32 * kGroups;
-  for (int i = blockIdx.y * kJoinWarps + warp; i < tasks; i += kJoinBlocks * kJoinWarps) {
+  for (int i = blockIdx.y * kJoinWarps + warp; i < tasks; i += gridDim.y * kJoinWarps) {
     const int r = i / kGroups * 32 + lane, d0 = i % kGroups * kJoinElems;
     if (d0 >= a.D) continue;
     const bool valid = r < rows;
@@ -1190,7 +1199,11 @@ int launch_typed(const spec_target &h, const TcArgs &args, const CUtensorMap &tm
   if (launch_chained(attention_tc_kernel<T, DPAD>, dim3(grid), dim3(kThreads), smem, stream, tmK,
                      tmV, args) != cudaSuccess)
     return SV_ERR_CUDA;
-  return launch_chained(attention_join_kernel<T, DPAD>, dim3(grid, kJoinBlocks),
+  // an item's rows, on average: sixteen warps for each 32 of them
+  const int64_t rows = (static_cast<int64_t>(args.a.T) * (args.a.Hq / args.a.Hkv) + args.a.B - 1) /
+                       args.a.B;
+  const int blocks = rows > 128 ? 8 : rows > 64 ? 4 : 2;
+  return launch_chained(attention_join_kernel<T, DPAD>, dim3(grid, blocks),
                         dim3(32 * kJoinWarps), 0, stream, args) == cudaSuccess
              ? SV_OK
              : SV_ERR_CUDA;
