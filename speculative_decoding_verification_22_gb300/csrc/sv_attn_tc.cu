@@ -649,6 +649,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++items;
       tc_fence_after();
 
+      // A NaN score is no maximum, so it may have left m at -inf; as the largest
+      // of all it is not taken for "saw nothing" where parts are joined.
+      if (l != l) m = INFINITY;
+
       // ---- the item's result, or this CTA's part of it ----
       float f0 = 1.0f, f1 = 0.0f;
       const bool join = !wide && n > 1;

@@ -11,6 +11,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -73,17 +74,37 @@ spec_target_t *handle(PyObject *self) {
   return h;
 }
 
-// The stream given (an object with cuda_stream, or its number), or the
-// current one of the tensor's device.
-void *stream_of(PyObject *o, const Tensor &x) {
-  if (!given(o)) return c10::cuda::getCurrentCUDAStream(x.get_device()).stream();
-  if (PyLong_Check(o)) return PyLong_AsVoidPtr(o);
-  PyObject *n = PyObject_GetAttr(o, g_stream);
-  if (!n) throw Raised();
-  void *s = PyLong_AsVoidPtr(n);
-  Py_DECREF(n);
-  return s;
-}
+// The stream of a call: the one given (an object with cuda_stream, or its
+// number), else the current one of the tensor's device.  While it lives the
+// given stream is the current one, so that new outputs come from its memory.
+class Stream {
+ public:
+  Stream(PyObject *o, const Tensor &x) {
+    const c10::DeviceIndex dev = x.get_device();
+    if (!given(o)) {
+      stream_ = c10::cuda::getCurrentCUDAStream(dev).stream();
+      return;
+    }
+    void *p;
+    if (PyLong_Check(o)) {
+      p = PyLong_AsVoidPtr(o);
+    } else {
+      PyObject *n = PyObject_GetAttr(o, g_stream);
+      if (!n) throw Raised();
+      p = PyLong_AsVoidPtr(n);
+      Py_DECREF(n);
+    }
+    if (PyErr_Occurred()) throw Raised();
+    stream_ = static_cast<cudaStream_t>(p);
+    guard_.reset_stream(p ? c10::cuda::getStreamFromExternal(stream_, dev)
+                          : c10::cuda::getDefaultCUDAStream(dev));
+  }
+  void *get() const { return stream_; }
+
+ private:
+  cudaStream_t stream_ = nullptr;
+  c10::cuda::OptionalCUDAStreamGuard guard_;
+};
 
 Tensor empty(at::IntArrayRef sizes, at::ScalarType t, const Tensor &like) {
   return at::detail::empty_cuda(sizes, t, like.device(), std::nullopt);
@@ -146,6 +167,7 @@ PyObject *norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
     need(w.scalar_type() == dt && w.is_contiguous(),
          "rms_norm: weight must be dense and of x's type");
     need(x.is_cuda() && w.is_cuda(), "rms_norm: tensors must be on the GPU");
+    const Stream stream(a[9], x);
     const int64_t rows = x.size(0), d = x.size(1), xs = row_stride(x, "x");
     auto like_x = [&](const Tensor &t) {
       return t.dim() == 2 && t.size(0) == rows && t.size(1) == d && t.scalar_type() == dt &&
@@ -194,7 +216,7 @@ PyObject *norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
     }
     if (!quant) {
       check(spec_target_rms_norm(handle(a[0]), x.data_ptr(), xs, res, rs, w.data_ptr(), eps, rows,
-                                 d, code, out, os, ro, ros, stream_of(a[9], x)),
+                                 d, code, out, os, ro, ros, stream.get()),
             "spec_target_rms_norm");
       PyObject *list = PyList_New(second ? 2 : 1);
       PyList_SET_ITEM(list, 0, result(a[6], made));
@@ -214,7 +236,7 @@ PyObject *norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
       scale = made_scale.data_ptr<float>();
     }
     check(spec_target_rms_norm_fp8(handle(a[0]), x.data_ptr(), xs, res, rs, w.data_ptr(), eps,
-                                   rows, d, code, group, out, scale, ro, ros, stream_of(a[9], x)),
+                                   rows, d, code, group, out, scale, ro, ros, stream.get()),
           "spec_target_rms_norm_fp8");
     PyObject *list = PyList_New(second ? 3 : 2);
     PyList_SET_ITEM(list, 0, result(a[6], made));
@@ -242,6 +264,7 @@ PyObject *matmul(PyObject *, PyObject *const *a, Py_ssize_t n) {
          "tensors must be contiguous");
     need(x.is_cuda() && w.is_cuda() && sx.is_cuda() && sw.is_cuda(),
          "matmul_fp8: tensors must be on the GPU");
+    const Stream stream(a[7], x);
     Tensor made;
     void *out;
     int64_t os = N;
@@ -261,7 +284,7 @@ PyObject *matmul(PyObject *, PyObject *const *a, Py_ssize_t n) {
     }
     check(spec_target_matmul_fp8(handle(a[0]), x.data_ptr(), sx.data_ptr<float>(), w.data_ptr(),
                                  sw.data_ptr<float>(), M, N, K, code, out, os,
-                                 stream_of(a[7], x)),
+                                 stream.get()),
           "spec_target_matmul_fp8");
     return result(a[6], made);
   });
@@ -298,6 +321,7 @@ PyObject *rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
     need(q.is_cuda() && k.is_cuda() && v.is_cuda() && pos.is_cuda() && slots.is_cuda() &&
              f.is_cuda() && kc.is_cuda() && vc.is_cuda(),
          "rope_append: tensors must be on the GPU");
+    const Stream stream(a[12], q);
     Tensor made;
     if (given(a[11])) {
       const Tensor &o = tensor(a[11], "rope_append: q_out");
@@ -345,7 +369,7 @@ PyObject *rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
     r.interleaved = PyObject_IsTrue(a[9]) == 1;
     r.dtype = code;
     r.magnitude = static_cast<float>(number(a[10]));
-    check(spec_target_rope_append(handle(a[0]), &r, stream_of(a[12], q)),
+    check(spec_target_rope_append(handle(a[0]), &r, stream.get()),
           "spec_target_rope_append");
     return result(a[11], made);
   });
@@ -377,6 +401,7 @@ PyObject *attention(PyObject *, PyObject *const *a, Py_ssize_t n) {
     need(T <= INT32_MAX && table.size(0) <= INT32_MAX && table.size(1) <= INT32_MAX &&
              kc.size(1) <= INT32_MAX,
          "attention: sizes");
+    const Stream stream(a[12], q);
     sv_attention_t r{};
     if (given(a[9])) {
       const Tensor &m = tensor(a[9], "attention: tree_mask");
@@ -435,7 +460,7 @@ PyObject *attention(PyObject *, PyObject *const *a, Py_ssize_t n) {
     r.dtype = code;
     r.scale = static_cast<float>(given(a[7]) ? number(a[7])
                                              : 1.0 / std::sqrt(static_cast<double>(D)));
-    check(spec_target_attention(handle(a[0]), &r, stream_of(a[12], q)), "spec_target_attention");
+    check(spec_target_attention(handle(a[0]), &r, stream.get()), "spec_target_attention");
     return result(a[10], made);
   });
 }

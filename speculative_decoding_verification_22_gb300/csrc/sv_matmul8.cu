@@ -18,6 +18,14 @@
 //    memory in the order of K (repeatable, no scratch, no second launch).
 //  * Warps 0-7: scale and add (two warpgroups, half of the columns each);
 //    warp 8: TMA; warp 9: products; warps 10, 11: the columns' scales.
+//
+// What bounds it (4096 x 14336 x 4096, 205 us, 2.35 PFLOP/s): a block of 128 x
+// 256 x 128 takes the tensor cores 512 cycles and the whole loop about 1000.
+// The products alone run in 127 us.  With the loads it is 190: a load takes
+// 1.6 us from its slot's being freed to its use, and the four blocks of 48 KB
+// that fit in shared memory are in flight for that long.  With the adding it
+// is 189: tensor memory holds two blocks, and a block's products, hand-over
+// and reading follow one another.
 #include <cudaTypedefs.h>
 
 #include "sv_target.cuh"
@@ -29,8 +37,11 @@ namespace {
 constexpr int kAddWarps = 8;
 constexpr int kThreads = 32 * kAddWarps + 128;
 // Registers a thread: 168 at launch; the adding warps take what the others give
-// back (256 * 216 + 128 * 72 = 384 * 168).
-constexpr int kAddRegs = 216, kOtherRegs = 72;
+// back (256 * 216 + 128 * 72 = 256 * 224 + 128 * 56 = 384 * 168).
+template <int kCols>
+constexpr int add_regs() { return kCols == 256 ? 224 : 216; }
+template <int kCols>
+constexpr int other_regs() { return kCols == 256 ? 56 : 72; }
 constexpr int kLoadWarp = kAddWarps, kMmaWarp = kAddWarps + 1, kScaleWarp = kAddWarps + 2;
 constexpr int kLanes = 128;      // rows of a tile
 constexpr int kBlk = 128;        // K elements (bytes) of a block
@@ -219,7 +230,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp < kAddWarps) {
     // ---------------- scale, add, store ----------------
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kAddRegs));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(add_regs<kCols>()));
     const int own = (warp >> 2) * kMine, row = tid & 127;  // first column, lane
     const uint32_t tacc =
         tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + own;
@@ -280,7 +291,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t s2 = pair2(s, s);
         if (work) {
           // the next columns are read while these are scaled and added
-          constexpr int kChunk = kMine == 64 || kMine == 32 ? 32 : 16, kChunks = kMine / kChunk;
+          constexpr int kChunk = kMine < 32 ? 16 : 32, kChunks = kMine / kChunk;
           uint32_t x[kChunks > 1 ? 2 : 1][kChunk];
           read_columns<kChunk>(tacc + slot * kCols, x[0]);
 #pragma unroll
@@ -382,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(other_regs<kCols>()));
     if (warp == kLoadWarp) {
       // ---------------- TMA ----------------
       const uint64_t policy = policy_evict_normal();

@@ -440,6 +440,138 @@ def test_attention_output_strides(ops):
         assert int((big != 5.0).sum()) <= want.numel()
 
 
+@pytest.mark.parametrize("B", [33, 64, 400, 1000])
+def test_attention_many_sequences(ops, B):
+    """More sequences than a warp and than a block counts at once, some empty."""
+    g = gen(B)
+    news = torch.randint(0, 4, (B,), generator=g, device="cuda").tolist()
+    lens = torch.randint(0, 300, (B,), generator=g, device="cuda").tolist()
+    news[0], news[-1], lens[B // 2] = 0, 2, 0
+    check_attention(ops, g, "bf16", 4, 2, 64, 16, news, lens)
+
+
+@pytest.mark.parametrize("hq,hkv,news,lens", [
+    (4, 1, [3, 1], [30000, 500]),        # one cache head: parts on every SM
+    (4, 1, [2100], [2500]),              # more items of a sequence than lanes
+    (2, 2, [1300, 40, 7], [1300, 9000, 64]),
+])
+def test_attention_long(ops, hq, hkv, news, lens):
+    check_attention(ops, gen(len(news)), "bf16", hq, hkv, 64, 32, news, lens)
+
+
+def test_attention_odd_alignments(ops):
+    """Queries and caches off 16 bytes, and strides that are no multiple of them."""
+    g = gen(14)
+    for name in ("q", "cache", "both"):
+        kc, vc, table, ks, vs = build_cache(g, [200, 90], 16, 2, 64, torch.bfloat16, fill=0.0)
+        q = randn(g, (6, 4, 64), torch.bfloat16)
+        want_q = q
+        if name != "cache":
+            q = torch.nn.functional.pad(q, (1, 2))[..., 1:65]
+        if name != "q":
+            kc = torch.nn.functional.pad(kc, (3, 0))[..., 3:]
+            vc = torch.nn.functional.pad(vc, (1, 0))[..., 1:]
+        qs = torch.tensor([0, 4, 6], dtype=torch.int32, device="cuda")
+        kl = torch.tensor([200, 90], dtype=torch.int32, device="cuda")
+        out = ops.attention(q, kc, vc, table, qs, kl)
+        o, mag, _, big = attention_ref(want_q, ks, vs, [4, 2], 0.125)
+        within(out, o, attention_bound(o, mag, big, 64, torch.bfloat16))
+
+
+def test_attention_query_not_finite(ops):
+    """A NaN query spoils its own row only."""
+    g = gen(15)
+    kc, vc, table, ks, vs = build_cache(g, [300], 16, 1, 64, torch.bfloat16)
+    q = randn(g, (9, 4, 64), torch.bfloat16)
+    qs = torch.tensor([0, 9], dtype=torch.int32, device="cuda")
+    kl = torch.tensor([300], dtype=torch.int32, device="cuda")
+    want = ops.attention(q, kc, vc, table, qs, kl)
+    q[4, 2, 5] = float("nan")
+    out = ops.attention(q, kc, vc, table, qs, kl)
+    assert torch.isnan(out[4, 2]).all()
+    out[4, 2] = want[4, 2]
+    assert torch.equal(out, want)
+
+
+# ---- refusals through Python, waits that run out ---------------------------------------
+
+def test_refusals_through_python(ops):
+    x = torch.ones(4, 72, device="cuda").to(torch.float8_e4m3fn)
+    s = torch.ones(4, 1, device="cuda")
+    with pytest.raises(sv.SpecVerifyError) as e:
+        ops.matmul_fp8(x, s, x, torch.ones(1, 1, device="cuda"))  # K no multiple of 16
+    assert e.value.code == sv.SV_ERR_SHAPE
+    h = torch.ones(4, 64, device="cuda")
+    w = torch.ones(64, device="cuda")
+    with pytest.raises(sv.SpecVerifyError) as e:
+        ops.rms_norm(h, w, eps=-1.0)
+    assert e.value.code == sv.SV_ERR_ARG
+    with pytest.raises(sv.SpecVerifyError) as e:
+        ops.rms_norm_fp8(h, w, group=64)
+    assert e.value.code == sv.SV_ERR_ARG
+    for bad in (h.cpu(), h.double(), h[0], "x"):
+        with pytest.raises(ValueError):
+            ops.rms_norm(bad, w)
+    with pytest.raises(ValueError):
+        ops.matmul_fp8(x, s, x, torch.ones(1, 1, device="cuda"), out_dtype=torch.float64)
+    c = torch.zeros(2, 16, 1, 64, device="cuda")
+    q = torch.zeros(2, 3, 64, device="cuda")
+    i = torch.zeros(1, 1, dtype=torch.int32, device="cuda")
+    two = torch.tensor([0, 2], dtype=torch.int32, device="cuda")
+    one = torch.tensor([2], dtype=torch.int32, device="cuda")
+    with pytest.raises(sv.SpecVerifyError):
+        ops.attention(q, c, c, i, two, one, window=-1)
+    with pytest.raises(ValueError):
+        ops.attention(q, c, c, i.long(), two, one)
+    with pytest.raises(ValueError):
+        ops.attention(q, c, c.half(), i, two, one)
+    assert ops.attention(q, c, c, i, two, one).shape == q.shape
+    closed = sv.TargetOps()
+    closed.close()
+    with pytest.raises(sv.SpecVerifyError) as e:
+        closed.rms_norm(h, w)
+    assert e.value.code == sv.SV_ERR_ARG
+
+
+def test_a_given_stream(ops):
+    g = gen(16)
+    x, w = randn(g, (33, 512), torch.bfloat16), randn(g, (512,), torch.bfloat16)
+    want = ops.rms_norm(x, w)[0]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for stream in (side, side.cuda_stream):
+        got = ops.rms_norm(x, w, stream=stream)[0]
+        side.synchronize()
+        assert torch.equal(got, want)
+    assert torch.cuda.current_stream() != side
+
+
+def test_a_wait_limit_of_nothing():
+    """With a limit of nothing a wait that is not soon satisfied gives up: the
+    call ends, either with its result or with a status that says so, and the
+    next call is right."""
+    ops = sv.TargetOps()
+    g = gen(17)
+    a, sa = quant_blocks(randn(g, (40, 2048)), 1)
+    w, sw = quant_blocks(randn(g, (512, 2048)), 128)
+    kc, vc, table, ks, vs = build_cache(g, [900], 16, 2, 64, torch.bfloat16, fill=0.0)
+    q = randn(g, (5, 4, 64), torch.bfloat16)
+    qs = torch.tensor([0, 5], dtype=torch.int32, device="cuda")
+    kl = torch.tensor([900], dtype=torch.int32, device="cuda")
+    calls = (lambda: ops.matmul_fp8(a, sa, w, sw), lambda: ops.attention(q, kc, vc, table, qs, kl))
+    for call in calls:
+        want = call()
+        assert ops.status() == sv.SV_OK
+        ops.set_wait_limit(0)
+        for _ in range(20):
+            got = call()
+            code = ops.status()
+            assert code == sv.SV_ERR_TIMEOUT or (code == sv.SV_OK and torch.equal(got, want))
+        ops.set_wait_limit(10 ** 9)
+        assert torch.equal(call(), want)
+        assert ops.status() == sv.SV_OK
+
+
 # ---- streams, graphs, use together ---------------------------------------------------
 
 def test_other_streams_and_graphs(ops):
