@@ -53,6 +53,10 @@ constexpr int kThreads = 384;
 constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
 constexpr int kSoftmaxWarps = 8;
 constexpr int kRingBytes = 160 * 1024;
+// Pages up to this size come with both 128-byte halves of a row in one box: 64
+// single tokens over 8192 in pages of 16 take 207 us against 242, as the TMA
+// takes about 55 ns a box whatever it holds; in pages of 32 202 against 200.
+constexpr int kPairedPage = 16;
 constexpr int kMaxSlots = 10;
 constexpr uint64_t kCleanupLimitNs = 2000000000ull;
 constexpr float kRescale = 8.0f;  // log2 of the growth of m that rescales O
@@ -125,6 +129,8 @@ struct TcArgs {
   int pow_page;  // log2 of the page size
   int side;      // cache heads walked side by side
   int walks;     // grid / side
+  int paired;    // both 128-byte halves of a row come in one box
+  int head2, head3;  // paired: a head's coordinates in dimensions 2 and 3
 };
 
 // `side` CTAs, for as many neighbouring cache heads, walk the same items and
@@ -838,7 +844,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 8) {
       // ---------------- TMA ----------------
       const int page_keys = min(64, a.page_size);
-      const uint32_t box_bytes = static_cast<uint32_t>(page_keys) * 128u;
+      const bool paired = Sh::kSlabs > 1 && args.paired;
+      const uint32_t box_bytes = static_cast<uint32_t>(page_keys) * (paired ? 128u * Sh::kSlabs : 128u);
       int slot = 0, issued = 0;
       uint32_t phase = 0;
       bool ok = true;
@@ -847,15 +854,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int n = it.n, tile0 = it.tile0, kv = it.s.kv, head = it.h;
         const bool wide = it.wide;
         // K and V that are not read again need not stay in L2: 64 single tokens
-        // over 8192 in 246 us against 253, eight trees of 65 in 62 against 68; a
+        // over 8192 in 247 us against 253, eight trees of 65 in 62 against 68; a
         // prompt's chunk, which comes back to them, in 723 against 653
         const uint64_t policy = it.once ? policy_evict_first() : policy_evict_normal();
         const int keys = wide ? kWideKeys : kNarrowKeys;
         const int32_t *pages = a.page_table + it.b * a.table_stride;
         // lane i brings box i of a tile: box i / slabs of its keys, slab i %
-        // slabs (at most 32 boxes, as a page holds 8 keys or more)
-        const int slab = lane % Sh::kSlabs, key_in = lane / Sh::kSlabs * page_keys;
-        const uint32_t offset = static_cast<uint32_t>(slab * keys * 128 + key_in * 128);
+        // slabs (at most 32 boxes, as a page holds 8 keys or more); paired: all
+        // slabs of box i
+        const int each = paired ? 1 : Sh::kSlabs;
+        const int slab = lane % each, key_in = lane / each * page_keys;
+        const uint32_t offset =
+            static_cast<uint32_t>(slab * keys * 128 + key_in * (paired ? 128 * Sh::kSlabs : 128));
+        const int head2 = head * args.head2, head3 = head * args.head3;
         auto page_of = [&](int t) {
           const int key = (tile0 + t) * keys + key_in;
           return t < n && key_in < keys && key < kv ? pages[key >> args.pow_page] : 0;
@@ -877,7 +888,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) mbar_arrive_expect_tx(full, wide ? bytes : 2 * bytes);
             __syncwarp();
             const uint32_t at = ring + slot * Sh::kSlotBytes + offset;
-            if (mine) {
+            if (mine && paired) {
+              const int group = head3 + (in_page >> 3);
+              tma_load_5d(at, v ? &tmV : &tmK, 0, 0, head2, group, page, full, policy);
+              if (!wide)
+                tma_load_5d(at + Sh::kSlotBytes / 2, &tmV, 0, 0, head2, group, page, full, policy);
+            } else if (mine) {
               tma_load_4d(at, v ? &tmV : &tmK, slab * 64, head, in_page, page, full, policy);
               if (!wide)
                 tma_load_4d(at + Sh::kSlotBytes / 2, &tmV, slab * 64, head, in_page, page, full,
@@ -920,12 +936,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         return r;
       };
-      const uint64_t q0 = sw128_desc(base), k_base = sw128_desc(ring);
+      // Bytes between the groups of eight keys of a tile, and between its slabs
+      // (of `keys` keys); in the layout of paired boxes a group's slabs are
+      // neighbours.
+      const bool paired = Sh::kSlabs > 1 && args.paired;
+      const uint32_t group_bytes = paired ? 1024 * Sh::kSlabs : 1024;
+      auto slab_bytes = [&](int keys) { return static_cast<uint32_t>(paired ? 1024 : keys * 128); };
+      const uint64_t q0 = sw128_desc(base);
+      const uint64_t k_base =
+          sw128_desc(ring) + (static_cast<uint64_t>((group_bytes - 1024) >> 4) << 32);
       constexpr uint32_t kSlot16 = Sh::kSlotBytes >> 4, kQ16 = Sh::kQBytes >> 4;
       // S of slot w: `keys` keys from ring slot s on; then commits s_full and,
       // if `last`, frees the slot
       auto scores = [&](int w, uint64_t q, int s, auto keys, bool last) {
-        constexpr uint32_t slab16 = keys * 128 >> 4;
+        const uint32_t slab16 = slab_bytes(keys) >> 4;
         constexpr uint32_t idesc = idesc_16(kBf16, kRows, keys, false);
         const uint64_t k = k_base + static_cast<uint32_t>(s) * kSlot16;
         if (elect_one()) {
@@ -940,11 +964,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       // O of slot w += P V, V at `at` in the ring, 16 keys a product
       auto outputs = [&](int w, uint32_t at, int s, auto keys, bool more, bool last) {
-        const uint64_t v = sw128_desc_mn(at, keys * 128);
+        const uint64_t v = sw128_desc_mn(at, slab_bytes(keys), group_bytes);
         if (elect_one()) {
 #pragma unroll
           for (int e = 0; e < keys / 16; ++e)
-            umma_16_ta(tmem + 256 + w * 128, tmem + w * 128 + e * 8, v + e * (2048 >> 4), idesc_o,
+            umma_16_ta(tmem + 256 + w * 128, tmem + w * 128 + e * 8, v + e * (2 * group_bytes >> 4), idesc_o,
                        more || e > 0);
           if (last) umma_commit(smem_u32(&ctl->empty[s]));
         }
@@ -954,11 +978,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       // has to give zero.
       auto zero_tail = [&](uint32_t at, int live, int keys) {
         uint8_t *v = smem + (at - base);
-        const int first = max(live, 0), count = (keys - first) * 8;
-        for (int x = lane; x < count * Sh::kSlabs; x += 32) {
-          const int slab = x / count, y = x - slab * count;
-          *reinterpret_cast<uint4 *>(v + slab * (keys * 128) + first * 128 + y * 16) =
-              make_uint4(0, 0, 0, 0);
+        for (int x = max(live, 0) * 8 + lane; x < keys * 8; x += 32) {
+          const int key = x >> 3;
+          uint8_t *at_key = v + (key >> 3) * group_bytes + (key & 7) * 128 + (x & 7) * 16;
+#pragma unroll
+          for (int slab = 0; slab < Sh::kSlabs; ++slab)
+            *reinterpret_cast<uint4 *>(at_key + slab * slab_bytes(keys)) = make_uint4(0, 0, 0, 0);
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -1171,23 +1196,34 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-// Map of a cache [page, token, head, D]: box of 64 elements of up to 64
-// tokens of one page and head.
-bool encode_cache(CUtensorMap *map, const sv_attention_t &a, const void *base, int64_t page,
+// The cache as a tensor map.  A box is 64 columns (128 bytes) of up to 64
+// tokens of one page and head, or, paired, both halves of their rows: columns,
+// tokens of a group of eight, halves, groups, page, where heads share a
+// dimension with the halves (head2 = 2: a token's heads lie side by side) or
+// with the groups (head3: a head's tokens lie side by side).
+bool encode_cache(CUtensorMap *map, const TcArgs &args, const void *base, int64_t page,
                   int64_t token, int64_t head) {
-  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(a.D), static_cast<cuuint64_t>(a.Hkv),
-                              static_cast<cuuint64_t>(a.page_size),
-                              static_cast<cuuint64_t>(a.num_pages)};
-  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(head) * 2,
-                                 static_cast<cuuint64_t>(token) * 2,
-                                 static_cast<cuuint64_t>(page) * 2};
-  const cuuint32_t box[4] = {64, 1, static_cast<cuuint32_t>(a.page_size < 64 ? a.page_size : 64),
-                             1};
-  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  const sv_attention_t &a = args.a;
+  const cuuint32_t keys = a.page_size < 64 ? a.page_size : 64;
+  auto bytes = [](int64_t elements) { return static_cast<cuuint64_t>(elements) * 2; };
+  const cuuint64_t heads = static_cast<cuuint64_t>(a.Hkv);
+  const cuuint64_t groups = static_cast<cuuint64_t>(a.page_size / 8);
+  const cuuint64_t pages = static_cast<cuuint64_t>(a.num_pages);
+  const cuuint64_t dims4[4] = {static_cast<cuuint64_t>(a.D), heads,
+                               static_cast<cuuint64_t>(a.page_size), pages};
+  const cuuint64_t strides4[3] = {bytes(head), bytes(token), bytes(page)};
+  const cuuint32_t box4[4] = {64, 1, keys, 1};
+  const cuuint64_t dims5[5] = {64, 8, args.head2 ? 2 * heads : 2,
+                               args.head3 ? heads * groups : groups, pages};
+  const cuuint64_t strides5[4] = {bytes(token), bytes(64), bytes(8 * token), bytes(page)};
+  const cuuint32_t box5[5] = {64, 8, 2, keys / 8, 1};
+  const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  const bool five = args.paired != 0;
   return encode_fn()(map,
                      a.dtype == SV_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                         : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
-                     4, const_cast<void *>(base), dims, strides, box, estr,
+                     five ? 5 : 4, const_cast<void *>(base), five ? dims5 : dims4,
+                     five ? strides5 : strides4, five ? box5 : box4, estr,
                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -1235,11 +1271,24 @@ int launch_attention_tc(const spec_target &h, const sv_attention_t &a, cudaStrea
     return kNotTaken;
   CUtensorMap tmK, tmV;
   if (!encode_fn()) return SV_ERR_CUDA;
-  if (!encode_cache(&tmK, a, a.k_cache, a.kc_page, a.kc_token, a.kc_head) ||
-      !encode_cache(&tmV, a, a.v_cache, a.vc_page, a.vc_token, a.vc_head))
-    return kNotTaken;
   TcArgs args{};
   args.a = a;
+  if (a.D == 128 && a.page_size <= kPairedPage) {
+    auto side_by_side = [&](int64_t head) { return head == a.D; };
+    auto in_turn = [&](int64_t token, int64_t head) { return head == token * a.page_size; };
+    if (a.Hkv == 1) {
+      args.paired = 1;
+    } else if (side_by_side(a.kc_head) && side_by_side(a.vc_head)) {
+      args.paired = 1;
+      args.head2 = 2;
+    } else if (in_turn(a.kc_token, a.kc_head) && in_turn(a.vc_token, a.vc_head)) {
+      args.paired = 1;
+      args.head3 = a.page_size / 8;
+    }
+  }
+  if (!encode_cache(&tmK, args, a.k_cache, a.kc_page, a.kc_token, a.kc_head) ||
+      !encode_cache(&tmV, args, a.v_cache, a.vc_page, a.vc_token, a.vc_head))
+    return kNotTaken;
   args.scratch = h.scratch;
   args.status = h.status;
   args.wait_limit_ns = h.wait_limit_ns;

@@ -375,6 +375,47 @@ def test_attention_strides(ops, dtype, heads_first, fused):
                     heads_first=heads_first, fused=fused)
 
 
+@pytest.mark.parametrize("heads_first", [False, True])
+@pytest.mark.parametrize("page", [8, 16, 32, 64, 128])
+@pytest.mark.parametrize("hkv", [1, 3])
+def test_attention_heads_of_128(ops, heads_first, page, hkv):
+    """Rows of two 128-byte halves, in both orders of the cache; one and many
+    rows, ends inside a page and on its edge."""
+    check_attention(ops, gen(page), "bf16", 2 * hkv, hkv, 128, page, [1, 5, 150, 2],
+                    [page, 517, 150, 2 * page + 1], heads_first=heads_first)
+
+
+@pytest.mark.parametrize("n", [6, 200])
+def test_attention_heads_of_128_masked_values_do_not_count(ops, n):
+    def spoil(kc, vc, table, ks, vs):
+        kv = vs[0].shape[0]
+        at = kv - 2
+        pg, off = int(table[0, at // 16]), at % 16
+        vs[0][at, 0, 3] = vc[pg, off, 0, 3] = float("inf")
+        vs[0][at, 1, 100] = vc[pg, off, 1, 100] = float("nan")
+        at = kv - 1
+        pg, off = int(table[0, at // 16]), at % 16
+        ks[0][at, 1, 70] = float("nan")
+        kc[pg, off, 1, 70] = float("nan")
+    check_attention(ops, gen(n), "fp16", 4, 2, 128, 16, [n, 3], [n + 300, 70], spoil=spoil)
+
+
+@pytest.mark.parametrize("page", [8, 16, 32])
+def test_attention_cache_orders_agree(ops, page):
+    """K and V of different orders give what equal orders give."""
+    g = gen(page)
+    news, lens, hkv = [5, 140], [700, 333], 2
+    kc, vc, table, _, _ = build_cache(g, lens, page, hkv, 128, torch.bfloat16)
+    q = randn(g, (sum(news), 3 * hkv, 128), torch.bfloat16)
+    qs = torch.tensor([0, 5, 145], dtype=torch.int32, device="cuda")
+    kl = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    turn = lambda c: c.transpose(1, 2).contiguous().transpose(1, 2)
+    want = ops.attention(q, kc, vc, table, qs, kl)
+    for k, v in ((kc, turn(vc)), (turn(kc), vc), (turn(kc), turn(vc))):
+        assert torch.equal(ops.attention(q, k, v, table, qs, kl), want)
+    assert torch.isfinite(want).all() and ops.status() == sv.SV_OK
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
 @pytest.mark.parametrize("n", [6, 200])
 def test_attention_masked_values_do_not_count(ops, dtype, n):
