@@ -20,8 +20,8 @@
  * the legacy default stream), returns without synchronising, allocates
  * nothing and can be captured in a CUDA graph.  A handle belongs to the
  * device that was current when it was created and owns scratch that the
- * product and the attention use, so two calls on one handle that may overlap
- * on the GPU (on different streams) race; use one handle for each.  Outputs
+ * attention uses, so two calls on one handle that may overlap on the GPU (on
+ * different streams) race; use one handle for each.  Outputs
  * are the same bit for bit when a call is repeated on the same inputs.
  * Strides are in elements; the innermost dimension is always dense.
  */
@@ -44,7 +44,7 @@ extern "C" {
 typedef struct spec_target spec_target_t; /* opaque handle */
 
 /* Creates a handle on the current CUDA device and allocates its scratch (a
- * fixed size, about 45 MB).  Errors: SV_ERR_ARG (null pointer), SV_ERR_ARCH,
+ * fixed size, 44 MiB).  Errors: SV_ERR_ARG (null pointer), SV_ERR_ARCH,
  * SV_ERR_CUDA.  On error *out is set to NULL. */
 int spec_target_create(spec_target_t **out);
 
@@ -83,7 +83,7 @@ int spec_target_rms_norm(spec_target_t *h, const void *x, int64_t x_stride,
                          void *stream);
 
 /* The same norm with y in 8 bits: per group of columns
- *   scale = max(max|y|, 1e-30) / 448,   out8 = E4M3(y / scale)
+ *   scale = max(max|y|, 1e-30) / 448,   out8 = E4M3(y * (1 / scale))
  * rounded to nearest even from the fp32 y.
  *   group   SV_SCALE_BLOCK: a scale for every 128 columns (the last group
  *           may be shorter), scale is fp32 [rows, ceil(d / 128)], what

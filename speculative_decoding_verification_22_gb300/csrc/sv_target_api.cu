@@ -8,7 +8,7 @@
 
 namespace {
 
-// Scratch of the product's and the attention's partial results.
+// Scratch of the attention's partial results.
 constexpr size_t kScratchBytes = size_t(44) << 20;
 
 size_t elem_size(int32_t dtype) { return dtype == SV_FP32 ? 4 : 2; }
