@@ -25,7 +25,9 @@
 // 1.6 us from its slot's being freed to its use, and the four blocks of 48 KB
 // that fit in shared memory are in flight for that long.  With the adding it
 // is 189: tensor memory holds two blocks, and a block's products, hand-over
-// and reading follow one another.
+// and reading follow one another.  So the second limit stays when the first is
+// lifted: pairs of CTAs that share W's blocks (six of 32 KB in flight) took 214
+// us, and handing over half a block's columns at a time 270.
 #include <cudaTypedefs.h>
 
 #include "sv_target.cuh"
