@@ -27,13 +27,12 @@
 //    handle's scratch and a second launch joins them in a fixed order.  The
 //    lengths are read on the device: no host plan, a graph replays with new
 //    ones.
-//  * Warps 0-3 and 4-7: softmax of the two slots, one row a thread; warp 8:
-//    TMA into a ring of 160 KB; warp 9: the products; warp 10
-//    hands out the items; warp 11 completes the warpgroup that gives its
-//    registers to the others.
+//  * Warps 0-3 and 4-7: softmax of the two slots, one row a thread; warp 8,
+//    and warp 11 for the V of narrow tiles: TMA into a ring of 160 KB; warp 9:
+//    the products; warp 10 hands out the items.
 //
 // What bounds it.  Cached bytes, for few rows a head: 64 single tokens over 2048
-// to 8192 in 212 us, 6.4 TB/s.  Products, for many: 4096 tokens over 16384 in
+// to 8192 in 211 us, 6.4 TB/s.  Products, for many: 4096 tokens over 16384 in
 // 650 us, 1.48 PFLOP/s, where the scores' product reads 8 KB of shared memory
 // in each of its 64 cycles, all that there is, beside the copies that arrive.
 // Latency, for short calls and short sequences: 5 tokens over 1000 in 14.4 us
@@ -64,9 +63,10 @@ constexpr int kThreads = 384;
 constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
 constexpr int kSoftmaxWarps = 8;
 constexpr int kRingBytes = 160 * 1024;
-// Pages up to this size come with both 128-byte halves of a row in one box: 64
-// single tokens over 8192 in pages of 16 take 207 us against 242, as the TMA
-// takes about 55 ns a box whatever it holds; in pages of 32 202 against 200.
+// Pages up to this size come with both 128-byte halves of a row in one box, as
+// a warp takes about 55 ns to issue one whatever it holds: 4096 tokens over 16384
+// in pages of 8 and 16 take 749 and 682 us against 1123 and 766, 64 single tokens
+// over 8192 209 and 207 against 260 and 209; pages of 32 and more gain nothing.
 constexpr int kPairedPage = 16;
 constexpr int kMaxSlots = 10;
 constexpr uint64_t kCleanupLimitNs = 2000000000ull;
@@ -103,7 +103,7 @@ struct Ctl {
   uint32_t tmem;
   int abort;
   int slow;           // a softmax warp is in attend_row: waits go on
-  int issued, consumed;
+  int issued[2], consumed;  // slots of the ring
   int start_b;
   int64_t start_off, start_per;
   int64_t scan[kThreads / 32];
@@ -410,12 +410,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (tid == 0) {
     for (int i = 0; i < Sh::kSlots; ++i) {
-      mbar_init(smem_u32(&ctl->full[i]), 1);
+      mbar_init(smem_u32(&ctl->full[i]), 2);
       mbar_init(smem_u32(&ctl->empty[i]), 1);
     }
     for (int i = 0; i < kRuns; ++i) {
       mbar_init(smem_u32(&ctl->run_full[i]), 1);
-      mbar_init(smem_u32(&ctl->run_empty[i]), kSoftmaxWarps + 2);
+      mbar_init(smem_u32(&ctl->run_empty[i]), kSoftmaxWarps + 3);
     }
     mbar_init(smem_u32(&ctl->q_ready), kSoftmaxWarps);
     for (int w = 0; w < 2; ++w) {
@@ -426,7 +426,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(smem_u32(&ctl->x_full), kSoftmaxWarps / 2);
     mbar_init(smem_u32(&ctl->x_free), kSoftmaxWarps / 2);
     mbar_init(smem_u32(&ctl->teardown), 1);
-    ctl->abort = ctl->slow = ctl->issued = ctl->consumed = 0;
+    ctl->abort = ctl->slow = ctl->issued[0] = ctl->issued[1] = ctl->consumed = 0;
     ctl->start_b = -1;
     mbar_fence_init();
   }
@@ -852,14 +852,32 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         more = it.next();
       }
-    } else if (warp == 8) {
+    } else if (warp == 8 || warp == 11) {
       // ---------------- TMA ----------------
+      // Warp 8 brings K, warp 11 a narrow tile's V (64 single tokens over 8192 in
+      // pages of 8: 208 us against 249 by one warp; heads of 64 in pages of 16: 145
+      // against 166).  A wide tile has twice the time: its V comes by warp 8 too
+      // (a chunk 1% slower by two).
+      const int v = warp == 8 ? 0 : 1;
       const int page_keys = min(64, a.page_size);
       const bool paired = Sh::kSlabs > 1 && args.paired;
-      const uint32_t box_bytes = static_cast<uint32_t>(page_keys) * (paired ? 128u * Sh::kSlabs : 128u);
+      const uint32_t box_bytes =
+          static_cast<uint32_t>(page_keys) * (paired ? 128u * Sh::kSlabs : 128u);
       int slot = 0, issued = 0;
       uint32_t phase = 0;
       bool ok = true;
+      // Both warps wait for every slot, their own or not, so that neither is ever
+      // a whole round of the ring ahead.
+      auto slot_free = [&]() {
+        return ok = wait_warp(ctl, &ctl->empty[slot], phase ^ 1, args.wait_limit_ns, args.status);
+      };
+      auto next_slot = [&]() {
+        ++issued;
+        if (++slot == Sh::kSlots) {
+          slot = 0;
+          phase ^= 1;
+        }
+      };
       while (ok && take()) {
         const Run &it = ctl->run[(runs - 1) % kRuns];
         const int n = it.n, tile0 = it.tile0, kv = it.s.kv, head = it.h;
@@ -891,37 +909,33 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (mine && static_cast<uint32_t>(page) >= a.num_pages)
             set_status(args.status, SV_ERR_CACHE);
           const int in_page = (k0 + key_in) & (a.page_size - 1);
-          for (int v = 0; v < (wide ? 2 : 1); ++v) {
-            if (!(ok = wait_warp(ctl, &ctl->empty[slot], phase ^ 1, args.wait_limit_ns,
-                                 args.status)))
-              break;
+          for (int x = 0; x < (wide ? 2 : 1); ++x) {
+            if (!slot_free()) break;
             const uint32_t full = smem_u32(&ctl->full[slot]);
-            if (lane == 0) mbar_arrive_expect_tx(full, wide ? bytes : 2 * bytes);
-            __syncwarp();
-            const uint32_t at = ring + slot * Sh::kSlotBytes + offset;
-            if (mine && paired) {
-              const int group = head3 + (in_page >> 3);
-              tma_load_5d(at, v ? &tmV : &tmK, 0, 0, head2, group, page, full, policy);
-              if (!wide)
-                tma_load_5d(at + Sh::kSlotBytes / 2, &tmV, 0, 0, head2, group, page, full, policy);
-            } else if (mine) {
-              tma_load_4d(at, v ? &tmV : &tmK, slab * 64, head, in_page, page, full, policy);
-              if (!wide)
-                tma_load_4d(at + Sh::kSlotBytes / 2, &tmV, slab * 64, head, in_page, page, full,
-                            policy);
+            const bool second = wide ? x == 1 : v == 1;  // V, not K
+            const CUtensorMap *map = second ? &tmV : &tmK;
+            // two arrivals a slot: of the two warps, or of the one that fills it
+            if (lane == 0 && !(wide && v)) {
+              mbar_arrive_expect_tx(full, bytes);
+              if (wide) mbar_arrive(full);
             }
             __syncwarp();
-            ++issued;
-            if (++slot == Sh::kSlots) {
-              slot = 0;
-              phase ^= 1;
+            const uint32_t at =
+                ring + slot * Sh::kSlotBytes + offset + (wide || !v ? 0 : Sh::kSlotBytes / 2);
+            if (mine && !(wide && v)) {
+              if (paired)
+                tma_load_5d(at, map, 0, 0, head2, head3 + (in_page >> 3), page, full, policy);
+              else
+                tma_load_4d(at, map, slab * 64, head, in_page, page, full, policy);
             }
+            __syncwarp();
+            next_slot();
           }
           page = next;
         }
         give_back();
       }
-      if (lane == 0) ctl->issued = issued;
+      if (lane == 0) ctl->issued[v] = issued;
     } else if (warp == 9) {
       // ---------------- products ----------------
       constexpr uint32_t idesc_o = idesc_16(kBf16, kRows, DPAD, true);
@@ -1079,11 +1093,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   if (warp == 8 && lane == 0) {
-    // only after an abort can copies still be in flight
+    // only after an abort can copies still be in flight (and a slot may then
+    // have its K or its V alone, for which one limit is waited)
     const int never = 0;
-    for (int p = ctl->consumed; p < ctl->issued; ++p)
-      mbar_wait(smem_u32(&ctl->full[p % Sh::kSlots]),
-                static_cast<uint32_t>((p / Sh::kSlots) & 1), kCleanupLimitNs, &never);
+    const int issued = max(ctl->issued[0], ctl->issued[1]);
+    for (int p = ctl->consumed; p < issued; ++p)
+      if (!mbar_wait(smem_u32(&ctl->full[p % Sh::kSlots]),
+                     static_cast<uint32_t>((p / Sh::kSlots) & 1), kCleanupLimitNs, &never))
+        break;
   }
   __syncthreads();
   if (warp == 9) {
