@@ -993,8 +993,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (elect_one()) {
 #pragma unroll
           for (int e = 0; e < keys / 16; ++e)
-            umma_16_ta(tmem + 256 + w * 128, tmem + w * 128 + e * 8, v + e * (2 * group_bytes >> 4), idesc_o,
-                       more || e > 0);
+            umma_16_ta(tmem + 256 + w * 128, tmem + w * 128 + e * 8,
+                       v + e * (2 * group_bytes >> 4), idesc_o, more || e > 0);
           if (last) umma_commit(smem_u32(&ctl->empty[s]));
         }
         __syncwarp();
