@@ -67,6 +67,15 @@ def test_norm_e4m3(ops, dtype, group, rows, d):
     assert not q[0].float().any()
 
 
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("rows,d", [(3, 127), (4, 129), (200, 2047), (2, 4097), (3, 8191),
+                                    (2, 8193), (2, 16383), (2, 16385)])
+def test_norm_odd_widths(ops, dtype, rows, d):
+    test_norm(ops, dtype, rows, d)
+    for group in (128, 0):
+        test_norm_e4m3(ops, dtype, group, rows, d)
+
+
 def test_norm_strides_in_place_and_unaligned(ops):
     g = gen(5)
     big = randn(g, (9, 3 * 512 + 8), torch.bfloat16)
