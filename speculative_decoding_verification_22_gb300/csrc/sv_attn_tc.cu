@@ -866,8 +866,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       int slot = 0, issued = 0;
       uint32_t phase = 0;
       bool ok = true;
-      // Both warps wait for every slot, their own or not, so that neither is ever
-      // a whole round of the ring ahead.
+      // Both warps wait for every slot and arrive at every slot, their own or not:
+      // it is full only after both, so neither is ever a whole round of the ring
+      // behind, where a wait by parity would take one round for another.
       auto slot_free = [&]() {
         return ok = wait_warp(ctl, &ctl->empty[slot], phase ^ 1, args.wait_limit_ns, args.status);
       };
@@ -882,6 +883,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const Run &it = ctl->run[(runs - 1) % kRuns];
         const int n = it.n, tile0 = it.tile0, kv = it.s.kv, head = it.h;
         const bool wide = it.wide;
+        const bool brings = !(wide && v);  // a wide tile's V comes by warp 8
         // K and V that are not read again need not stay in L2: 64 single tokens
         // over 8192 in 247 us against 253, eight trees of 65 in 62 against 68; a
         // prompt's chunk, which comes back to them, in 723 against 653
@@ -898,7 +900,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int head2 = head * args.head2, head3 = head * args.head3;
         auto page_of = [&](int t) {
           const int key = (tile0 + t) * keys + key_in;
-          return t < n && key_in < keys && key < kv ? pages[key >> args.pow_page] : 0;
+          return brings && t < n && key_in < keys && key < kv ? pages[key >> args.pow_page] : 0;
         };
         int page = page_of(0);
         for (int t = 0; t < n && ok; ++t) {
@@ -914,15 +916,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t full = smem_u32(&ctl->full[slot]);
             const bool second = wide ? x == 1 : v == 1;  // V, not K
             const CUtensorMap *map = second ? &tmV : &tmK;
-            // two arrivals a slot: of the two warps, or of the one that fills it
-            if (lane == 0 && !(wide && v)) {
-              mbar_arrive_expect_tx(full, bytes);
-              if (wide) mbar_arrive(full);
+            if (lane == 0) {
+              if (brings)
+                mbar_arrive_expect_tx(full, bytes);
+              else
+                mbar_arrive(full);
             }
             __syncwarp();
             const uint32_t at =
                 ring + slot * Sh::kSlotBytes + offset + (wide || !v ? 0 : Sh::kSlotBytes / 2);
-            if (mine && !(wide && v)) {
+            if (mine && brings) {
               if (paired)
                 tma_load_5d(at, map, 0, 0, head2, head3 + (in_page >> 3), page, full, policy);
               else
