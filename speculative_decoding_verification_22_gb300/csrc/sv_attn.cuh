@@ -53,10 +53,12 @@ __device__ __forceinline__ bool tree_sees(const int32_t *row, int words, int jj)
 // with a running maximum and sum: each lane forms one key's score, the lanes
 // agree on the maximum, and the values are added up with the lanes spread
 // over the head's elements.  A key that is not seen is never multiplied, so
-// what the cache holds there does not count.
+// what the cache holds there does not count.  It writes the elements [d0, d1) of
+// the row, and the lse with element 0.
 template <class T>
 __device__ __noinline__ void attend_row(const sv_attention_t &a, const SeqGeom &s, int b, int i,
-                                        int head, int lane, int *status) {
+                                        int head, int lane, int *status, int d0 = 0,
+                                        int d1 = SV_MAX_HEAD_DIM) {
   const int t = s.t0 + i;
   const T *q = static_cast<const T *>(a.q) + t * a.q_token + head * a.q_head;
   const int kvh = head / (a.Hq / a.Hkv);
@@ -116,9 +118,9 @@ __device__ __noinline__ void attend_row(const sv_attention_t &a, const SeqGeom &
   T *o = static_cast<T *>(a.out) + t * a.o_token + head * a.o_head;
 #pragma unroll
   for (int e = 0; e < kPer; ++e)
-    if (lane + 32 * e < a.D)
+    if (lane + 32 * e < a.D && lane + 32 * e >= d0 && lane + 32 * e < d1)
       o[lane + 32 * e] = from_float<T>(l != 0.0f ? acc[e] * inv : 0.0f);
-  if (a.lse && lane == 0)
+  if (a.lse && lane == 0 && d0 == 0)
     a.lse[static_cast<int64_t>(t) * a.Hq + head] = l != 0.0f ? m + logf(l) : -INFINITY;
 }
 

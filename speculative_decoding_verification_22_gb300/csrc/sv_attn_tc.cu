@@ -1193,12 +1193,16 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
         acc[e] = sum != 0.0f ? acc[e] * inv : 0.0f;
         fine &= fabsf(acc[e]) < INFINITY;
       }
-      store_row<T, kJoinElems>(a, static_cast<T *>(a.out) + t * a.o_token + head * a.o_head, d0,
-                               acc, fast_output(a));
-      if (a.lse && d0 == 0)
-        a.lse[t * a.Hq + head] =
-            sum != 0.0f ? top * (args.c * 0.69314718055994531f) + logf(sum) : -INFINITY;
+      if (fine) {
+        store_row<T, kJoinElems>(a, static_cast<T *>(a.out) + t * a.o_token + head * a.o_head,
+                                 d0, acc, fast_output(a));
+        if (a.lse && d0 == 0)
+          a.lse[t * a.Hq + head] =
+              sum != 0.0f ? top * (args.c * 0.69314718055994531f) + logf(sum) : -INFINITY;
+      }
     }
+    // Other warps, at any time, have the row's other elements: this one takes
+    // its own again and no more.
     unsigned again = __ballot_sync(0xffffffffu, !fine);
     if (again) {
       bool bad;
@@ -1207,7 +1211,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
         const int src = __ffs(again) - 1;
         again &= again - 1;
         attend_row<T>(a, s, b, __shfl_sync(0xffffffffu, tok, src),
-                      __shfl_sync(0xffffffffu, head, src), lane, args.status);
+                      __shfl_sync(0xffffffffu, head, src), lane, args.status, d0,
+                      d0 + kJoinElems);
       }
     }
   }
