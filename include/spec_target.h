@@ -216,7 +216,9 @@ int spec_target_rope_append(spec_target_t *h, const sv_rope_append_t *a, void *s
  * SV_ERR_SHAPE, SV_ERR_ALIGN, SV_ERR_CUDA.  Through the status word:
  * SV_ERR_CACHE for a sequence whose kv_len or token range is out of bounds
  * (its outputs are o = 0, lse = -inf, as far as its tokens are known) or
- * that uses a page outside the cache (read as zeros). */
+ * with a page outside the cache of which a token sees a key (read as zeros).
+ * Entries of pages that no token sees, as those below the window, may hold
+ * anything. */
 typedef struct {
   const void *q;
   const void *k_cache, *v_cache;

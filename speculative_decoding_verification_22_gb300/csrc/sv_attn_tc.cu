@@ -343,6 +343,27 @@ __device__ __forceinline__ uint32_t tree_bits(const int32_t *row, int words, int
   };
   return __funnelshift_r(word(w), word(w + 1), s & 31);
 }
+// Whether a row of the run's item sees a key of [k0, k1).  Asked only where the
+// page of these keys is not there, as tiles and pages reach beyond what is seen:
+// below a window, and new tokens that no row of a tree has its bit for.
+__device__ __forceinline__ bool item_sees(const TcArgs &args, const Run &it, int k0, int k1) {
+  const sv_attention_t &a = args.a;
+  const int G = a.Hq / a.Hkv;
+  const int first = group_div(args, G, it.r0), last = group_div(args, G, it.r0 + it.rows - 1);
+  int lo, hi, x;
+  key_range(a, it.s, first, lo, x);
+  key_range(a, it.s, last, x, hi);
+  k0 = max(k0, lo);
+  k1 = min(k1, hi);
+  if (k0 >= k1) return false;
+  if (!a.tree_mask || k0 < it.s.ctx) return true;
+  for (int i = first; i <= last; ++i) {
+    const int32_t *row = a.tree_mask + static_cast<int64_t>(it.s.t0 + i) * a.tree_words;
+    for (int k = k0; k < k1; ++k)
+      if (tree_sees(row, a.tree_words, k - it.s.ctx)) return true;
+  }
+  return false;
+}
 // Bits i of [lo, hi) of a group of 32 keys.
 __device__ __forceinline__ uint32_t range_bits(int lo, int hi) {
   const uint32_t below = hi >= 32 ? 0xffffffffu : hi <= 0 ? 0u : (1u << hi) - 1u;
@@ -908,7 +929,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int k0 = (tile0 + t) * keys;
           const bool mine = key_in < keys && k0 + key_in < kv;
           const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, mine)) * box_bytes;
-          if (mine && static_cast<uint32_t>(page) >= a.num_pages)
+          // (a page that is not there is loaded as zeros)
+          if (mine && static_cast<uint32_t>(page) >= a.num_pages &&
+              item_sees(args, it, k0 + key_in, k0 + key_in + page_keys))
             set_status(args.status, SV_ERR_CACHE);
           const int in_page = (k0 + key_in) & (a.page_size - 1);
           for (int x = 0; x < (wide ? 2 : 1); ++x) {

@@ -6,8 +6,8 @@ import pytest
 import torch
 
 import speculative_decoding_verification_22_gb300 as sv
-from target_common import (attention_bound, attention_ref, build_cache, gen, randn, score_error,
-                           within)
+from target_common import (DTYPES, attention_bound, attention_ref, build_cache, gen, randn,
+                           score_error, within)
 
 pytestmark = pytest.mark.gpu
 
@@ -80,3 +80,54 @@ def test_attention_cut_rows_with_some_columns_not_finite(ops, dtype, n, kv):
         assert torch.equal(out.view(torch.int16), again[0].view(torch.int16))
         assert torch.equal(lse.view(torch.int32), again[1].view(torch.int32))
     assert ops.status() == sv.SV_OK
+
+
+# ---- attention: pages that are not there ----------------------------------------------
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("page", [8, 16, 32])
+@pytest.mark.parametrize("news,lens,window", [
+    ([1], [1000], 37), ([3, 300], [700, 2000], 100),  # few rows; blocks of many
+    ([5], [30000], 20001), ([90], [4000], 130)])      # a cut item; one wide item
+def test_attention_window_over_freed_pages(ops, dtype, page, news, lens, window):
+    """Pages that lie wholly below the window may be gone from the table; the
+    last one that is seen may not."""
+    g = gen(page + window)
+    dt = DTYPES[dtype]
+    kc, vc, table, ks, vs = build_cache(g, lens, page, 2, 128, dt)
+    q = randn(g, (sum(news), 8, 128), dt)
+    seen = [max(0, kv - n + 1 - window) // page for n, kv in zip(news, lens)]
+    for b, first in enumerate(seen):
+        table[b, :first] = -1
+    out = ops.attention(q, kc, vc, table, starts(news), int32(lens), window=window)
+    assert ops.status() == sv.SV_OK
+    o, mag, _, big = attention_ref(q, ks, vs, news, 128 ** -0.5, window)
+    within(out, o, attention_bound(o, mag, big, 128, dt))
+    table[-1, seen[-1]] = -1
+    ops.attention(q, kc, vc, table, starts(news), int32(lens), window=window)
+    assert ops.status() == sv.SV_ERR_CACHE
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_attention_tree_over_pages_that_no_node_sees(ops, dtype):
+    """A tree padded to 40 nodes of which 17 are live: the others' pages may be
+    missing, those of live nodes may not."""
+    dt = DTYPES[dtype]
+    g = gen(3)
+    n, live, kv, page = 40, 17, 140, 8
+    see = torch.zeros(n, n, dtype=torch.bool, device="cuda")
+    see[:live, :live] = torch.ones(live, live, device="cuda").tril().bool()
+    bits = torch.nn.functional.pad(see, (0, 24)).view(n, 2, 32).long()
+    bits = (bits << torch.arange(32, device="cuda")).sum(-1)
+    mask = torch.where(bits >= 2 ** 31, bits - 2 ** 32, bits).int().contiguous()
+    kc, vc, table, ks, vs = build_cache(g, [kv], page, 2, 64, dt)
+    q = randn(g, (n, 4, 64), dt)
+    end = kv - n + live
+    table[0, -(-end // page):] = -1
+    out = ops.attention(q, kc, vc, table, starts([n]), int32([kv]), tree_mask=mask)
+    assert ops.status() == sv.SV_OK
+    o, mag, _, big = attention_ref(q, ks, vs, [n], 0.125, see=[see])
+    within(out, o, attention_bound(o, mag, big, 64, dt))
+    table[0, (end - 1) // page] = -1
+    ops.attention(q, kc, vc, table, starts([n]), int32([kv]), tree_mask=mask)
+    assert ops.status() == sv.SV_ERR_CACHE
