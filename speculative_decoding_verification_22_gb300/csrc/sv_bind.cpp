@@ -54,6 +54,11 @@ int code_of(at::ScalarType t, const char *what) {
   }
 }
 
+// E4M3 values, or their bytes.
+bool e4m3(const Tensor &t) {
+  return t.scalar_type() == at::kFloat8_e4m3fn || t.scalar_type() == at::kByte;
+}
+
 long long integer(PyObject *o) {
   const long long v = PyLong_AsLongLong(o);
   if (v == -1 && PyErr_Occurred()) throw Raised();
@@ -203,9 +208,9 @@ PyObject *norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
     if (given(a[6])) {
       const Tensor &o = tensor(a[6], "rms_norm: out");
       if (quant)
-        need(o.dim() == 2 && o.size(0) == rows && o.size(1) == d && o.element_size() == 1 &&
+        need(o.dim() == 2 && o.size(0) == rows && o.size(1) == d && e4m3(o) &&
                  o.is_contiguous() && o.is_cuda(),
-             "rms_norm_fp8: out must be dense bytes of x's shape");
+             "rms_norm_fp8: out must be dense float8_e4m3fn (or uint8) of x's shape");
       else
         need(like_x(o), "rms_norm: out must have x's shape and type");
       out = o.data_ptr();
@@ -255,7 +260,7 @@ PyObject *matmul(PyObject *, PyObject *const *a, Py_ssize_t n) {
          "matmul_fp8: a8 [M, K] and w8 [N, K]");
     const int64_t M = x.size(0), K = x.size(1), N = w.size(0);
     const int64_t kb = (K + SV_SCALE_BLOCK - 1) / SV_SCALE_BLOCK;
-    need(x.element_size() == 1 && w.element_size() == 1, "matmul_fp8: a8 and w8 hold E4M3 bytes");
+    need(e4m3(x) && e4m3(w), "matmul_fp8: a8 and w8 must be float8_e4m3fn (or its bytes, uint8)");
     need(sx.scalar_type() == at::kFloat && sw.scalar_type() == at::kFloat && sx.dim() == 2 &&
              sw.dim() == 2 && sx.size(0) == M && sx.size(1) == kb &&
              sw.size(0) == (N + SV_SCALE_BLOCK - 1) / SV_SCALE_BLOCK && sw.size(1) == kb,

@@ -128,8 +128,9 @@ class TargetOps:
 
     def matmul_fp8(self, a8, a_scale, w8, w_scale, out_dtype=torch.bfloat16, out=None,
                    stream=None):
-        """a8 [M, K] and w8 [N, K] in E4M3 with scales [M, ceil(K/128)] and
-        [ceil(N/128), ceil(K/128)]: the [M, N] product a8 w8^T."""
+        """a8 [M, K] and w8 [N, K] in E4M3 (float8_e4m3fn, or its bytes as uint8)
+        with scales [M, ceil(K/128)] and [ceil(N/128), ceil(K/128)]: the [M, N]
+        product a8 w8^T."""
         code = _CODES.get(out_dtype)
         if code is None:
             raise ValueError("matmul_fp8: out must be bfloat16, float16 or float32")

@@ -131,3 +131,15 @@ def test_attention_tree_over_pages_that_no_node_sees(ops, dtype):
     table[0, (end - 1) // page] = -1
     ops.attention(q, kc, vc, table, starts([n]), int32([kv]), tree_mask=mask)
     assert ops.status() == sv.SV_ERR_CACHE
+
+
+# ---- refusals -------------------------------------------------------------------------
+
+def test_norm_into_eight_bits_that_are_not_e4m3_is_refused(ops):
+    x, w = torch.ones(4, 128, device="cuda"), torch.ones(128, device="cuda")
+    for dtype in (torch.float8_e5m2, torch.int8, torch.bool):
+        with pytest.raises(ValueError, match="e4m3"):
+            ops.rms_norm_fp8(x, w, out=torch.zeros(4, 128, device="cuda").to(dtype))
+    want = ops.rms_norm_fp8(x, w)[0]
+    out = torch.empty(4, 128, dtype=torch.uint8, device="cuda")
+    assert torch.equal(ops.rms_norm_fp8(x, w, out=out)[0], want.view(torch.uint8))

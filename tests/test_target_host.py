@@ -242,3 +242,17 @@ def test_every_entry_point_is_bound(lib):
         f = getattr(lib, n)
         assert f.argtypes is not None, n
         assert f.restype in (ctypes.c_int, None), n
+
+
+@pytest.mark.parametrize("dtype", [torch.float8_e5m2, torch.int8, torch.bool])
+def test_eight_bits_that_are_not_e4m3_are_refused(dtype):
+    ops = sv.TargetOps.__new__(sv.TargetOps)  # no GPU, no handle
+    ops.h, ops._lib = None, None
+    good, bad = (torch.zeros(128, 128).to(t) for t in (torch.float8_e4m3fn, dtype))
+    s, one = torch.ones(128, 1), torch.ones(1, 1)
+    for a, w in ((good, bad), (bad, good)):
+        with pytest.raises(ValueError, match="must be float8_e4m3fn"):
+            ops.matmul_fp8(a, s, w, one)
+    for a in (good, good.view(torch.uint8)):  # these come to the check of the device
+        with pytest.raises(ValueError, match="on the GPU"):
+            ops.matmul_fp8(a, s, good, one)
