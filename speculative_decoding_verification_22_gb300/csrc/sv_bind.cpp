@@ -27,6 +27,7 @@ using at::Tensor;
 
 PyObject *g_error = nullptr;      // SpecVerifyError(code, what)
 PyObject *g_raw = nullptr;        // "_raw": the handle's address, or None
+PyObject *g_index = nullptr;      // "_index": the number of the handle's device
 PyObject *g_stream = nullptr;     // "cuda_stream"
 
 struct Bad : std::runtime_error {
@@ -78,6 +79,30 @@ spec_target_t *handle(PyObject *self) {
   Py_DECREF(o);
   return h;
 }
+
+// The device of the handle, the only one whose memory its kernels may be given.
+class Device {
+ public:
+  explicit Device(PyObject *self) : self_(self) {}
+  bool has(const Tensor &t) {
+    if (!t.is_cuda()) return false;
+    if (index_ < 0) {
+      PyObject *o = PyObject_GetAttr(self_, g_index);
+      if (!o) throw Raised();
+      index_ = integer(o);
+      Py_DECREF(o);
+    }
+    return t.get_device() == index_;
+  }
+  template <class... More>
+  bool has(const Tensor &t, const More &...more) {
+    return has(t) && has(more...);
+  }
+
+ private:
+  PyObject *self_;
+  long long index_ = -1;
+};
 
 // The stream of a call: the one given (an object with cuda_stream, or its
 // number), else the current one of the tensor's device.  While it lives the
@@ -171,12 +196,13 @@ PyObject *norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
          "rms_norm: x [rows, d] and weight [d]");
     need(w.scalar_type() == dt && w.is_contiguous(),
          "rms_norm: weight must be dense and of x's type");
-    need(x.is_cuda() && w.is_cuda(), "rms_norm: tensors must be on the GPU");
+    Device device(a[0]);
+    need(device.has(x, w), "rms_norm: tensors must be on the GPU of the handle");
     const Stream stream(a[9], x);
     const int64_t rows = x.size(0), d = x.size(1), xs = row_stride(x, "x");
     auto like_x = [&](const Tensor &t) {
       return t.dim() == 2 && t.size(0) == rows && t.size(1) == d && t.scalar_type() == dt &&
-             t.is_cuda();
+             device.has(t);
     };
     const void *res = nullptr;
     int64_t rs = 0, ros = 0;
@@ -184,14 +210,14 @@ PyObject *norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
     void *ro = nullptr;
     if (given(a[4])) {
       const Tensor &r = tensor(a[4], "rms_norm: residual");
-      need(like_x(r), "rms_norm: residual must have x's shape and type");
+      need(like_x(r), "rms_norm: residual must have x's shape, type and device");
       res = r.data_ptr();
       rs = row_stride(r, "residual");
     }
     const bool second = given(a[4]) || given(a[8]);
     if (given(a[8])) {
       const Tensor &r = tensor(a[8], "rms_norm: residual_out");
-      need(like_x(r), "rms_norm: residual_out must have x's shape and type");
+      need(like_x(r), "rms_norm: residual_out must have x's shape, type and device");
       ro = r.data_ptr();
       ros = row_stride(r, "residual_out");
     } else if (res) {
@@ -209,10 +235,10 @@ PyObject *norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
       const Tensor &o = tensor(a[6], "rms_norm: out");
       if (quant)
         need(o.dim() == 2 && o.size(0) == rows && o.size(1) == d && e4m3(o) &&
-                 o.is_contiguous() && o.is_cuda(),
+                 o.is_contiguous() && device.has(o),
              "rms_norm_fp8: out must be dense float8_e4m3fn (or uint8) of x's shape");
       else
-        need(like_x(o), "rms_norm: out must have x's shape and type");
+        need(like_x(o), "rms_norm: out must have x's shape, type and device");
       out = o.data_ptr();
       os = row_stride(o, "out");
     } else {
@@ -232,7 +258,7 @@ PyObject *norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
     float *scale;
     if (given(a[7])) {
       const Tensor &s = tensor(a[7], "rms_norm_fp8: scale");
-      need(s.scalar_type() == at::kFloat && s.is_contiguous() && s.is_cuda() &&
+      need(s.scalar_type() == at::kFloat && s.is_contiguous() && device.has(s) &&
                s.dim() == (group ? 2 : 1) && s.size(0) == rows && (!group || s.size(1) == groups),
            "rms_norm_fp8: scale must be float32 [rows, ceil(d/128)] or [rows]");
       scale = s.data_ptr<float>();
@@ -267,8 +293,8 @@ PyObject *matmul(PyObject *, PyObject *const *a, Py_ssize_t n) {
          "matmul_fp8: float32 scales [M, ceil(K/128)] and [ceil(N/128), ceil(K/128)]");
     need(x.is_contiguous() && w.is_contiguous() && sx.is_contiguous() && sw.is_contiguous(),
          "tensors must be contiguous");
-    need(x.is_cuda() && w.is_cuda() && sx.is_cuda() && sw.is_cuda(),
-         "matmul_fp8: tensors must be on the GPU");
+    Device device(a[0]);
+    need(device.has(x, w, sx, sw), "matmul_fp8: tensors must be on the GPU of the handle");
     const Stream stream(a[7], x);
     Tensor made;
     void *out;
@@ -276,8 +302,8 @@ PyObject *matmul(PyObject *, PyObject *const *a, Py_ssize_t n) {
     int code;
     if (given(a[6])) {
       const Tensor &o = tensor(a[6], "matmul_fp8: out");
-      need(o.dim() == 2 && o.size(0) == M && o.size(1) == N && o.is_cuda(),
-           "matmul_fp8: out must be [M, N] on the GPU");
+      need(o.dim() == 2 && o.size(0) == M && o.size(1) == N && device.has(o),
+           "matmul_fp8: out must be [M, N] on the GPU of the handle");
       code = code_of(o.scalar_type(), "matmul_fp8: out");
       os = row_stride(o, "out");
       out = o.data_ptr();
@@ -323,15 +349,15 @@ PyObject *rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
          "rope_append: positions and slots are int64 [T]");
     need(f.scalar_type() == at::kDouble && f.is_contiguous(),
          "rope_append: freqs is float64 [rot_dim/2]");
-    need(q.is_cuda() && k.is_cuda() && v.is_cuda() && pos.is_cuda() && slots.is_cuda() &&
-             f.is_cuda() && kc.is_cuda() && vc.is_cuda(),
-         "rope_append: tensors must be on the GPU");
+    Device device(a[0]);
+    need(device.has(q, k, v, pos, slots, f, kc, vc),
+         "rope_append: tensors must be on the GPU of the handle");
     const Stream stream(a[12], q);
     Tensor made;
     if (given(a[11])) {
       const Tensor &o = tensor(a[11], "rope_append: q_out");
-      need(o.sizes() == q.sizes() && o.scalar_type() == dt && o.is_cuda(),
-           "rope_append: q_out must have q's shape and type");
+      need(o.sizes() == q.sizes() && o.scalar_type() == dt && device.has(o),
+           "rope_append: q_out must have q's shape, type and device");
     } else {
       made = empty({T, Hq, D}, dt, q);
     }
@@ -400,9 +426,9 @@ PyObject *attention(PyObject *, PyObject *const *a, Py_ssize_t n) {
              kl.scalar_type() == at::kInt && qs.numel() == table.size(0) + 1 &&
              kl.numel() == table.size(0) && qs.is_contiguous() && kl.is_contiguous(),
          "attention: int32 page_table [B, max_pages], q_start [B+1], kv_len [B]");
-    need(q.is_cuda() && kc.is_cuda() && vc.is_cuda() && table.is_cuda() && qs.is_cuda() &&
-             kl.is_cuda(),
-         "attention: tensors must be on the GPU");
+    Device device(a[0]);
+    need(device.has(q, kc, vc, table, qs, kl),
+         "attention: tensors must be on the GPU of the handle");
     need(T <= INT32_MAX && table.size(0) <= INT32_MAX && table.size(1) <= INT32_MAX &&
              kc.size(1) <= INT32_MAX,
          "attention: sizes");
@@ -411,7 +437,7 @@ PyObject *attention(PyObject *, PyObject *const *a, Py_ssize_t n) {
     if (given(a[9])) {
       const Tensor &m = tensor(a[9], "attention: tree_mask");
       need(m.dim() == 2 && m.size(0) == T && m.scalar_type() == at::kInt && m.is_contiguous() &&
-               m.is_cuda(),
+               device.has(m),
            "attention: tree_mask must be int32 [T, words]");
       r.tree_mask = m.data_ptr<int32_t>();
       r.tree_words = static_cast<int32_t>(m.size(1));
@@ -419,15 +445,15 @@ PyObject *attention(PyObject *, PyObject *const *a, Py_ssize_t n) {
     if (given(a[11])) {
       const Tensor &l = tensor(a[11], "attention: lse");
       need(l.dim() == 2 && l.size(0) == T && l.size(1) == Hq && l.scalar_type() == at::kFloat &&
-               l.is_contiguous() && l.is_cuda(),
+               l.is_contiguous() && device.has(l),
            "attention: lse must be float32 [T, Hq]");
       r.lse = l.data_ptr<float>();
     }
     Tensor made;
     if (given(a[10])) {
       const Tensor &o = tensor(a[10], "attention: out");
-      need(o.sizes() == q.sizes() && o.scalar_type() == dt && o.is_cuda(),
-           "attention: out must have q's shape and type");
+      need(o.sizes() == q.sizes() && o.scalar_type() == dt && device.has(o),
+           "attention: out must have q's shape, type and device");
     } else {
       made = empty({T, Hq, D}, dt, q);
     }
@@ -495,6 +521,7 @@ PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_target_bind", nullptr, -1, g_me
 
 PyMODINIT_FUNC PyInit__target_bind() {
   g_raw = PyUnicode_InternFromString("_raw");
+  g_index = PyUnicode_InternFromString("_index");
   g_stream = PyUnicode_InternFromString("cuda_stream");
   return PyModule_Create(&g_module);
 }

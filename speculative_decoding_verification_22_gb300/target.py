@@ -112,6 +112,9 @@ class TargetOps:
             raise SpecVerifyError(SV_ERR_ARG, "closed handle")
         return self._raw
 
+    def _has(self, t):
+        return t.is_cuda and t.get_device() == self._index
+
     def rms_norm(self, x, weight, eps=1e-6, residual=None, out=None, residual_out=None,
                  stream=None):
         """h = x + residual; out = h / sqrt(mean(h^2) + eps) * weight.  Returns
@@ -161,14 +164,15 @@ class TargetOps:
         [B * (N + 1), ceil((N + 1) / 32)], row 0 of a sequence its root."""
         B, N = tree_parents.shape
         _need(tree_parents.dtype == torch.int32 and tree_parents.is_contiguous()
-              and tree_parents.is_cuda, "tree_mask: parents must be int32 [B, N] on the GPU")
+              and self._has(tree_parents),
+              "tree_mask: parents must be int32 [B, N] on the GPU of the handle")
         shape = (B * (N + 1), (N + 32) // 32)
         if out is None:
             out = torch.empty(shape, dtype=torch.int32, device=tree_parents.device)
         else:
             _need(tuple(out.shape) == shape and out.dtype == torch.int32
-                  and out.is_contiguous() and out.is_cuda,
-                  f"tree_mask: out must be int32 {shape}")
+                  and out.is_contiguous() and self._has(out),
+                  f"tree_mask: out must be int32 {shape} on the GPU of the handle")
         _check(self._lib.spec_target_tree_mask(self._handle(), tree_parents.data_ptr(), B, N,
                                                out.data_ptr(), self._stream(stream)),
                "spec_target_tree_mask")

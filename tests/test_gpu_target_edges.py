@@ -143,3 +143,26 @@ def test_norm_into_eight_bits_that_are_not_e4m3_is_refused(ops):
     want = ops.rms_norm_fp8(x, w)[0]
     out = torch.empty(4, 128, dtype=torch.uint8, device="cuda")
     assert torch.equal(ops.rms_norm_fp8(x, w, out=out)[0], want.view(torch.uint8))
+
+
+def test_tensors_of_another_device_are_refused(ops):
+    """A handle that says it belongs to the next device refuses this one's tensors
+    before anything is launched, whichever argument they are."""
+    other = sv.TargetOps.__new__(sv.TargetOps)
+    other.__dict__.update(ops.__dict__)
+    other._index = ops._index + 1
+    x, w = torch.ones(4, 128, device="cuda"), torch.ones(128, device="cuda")
+    q, c = x.view(4, 1, 128), x.view(1, 4, 1, 128)
+    e, s = x.to(torch.float8_e4m3fn), torch.ones(4, 1, device="cuda")
+    pos, f = torch.arange(4, device="cuda"), torch.zeros(64, dtype=torch.float64, device="cuda")
+    try:
+        for call in (lambda: other.rms_norm(x, w), lambda: other.rms_norm_fp8(x, w),
+                     lambda: other.matmul_fp8(e, s, e, s[:1]),
+                     lambda: other.rope_append(q, q, q, pos, pos, f, c, c.clone()),
+                     lambda: other.attention(q, c, c, int32([[0]]), int32([0, 4]), int32([4])),
+                     lambda: other.tree_mask(int32([[-1, 0]]))):
+            with pytest.raises(ValueError, match="GPU of the handle"):
+                call()
+    finally:
+        other.h = other._raw = None  # the handle is the fixture's
+    assert ops.status() == sv.SV_OK
