@@ -88,6 +88,15 @@ class TargetOps:
             return torch._C._cuda_getCurrentRawStream(self._index)
         return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
+    def _torch_stream(self, stream):
+        """The given stream as torch's (None, which changes nothing, for none)."""
+        if stream is None or isinstance(stream, torch.cuda.Stream):
+            return stream
+        raw = self._stream(stream)
+        if raw == 0:
+            return torch.cuda.default_stream(self._index)
+        return torch.cuda.ExternalStream(raw, device=self._index)
+
     def status(self, stream=None) -> int:
         """Waits for the stream; the first device-side error since the last call."""
         return int(self._lib.spec_target_status(self._handle(), self._stream(stream)))
@@ -168,7 +177,9 @@ class TargetOps:
               "tree_mask: parents must be int32 [B, N] on the GPU of the handle")
         shape = (B * (N + 1), (N + 32) // 32)
         if out is None:
-            out = torch.empty(shape, dtype=torch.int32, device=tree_parents.device)
+            # from the call's own stream, whose order its memory is reused in
+            with torch.cuda.stream(self._torch_stream(stream)):
+                out = torch.empty(shape, dtype=torch.int32, device=tree_parents.device)
         else:
             _need(tuple(out.shape) == shape and out.dtype == torch.int32
                   and out.is_contiguous() and self._has(out),

@@ -166,3 +166,33 @@ def test_tensors_of_another_device_are_refused(ops):
     finally:
         other.h = other._raw = None  # the handle is the fixture's
     assert ops.status() == sv.SV_OK
+
+
+# ---- streams --------------------------------------------------------------------------
+
+def stream_of(t):
+    """The stream whose pool a tensor's memory belongs to."""
+    for seg in torch.cuda.memory_snapshot():
+        if seg["address"] <= t.data_ptr() < seg["address"] + seg["total_size"]:
+            return seg["stream"]
+    raise AssertionError("not the allocator's memory")
+
+
+def test_outputs_come_from_the_given_stream(ops):
+    """New outputs are of the memory of the stream that the call goes to, so that
+    nothing enqueued elsewhere may still use it."""
+    x, w = torch.ones(4, 128, device="cuda"), torch.ones(128, device="cuda")
+    parents = int32([[-1, 0, 0, 2]])
+    want = ops.tree_mask(parents)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for stream in (side, side.cuda_stream):
+        for call in (lambda s: ops.rms_norm(x, w, stream=s)[0],
+                     lambda s: ops.tree_mask(parents, stream=s)):
+            assert stream_of(call(stream)) == side.cuda_stream
+            assert stream_of(call(None)) == torch.cuda.current_stream().cuda_stream
+        got = ops.tree_mask(parents, stream=stream)
+        side.synchronize()
+        assert torch.equal(got, want)
+    assert torch.equal(ops.tree_mask(parents, stream=0), want)
+    assert ops.status() == sv.SV_OK
