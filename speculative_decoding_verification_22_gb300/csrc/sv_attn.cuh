@@ -43,7 +43,7 @@ __device__ __forceinline__ void key_range(const sv_attention_t &a, const SeqGeom
   hi = a.tree_mask ? s.kv : at + 1;  // kv bounds both
   if (hi > s.kv) hi = s.kv;
   if (hi < 0) hi = 0;
-  lo = a.window > 0 && at + 1 - a.window > 0 ? at + 1 - a.window : 0;
+  lo = a.window > 0 && at >= a.window ? at + 1 - a.window : 0;
 }
 __device__ __forceinline__ bool tree_sees(const int32_t *row, int words, int jj) {
   return jj < 32 * words && ((static_cast<uint32_t>(row[jj >> 5]) >> (jj & 31)) & 1u);

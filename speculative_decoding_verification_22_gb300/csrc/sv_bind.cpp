@@ -15,6 +15,7 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
 #include <cmath>
 #include <stdexcept>
 #include <string>
@@ -64,6 +65,12 @@ long long integer(PyObject *o) {
   const long long v = PyLong_AsLongLong(o);
   if (v == -1 && PyErr_Occurred()) throw Raised();
   return v;
+}
+// A size in 32 bits; beyond them the nearest, so that none turns into another's
+// value (a window of 2^32 + 5 keys is one of all keys, -2^32 is still negative).
+int32_t size32(PyObject *o) {
+  return static_cast<int32_t>(
+      std::clamp<long long>(integer(o), INT32_MIN, INT32_MAX));
 }
 double number(PyObject *o) {
   const double v = PyFloat_AsDouble(o);
@@ -226,7 +233,7 @@ PyObject *norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
       ros = d;
     }
     const bool quant = given(a[5]);
-    const int group = quant ? static_cast<int>(integer(a[5])) : 0;
+    const int group = quant ? size32(a[5]) : 0;
     const float eps = static_cast<float>(number(a[3]));
     Tensor made, made_scale;
     void *out;
@@ -487,7 +494,7 @@ PyObject *attention(PyObject *, PyObject *const *a, Py_ssize_t n) {
     r.D = static_cast<int32_t>(D);
     r.page_size = static_cast<int32_t>(kc.size(1));
     r.max_pages = static_cast<int32_t>(table.size(1));
-    r.window = static_cast<int32_t>(integer(a[8]));
+    r.window = size32(a[8]);
     r.dtype = code;
     r.scale = static_cast<float>(given(a[7]) ? number(a[7])
                                              : 1.0 / std::sqrt(static_cast<double>(D)));

@@ -133,6 +133,33 @@ def test_attention_tree_over_pages_that_no_node_sees(ops, dtype):
     assert ops.status() == sv.SV_ERR_CACHE
 
 
+def test_attention_windows_of_any_size(ops):
+    """A window beyond 32 bits is one of all keys, and a negative one is refused."""
+    g = gen(4)
+    kc, vc, table, _, _ = build_cache(g, [400], 16, 2, 64, torch.bfloat16)
+    q = randn(g, (9, 4, 64), torch.bfloat16)
+    args = q, kc, vc, table, starts([9]), int32([400])
+    want = ops.attention(*args)
+    for window in (2 ** 31 - 1, 2 ** 31, 2 ** 32, 2 ** 32 + 5, 2 ** 62 + 7):
+        assert torch.equal(ops.attention(*args, window=window), want)
+    for window in (-1, -2 ** 32, 5 - 2 ** 32, -2 ** 62):
+        with pytest.raises(sv.SpecVerifyError):
+            ops.attention(*args, window=window)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_attention_largest_window_with_more_tokens_than_keys(ops, dtype):
+    g = gen(5)
+    dt = DTYPES[dtype]
+    news, lens, window = [40, 300], [7, 200], 2 ** 31 - 1
+    kc, vc, table, ks, vs = build_cache(g, lens, 16, 2, 64, dt)
+    q = randn(g, (340, 4, 64), dt)
+    out = ops.attention(q, kc, vc, table, starts(news), int32(lens), window=window)
+    o, mag, _, big = attention_ref(q, ks, vs, news, 0.125, window)
+    within(out, o, attention_bound(o, mag, big, 64, dt))
+    assert ops.status() == sv.SV_OK
+
+
 # ---- refusals -------------------------------------------------------------------------
 
 def test_norm_into_eight_bits_that_are_not_e4m3_is_refused(ops):
@@ -143,6 +170,13 @@ def test_norm_into_eight_bits_that_are_not_e4m3_is_refused(ops):
     want = ops.rms_norm_fp8(x, w)[0]
     out = torch.empty(4, 128, dtype=torch.uint8, device="cuda")
     assert torch.equal(ops.rms_norm_fp8(x, w, out=out)[0], want.view(torch.uint8))
+
+
+def test_norm_groups_beyond_32_bits_are_refused(ops):
+    x, w = torch.ones(4, 256, device="cuda"), torch.ones(256, device="cuda")
+    for group in (2 ** 32, 2 ** 32 + 128, 128 - 2 ** 32):
+        with pytest.raises(sv.SpecVerifyError):
+            ops.rms_norm_fp8(x, w, group=group)
 
 
 def test_tensors_of_another_device_are_refused(ops):
