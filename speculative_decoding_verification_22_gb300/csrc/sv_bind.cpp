@@ -443,9 +443,10 @@ PyObject *attention(PyObject *, PyObject *const *a, Py_ssize_t n) {
     sv_attention_t r{};
     if (given(a[9])) {
       const Tensor &m = tensor(a[9], "attention: tree_mask");
-      need(m.dim() == 2 && m.size(0) == T && m.scalar_type() == at::kInt && m.is_contiguous() &&
-               device.has(m),
-           "attention: tree_mask must be int32 [T, words]");
+      // (a mask without words has no address, and would be taken for none)
+      need(m.dim() == 2 && m.size(0) == T && m.size(1) >= 1 && m.scalar_type() == at::kInt &&
+               m.is_contiguous() && device.has(m),
+           "attention: tree_mask must be int32 [T, words], with a word at least");
       r.tree_mask = m.data_ptr<int32_t>();
       r.tree_words = static_cast<int32_t>(m.size(1));
     }

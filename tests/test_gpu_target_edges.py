@@ -179,6 +179,16 @@ def test_norm_groups_beyond_32_bits_are_refused(ops):
             ops.rms_norm_fp8(x, w, group=group)
 
 
+def test_tree_masks_without_words_are_refused(ops):
+    """As the C entry point does; it is not a call without a mask."""
+    g = gen(8)
+    kc, vc, table, _, _ = build_cache(g, [40], 16, 1, 64, torch.bfloat16)
+    q = randn(g, (4, 2, 64), torch.bfloat16)
+    none = torch.empty(4, 0, dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError, match="word"):
+        ops.attention(q, kc, vc, table, starts([4]), int32([40]), tree_mask=none)
+
+
 def test_tensors_of_another_device_are_refused(ops):
     """A handle that says it belongs to the next device refuses this one's tensors
     before anything is launched, whichever argument they are."""
