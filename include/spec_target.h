@@ -197,7 +197,10 @@ int spec_target_rope_append(spec_target_t *h, const sv_rope_append_t *a, void *s
  *   o = sum_j softmax_j(scale q . k_j) v_j,  lse = log sum_j exp(scale q . k_j)
  * Query head h reads cache head h / (Hq / Hkv).  A token that sees nothing
  * gets o = 0 and lse = -inf; what is masked does not count even where the
- * cache holds NaN or infinities there.
+ * cache holds NaN or infinities there.  Scores, their maximum, the sums and o
+ * are fp32; on the tensor cores a weight is rounded to dtype before it
+ * multiplies v_j, half a step of its value (2^-8 in bf16, 2^-11 in fp16, where
+ * weights below 2^-21 of the row's largest are kept to 2^-32 of it).
  *   q          device, dtype [T, Hq, D], token and head strides
  *   k_cache, v_cache  as above
  *   page_table device, int32 [B, max_pages], row stride: page of the cached

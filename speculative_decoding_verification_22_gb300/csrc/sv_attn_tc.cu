@@ -7,8 +7,12 @@
 // in one pass over the keys with a running maximum m and sum l of each row:
 // a tile of keys gives S = Q K^T, P = 2^((S - m) scale log2 e), and
 // O += P V.  m only moves when a row's maximum has grown by more than 2^8, so
-// that O is rarely rescaled; P is at most 2^8 and l and O stay exact relative
-// to the m they were summed with.
+// that O is rarely rescaled; l and O stay relative to the m they were summed
+// with.  P is rounded to the 16-bit type for its product (half a step a weight),
+// l sums it unrounded.  fp16 has few exponents below one: there P, and with it
+// l and O, carry a further 2^7 (up to 2^15 of 2^16), so that a weight is lost
+// only below 2^-32 of the row's largest, and not below 2^-25, of which 2^17 equal
+// ones under one large weight would be missed by 0.2% of the output.
 //
 //  * The rows of one cache head are its new tokens times the G = Hq / Hkv
 //    query heads that share it, so each K and V tile serves all of them.  An
@@ -71,6 +75,11 @@ constexpr int kPairedPage = 16;
 constexpr int kMaxSlots = 10;
 constexpr uint64_t kCleanupLimitNs = 2000000000ull;
 constexpr float kRescale = 8.0f;  // log2 of the growth of m that rescales O
+// log2 of what P, l and O carry beside the weights: fp16 ends at 2^16, which
+// leaves kRescale 7 and a bit; bf16 has fp32's exponents.
+template <class T>
+constexpr float carried() { return __is_same(T, __half) ? 7.0f : 0.0f; }
+constexpr float kLn2 = 0.69314718055994531f;
 
 template <int DPAD>
 struct Shape {
@@ -641,7 +650,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        const float off = m == -INFINITY ? 0.0f : -m * args.c;
+        const float off = m == -INFINITY ? 0.0f : -m * args.c + carried<T>();
         const uint64_t c2 = pair2(args.c, args.c), off2 = pair2(off, off);
         uint64_t ls[2] = {0, 0};
 #pragma unroll
@@ -761,7 +770,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (all) {
             if (a.lse)
               a.lse[t * a.Hq + head] =
-                  l != 0.0f ? m * (args.c * 0.69314718055994531f) + logf(l) : -INFINITY;
+                  l != 0.0f ? m * (args.c * kLn2) + (logf(l) - carried<T>() * kLn2) : -INFINITY;
           } else {
             part[r] = m;
             part[kPartRows + r] = l;
@@ -1221,7 +1230,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
                                  d0, acc, fast_output(a));
         if (a.lse && d0 == 0)
           a.lse[t * a.Hq + head] =
-              sum != 0.0f ? top * (args.c * 0.69314718055994531f) + logf(sum) : -INFINITY;
+              sum != 0.0f ? top * (args.c * kLn2) + (logf(sum) - carried<T>() * kLn2) : -INFINITY;
       }
     }
     // Other warps, at any time, have the row's other elements: this one takes

@@ -160,6 +160,40 @@ def test_attention_largest_window_with_more_tokens_than_keys(ops, dtype):
     assert ops.status() == sv.SV_OK
 
 
+# ---- attention: many small weights under a large one ---------------------------------
+
+@pytest.mark.parametrize("first", [True, False])
+@pytest.mark.parametrize("n", [1, 40])  # few rows, a block of many
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_attention_small_weights_of_a_long_cache_count(ops, dtype, n, first):
+    """One key 17 nats above 131072 equal ones, whose weights of e^-17 make half a
+    percent of the sum. As many sequences as keep each on one SM, over the same
+    pages. In fp16 a weight is rounded to half a step or, below the normal range,
+    by 2^-25 at most, which stands for 2^-32 of the largest."""
+    g = gen(6)
+    dt = DTYPES[dtype]
+    B, D, page, kv = 160, 64, 64, 131073
+    kc, vc, table, ks, vs = build_cache(g, [kv], page, 1, D, dt, fill=0.0)
+    top = 0 if first else kv - n - 1  # before the new tokens: every row sees it
+    at = int(table[0, top // page]), top % page
+    for t in (kc, ks[0]):
+        t.zero_()
+    for t in (vc, vs[0]):
+        t.fill_(1.0)
+    kc[at] = ks[0][top] = 2.125  # 64 * 2.125 / 8 = 17
+    vc[at] = vs[0][top] = 0.0
+    q = torch.ones(B * n, 4, D, dtype=dt, device="cuda")
+    lse = torch.empty(B * n, 4, device="cuda")
+    out = ops.attention(q, kc, vc, table.expand(B, -1).contiguous(), starts([n] * B),
+                        int32([kv] * B), lse=lse)
+    o, mag, l, big = attention_ref(q[:n], ks, vs, [n], 0.125)
+    bound = attention_bound(o, mag, big, D, dt) + (kv * 2.0 ** -32 if dtype == "fp16" else 0.0)
+    within(out, o.repeat(B, 1, 1), bound.repeat(B, 1, 1))
+    l = l.repeat(B, 1)
+    within(lse, l, score_error(big, D) + 2.0 ** -20 * l.abs())
+    assert ops.status() == sv.SV_OK
+
+
 # ---- refusals -------------------------------------------------------------------------
 
 def test_norm_into_eight_bits_that_are_not_e4m3_is_refused(ops):
