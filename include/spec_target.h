@@ -156,8 +156,9 @@ int spec_target_rope_freqs(const sv_rope_t *cfg, double *freqs, double *magnitud
  * cache slots, in one launch.  Of each head's D elements the first rot_dim
  * are rotated, as pairs (i, i + rot_dim/2) or, interleaved, (2i, 2i + 1):
  *   (a, b) -> m (a cos - b sin, a sin + b cos),
- * the others are copied.  The angle is reduced in 64 bits, so it is exact to
- * fp32 at any position.
+ * the others are copied.  The fraction of a turn p f is taken from the exact
+ * product and rounded once, to fp32 (2^-25 of a turn at most), for positions and
+ * turns up to 2^53.
  *   q, k, v     device, dtype (SV_BF16, SV_FP16, SV_FP32); token and head
  *               strides (they may be slices of one fused projection)
  *   positions   device, int64 [T] (a tree's nodes: the depth)

@@ -2,9 +2,10 @@
 // append of K and V to their cache pages, in one launch; and the tree mask of
 // the attention.
 //
-// One block takes one token: its rot/2 angles are formed once (64-bit product
-// and reduction to a fraction of a turn, then sin and cos of pi times twice
-// that in fp32, so a far position loses nothing) and shared by all heads.
+// One block takes one token: its rot/2 angles are formed once (the exact product
+// in two 64-bit parts, reduced to a fraction of a turn, then sin and cos of pi
+// times twice that in fp32, so a far position loses nothing) and shared by all
+// heads.
 // Every element is read once and written once; with many tokens HBM bounds
 // it, with few the launch.  A thread has one unit in flight and few registers,
 // so that eight blocks share an SM: 8192 tokens of 48 heads of 128 in 36 us
@@ -104,8 +105,10 @@ __global__ void __launch_bounds__(kRopeThreads, 8)
     if (first) {
       const double pos = static_cast<double>(a.positions[t]);
       for (int i = threadIdx.x; i < half; i += kRopeThreads) {
-        const double turns = pos * a.freqs[i];
-        const float f = static_cast<float>(turns - rint(turns));  // -1/2 .. 1/2
+        // the product in two parts: its rounding to 64 bits counts among the
+        // fractions of a turn from about 2^28 turns on
+        const double by = a.freqs[i], turns = pos * by, rest = fma(pos, by, -turns);
+        const float f = static_cast<float>((turns - rint(turns)) + rest);  // about -1/2 .. 1/2
         float s, c;
         sincospif(2.0f * f, &s, &c);
         cs[i] = make_float2(c * a.magnitude, s * a.magnitude);

@@ -1,6 +1,7 @@
 """The target-layer operators on the GPU where roles, masks, types and streams
 meet: cases beside those of test_gpu_target_ops.py."""
 import math
+from fractions import Fraction
 
 import pytest
 import torch
@@ -191,6 +192,29 @@ def test_attention_small_weights_of_a_long_cache_count(ops, dtype, n, first):
     within(out, o.repeat(B, 1, 1), bound.repeat(B, 1, 1))
     l = l.repeat(B, 1)
     within(lse, l, score_error(big, D) + 2.0 ** -20 * l.abs())
+    assert ops.status() == sv.SV_OK
+
+
+# ---- rotary: far positions ------------------------------------------------------------
+
+@pytest.mark.parametrize("far", [2 ** 21, 2 ** 28, 2 ** 34, 2 ** 40, 2 ** 46, 2 ** 52])
+def test_rope_far_positions(ops, far):
+    """Fractions of a turn against exact products. They are rounded to fp32 (2^-25
+    of a turn, 2 pi times that in radians, below 2^-22), then cos and sin have two
+    units of half a step each and the products one: together below 2^-20."""
+    T, D = 64, 64
+    freqs, _ = sv.spec_target_rope_freqs(D, 10000.0)
+    pos = far + torch.randint(0, far, (T,), generator=gen(7), device="cuda")
+    pos[::2] *= -1
+    x = torch.zeros(T, 1, D, device="cuda")
+    x[..., :D // 2] = 1.0
+    c = torch.zeros(1, 1, 1, D, device="cuda")
+    none = torch.full((T,), -1, device="cuda")
+    y = ops.rope_append(x, x, x, pos, none, freqs.cuda(), c, c.clone())
+    turns = [[float(p * Fraction(f) % 1) for f in freqs.tolist()] for p in pos.tolist()]
+    angle = torch.tensor(turns, dtype=torch.float64, device="cuda")[:, None] * (2 * math.pi)
+    want = torch.cat((angle.cos(), angle.sin()), -1)
+    within(y, want, torch.full_like(want, 2.0 ** -20))
     assert ops.status() == sv.SV_OK
 
 
