@@ -4,6 +4,8 @@ Python binding of the target-layer operators beside it.
 Each CUDA translation unit is compiled in parallel into ``_build/`` and
 linked with the static CUDA runtime, so the library loads on machines
 without a GPU (for symbol checks) and needs only the driver at run time.
+The library does not need the binding: it is linked first, and stands where
+the binding fails to build or torch is missing or has no CUDA.
 """
 from __future__ import annotations
 
@@ -35,8 +37,14 @@ BIND = os.path.join(HERE, "_target_bind.so")
 
 
 def _bind_commands():
-    """(compile, link, object) of the binding for the torch that is installed."""
-    import torch
+    """(compile, link, object) of the binding for the torch that is installed;
+    None where there is none with CUDA, and nothing to bind."""
+    try:
+        import torch
+    except ImportError:
+        return None
+    if torch.version.cuda is None:
+        return None
     t = os.path.dirname(torch.__file__)
     cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
     obj = os.path.join(BUILD, f"sv_bind.{torch.__version__}.o")
@@ -83,21 +91,29 @@ def build(force: bool = False, ptxas_verbose: bool = False, verbose: bool = Fals
                 cmd.append("-Xptxas=-v")
             jobs.append(cmd)
 
-    bind_compile, bind_link, bind_obj = _bind_commands()
-    if force or _stale(bind_obj, [BIND_SRC] + hdrs):
-        jobs.insert(0, bind_compile)
+    bind = _bind_commands()
+    bind_job = bind is not None and (force or _stale(bind[2], [BIND_SRC] + hdrs))
+    if bind_job:
+        jobs.insert(0, bind[0])
 
     def run(cmd):
         r = subprocess.run(cmd, capture_output=True, text=True)
         return cmd, r
 
+    failed = bind_failed = None
     if jobs:
         with concurrent.futures.ThreadPoolExecutor(max_workers=len(jobs)) as ex:
-            for cmd, r in ex.map(run, jobs):
+            for i, (cmd, r) in enumerate(ex.map(run, jobs)):
                 if verbose or ptxas_verbose or r.returncode != 0:
                     sys.stderr.write(r.stdout + r.stderr)
                 if r.returncode != 0:
-                    raise RuntimeError(f"compilation failed: {' '.join(cmd)}")
+                    what = f"compilation failed: {' '.join(cmd)}"
+                    if bind_job and i == 0:
+                        bind_failed = what
+                    else:
+                        failed = failed or what
+    if failed:
+        raise RuntimeError(failed)
     if force or _stale(LIB, objs):
         tmp = LIB + f".tmp{os.getpid()}"
         cmd = [nvcc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs,
@@ -107,6 +123,13 @@ def build(force: bool = False, ptxas_verbose: bool = False, verbose: bool = Fals
             sys.stderr.write(r.stdout + r.stderr)
             raise RuntimeError("link failed")
         os.replace(tmp, LIB)
+    if bind is None:
+        sys.stderr.write("no torch with CUDA: the Python binding of the target-layer "
+                         "operators is not built\n")
+        return LIB
+    if bind_failed:
+        raise RuntimeError(bind_failed)
+    _, bind_link, bind_obj = bind
     if force or _stale(BIND, [bind_obj, LIB]):
         tmp = BIND + f".tmp{os.getpid()}"
         r = subprocess.run([*bind_link, "-o", tmp], capture_output=True, text=True)

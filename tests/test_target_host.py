@@ -2,6 +2,8 @@
 and the rotary frequencies against their formulas."""
 import ctypes
 import math
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -256,3 +258,52 @@ def test_eight_bits_that_are_not_e4m3_are_refused(dtype):
     for a in (good, good.view(torch.uint8)):  # these come to the check of the device
         with pytest.raises(ValueError, match="on the GPU"):
             ops.matmul_fp8(a, s, good, one)
+
+
+# ---- build -----------------------------------------------------------------------
+
+@pytest.fixture
+def fake_build(monkeypatch, tmp_path):
+    """The build with commands that only make their outputs; those whose compiler
+    is in `broken` fail."""
+    from speculative_decoding_verification_22_gb300 import build as b
+    for name, path in (("BUILD", "objects"), ("LIB", "lib.so"), ("BIND", "bind.so")):
+        monkeypatch.setattr(b, name, str(tmp_path / path))
+    broken, ran = set(), []
+
+    def run(cmd, **_):
+        ran.append(cmd[0])
+        if cmd[0] not in broken:
+            open(cmd[cmd.index("-o") + 1], "w").close()
+        return subprocess.CompletedProcess(cmd, int(cmd[0] in broken), "", "")
+    monkeypatch.setattr(b.subprocess, "run", run)
+    return b, broken, ran, tmp_path
+
+
+def test_the_library_is_built_where_the_binding_cannot_be(fake_build):
+    b, broken, ran, path = fake_build
+    broken.add("g++")
+    with pytest.raises(RuntimeError, match="g\\+\\+"):
+        b.build(force=True)
+    assert (path / "lib.so").exists() and not (path / "bind.so").exists()
+    broken.clear()
+    assert b.build() == str(path / "lib.so") and (path / "bind.so").exists()
+
+
+def test_a_broken_library_is_an_error_and_links_nothing(fake_build):
+    b, broken, ran, path = fake_build
+    broken.add(b._nvcc())
+    with pytest.raises(RuntimeError, match="nvcc"):
+        b.build(force=True)
+    assert not (path / "lib.so").exists() and not (path / "bind.so").exists()
+
+
+@pytest.mark.parametrize("torch_is", ["missing", "without CUDA"])
+def test_without_a_torch_to_bind_to_the_library_alone_is_built(fake_build, monkeypatch, torch_is):
+    b, broken, ran, path = fake_build
+    if torch_is == "missing":
+        monkeypatch.setitem(sys.modules, "torch", None)
+    else:
+        monkeypatch.setattr(torch.version, "cuda", None)
+    assert b.build(force=True) == str(path / "lib.so")
+    assert (path / "lib.so").exists() and "g++" not in ran
