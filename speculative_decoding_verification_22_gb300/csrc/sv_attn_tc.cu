@@ -869,7 +869,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const unsigned held = __ballot_sync(0xffffffffu, c < args.walks && kb < ke);
             if (lane == 0) desc->held[k0 / 32] = held;
             if (held) n = k0 + 32 - __clz(held);
-            if (!__all_sync(0xffffffffu, c < args.walks && c0 < ue)) break;
+            // (the last lane's next CTA is the next round's first)
+            if (!__all_sync(0xffffffffu, c + 1 < args.walks && c0 < ue)) break;
           }
           if (lane == 0) {
             desc->b = r.b;
