@@ -53,7 +53,7 @@ void spec_target_destroy(spec_target_t *h);
 
 /* Synchronises `stream`, then returns and clears the handle's status word:
  * SV_OK, SV_ERR_CACHE (a slot, page, cache length or token range out of
- * bounds), SV_ERR_TIMEOUT (a bounded device-side wait ran out: the call's
+ * bounds), SV_ERR_TOKEN (a tree's parent), SV_ERR_TIMEOUT (a bounded device-side wait ran out: the call's
  * outputs are not valid), or SV_ERR_CUDA if synchronisation failed. */
 int spec_target_status(spec_target_t *h, void *stream);
 
@@ -211,7 +211,7 @@ int spec_target_rope_append(spec_target_t *h, const sv_rope_append_t *a, void *s
  *   tree_mask  device, int32 [T, tree_words] or NULL: bit jj % 32 of word
  *              jj / 32 of a new token's row says whether it sees new token
  *              jj of its sequence (further ones: no)
- *   out        device, dtype [T, Hq, D], token and head strides
+ *   out        device, dtype [T, Hq, D], token and head strides; apart from q
  *   lse        device, fp32 [T, Hq] or NULL
  * dtype: SV_BF16, SV_FP16 (tensor cores where D is a multiple of 8 up to
  * 128, page_size a power of two from 8, pointers and strides multiples of 16

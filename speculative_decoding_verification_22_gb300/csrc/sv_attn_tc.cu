@@ -35,9 +35,11 @@
 //    and warp 11 for the V of narrow tiles: TMA into a ring of 160 KB; warp 9:
 //    the products; warp 10 hands out the items.
 //
-// What bounds it.  Cached bytes, for few rows a head: 64 single tokens over 2048
-// to 8192 in 211 us, 6.4 TB/s.  Products, for many: 4096 tokens over 16384 in
-// 650 us, 1.48 PFLOP/s, where the scores' product reads 8 KB of shared memory
+// What bounds it (times in this file are of kernels in a CUDA graph, but for those
+// at report_pages).  Cached bytes, for few rows a head: 64 single tokens over 2048
+// to 8192 in 211 us, 6.4 TB/s (210 to 222 by single calls).  Products, for many:
+// 4096 tokens over 16384 in 657 us, 1.46 PFLOP/s (675 to 685 by single calls),
+// where the scores' product reads 8 KB of shared memory
 // in each of its 64 cycles, all that there is, beside the copies that arrive.
 // Latency, for short calls and short sequences: 5 tokens over 1000 in 14.4 us
 // (4 of them the second launch), and about 8 us an item of up to 512 keys (256
@@ -376,7 +378,8 @@ __device__ __forceinline__ bool item_sees(const TcArgs &args, const Run &it, int
 // where a row sees a key of them, as tiles and pages reach beyond what is seen:
 // below a window, and to new tokens that no row of a tree has its bit for.  Asked
 // after a run that met such a page: in the loop over the tiles it cost a chunk of
-// 4096 tokens 684 us against 677 and a round of 5 tokens 14.8 against 14.4.
+// 4096 tokens 684 us against 677 and a round of 5 tokens 14.8 against 14.4 (single
+// calls; here 680 and 14.5).
 __device__ __forceinline__ void report_pages(const TcArgs &args, const Run &it, int keys,
                                              int key_in, int page_keys) {
   const sv_attention_t &a = args.a;

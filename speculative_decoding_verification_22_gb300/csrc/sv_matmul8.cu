@@ -19,7 +19,8 @@
 //  * Warps 0-7: scale and add (two warpgroups, half of the columns each);
 //    warp 8: TMA; warp 9: products; warps 10, 11: the columns' scales.
 //
-// What bounds it (4096 x 14336 x 4096, 205 us, 2.35 PFLOP/s): a block of 128 x
+// Times in this file are of kernels in a CUDA graph.  What bounds it (4096 x 14336 x
+// 4096, 206 us, 2.33 PFLOP/s; 220 to 230 by single calls): a block of 128 x
 // 256 x 128 takes the tensor cores 512 cycles and the whole loop about 1000.
 // The products alone run in 127 us.  With the loads it is 190: a load takes
 // 1.6 us from its slot's being freed to its use, and the four blocks of 48 KB

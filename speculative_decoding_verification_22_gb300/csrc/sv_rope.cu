@@ -8,8 +8,9 @@
 // heads.
 // Every element is read once and written once; with many tokens HBM bounds
 // it, with few the launch.  A thread has one unit in flight and few registers,
-// so that eight blocks share an SM: 8192 tokens of 48 heads of 128 in 36 us
-// (5.5 TB/s); with two units a thread and six blocks 39 us, with three 40.
+// so that eight blocks share an SM: 8192 tokens of 48 heads of 128 in 36.6 us
+// (5.5 TB/s, in a CUDA graph); with two units a thread and six blocks 39 us, with
+// three 40.
 #include "sv_target.cuh"
 
 namespace sv {
@@ -47,14 +48,14 @@ __device__ __forceinline__ void store_unit(U *p, const U &x) {
     *p = x;
 }
 
-// Vectors of eight elements (kVecs): a unit is the two vectors of eight
-// half-layout pairs, one vector of four interleaved pairs, or one vector that
-// is copied.  Otherwise single elements: a unit is one pair or one element.
 // u / d by d's 32-bit reciprocal (which is 0 for d = 1).
 __device__ __forceinline__ int divide(int u, uint32_t by) {
   return by ? static_cast<int>(__umulhi(static_cast<uint32_t>(u), by)) : u;
 }
 
+// Vectors of eight elements (kVecs): a unit is the two vectors of eight
+// half-layout pairs, one vector of four interleaved pairs, or one vector that
+// is copied.  Otherwise single elements: a unit is one pair or one element.
 template <class T, bool kVecs>
 __global__ void __launch_bounds__(kRopeThreads, 8)
     rope_append_kernel(const sv_rope_append_t a, uint32_t by_per, uint32_t by_v, int *status) {
