@@ -373,21 +373,20 @@ __device__ __forceinline__ bool item_sees(const TcArgs &args, const Run &it, int
   }
   return false;
 }
-// Reports pages outside the cache among those of a run's tiles, the ones that this
-// lane brings (keys key_in .. key_in + page_keys - 1 of a tile of `keys`).  Only
+// Reports pages outside the cache among those of a run's tiles t .. last, the ones that
+// this lane brings (keys key_in .. key_in + page_keys - 1 of a tile of `keys`).  Only
 // where a row sees a key of them, as tiles and pages reach beyond what is seen:
 // below a window, and to new tokens that no row of a tree has its bit for.  Asked
 // after a run that met such a page: in the loop over the tiles it cost a chunk of
 // 4096 tokens 684 us against 677 and a round of 5 tokens 14.8 against 14.4 (single
-// calls; here 680 and 14.5).
-__device__ __forceinline__ void report_pages(const TcArgs &args, const Run &it, int keys,
-                                             int key_in, int page_keys) {
+// calls; here 680 and 14.5), and a scan of whole runs 64 windows of 4000 over freed
+// pages of 8 179 us against 172.
+__device__ __forceinline__ void report_pages(const TcArgs &args, const Run &it, int t, int last,
+                                             int keys, int key_in, int page_keys) {
   const sv_attention_t &a = args.a;
-  if (key_in >= keys) return;
   const int32_t *pages = a.page_table + it.b * a.table_stride;
-  for (int t = 0; t < it.n; ++t) {
+  for (; t <= last; ++t) {
     const int key = (it.tile0 + t) * keys + key_in;
-    if (key >= it.s.kv) return;
     if (static_cast<uint32_t>(pages[key >> args.pow_page]) >= a.num_pages &&
         item_sees(args, it, key, key + page_keys)) {
       set_status(args.status, SV_ERR_CACHE);
@@ -956,13 +955,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           return brings && t < n && key_in < keys && key < kv ? pages[key >> args.pow_page] : 0;
         };
         int page = page_of(0);
-        bool missing = false;  // a page that is not there is loaded as zeros
+        // tiles with a page that is not there (which is loaded as zeros): the first
+        // and the last, for the lane
+        int miss0 = n, miss1 = -1;
         for (int t = 0; t < n && ok; ++t) {
           const int next = page_of(t + 1);
           const int k0 = (tile0 + t) * keys;
           const bool mine = key_in < keys && k0 + key_in < kv;
           const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, mine)) * box_bytes;
-          missing |= mine && static_cast<uint32_t>(page) >= a.num_pages;
+          if (mine && static_cast<uint32_t>(page) >= a.num_pages) {
+            miss0 = min(miss0, t);
+            miss1 = t;
+          }
           const int in_page = (k0 + key_in) & (a.page_size - 1);
           for (int x = 0; x < (wide ? 2 : 1); ++x) {
             if (!slot_free()) break;
@@ -989,7 +993,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           page = next;
         }
-        if (missing) report_pages(args, it, keys, key_in, page_keys);
+        if (miss0 <= miss1) report_pages(args, it, miss0, miss1, keys, key_in, page_keys);
         give_back();
       }
       if (lane == 0) ctl->issued[v] = issued;
