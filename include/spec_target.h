@@ -15,6 +15,8 @@
  * (the same page, "Tree attention").  The pages give no code for these
  * steps; the formulas below are the common ones.
  *
+ * The operators of the layer's second half are declared in spec_layer.h.
+ *
  * Conventions: return values, error codes and ownership as in
  * spec_verify.h.  Every call takes the cudaStream_t it is enqueued on (NULL:
  * the legacy default stream), returns without synchronising, allocates

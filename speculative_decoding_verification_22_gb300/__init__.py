@@ -35,7 +35,7 @@ SV_MAX_B = 4096
 SV_MAX_ROWS_BF16 = 384
 SV_NGRAM_MAX = 16
 
-# every symbol of include/spec_verify.h and include/spec_target.h
+# every symbol of include/spec_verify.h, include/spec_target.h and include/spec_layer.h
 EXPORTS = ("spec_verify_create", "spec_verify_run", "spec_verify_run_host",
            "spec_verify_status", "spec_verify_set_stream",
            "spec_verify_debug_logits", "spec_verify_debug_lse",
@@ -48,7 +48,8 @@ EXPORTS = ("spec_verify_create", "spec_verify_run", "spec_verify_run_host",
            "spec_target_create", "spec_target_destroy", "spec_target_status",
            "spec_target_set_wait_limit", "spec_target_rms_norm", "spec_target_rms_norm_fp8",
            "spec_target_matmul_fp8", "spec_target_rope_freqs", "spec_target_rope_append",
-           "spec_target_attention", "spec_target_tree_mask")
+           "spec_target_attention", "spec_target_tree_mask", "spec_layer_linear",
+           "spec_layer_gated_linear", "spec_layer_block_norm", "spec_layer_log_probs")
 
 
 class sv_plan_t(ctypes.Structure):
@@ -130,6 +131,8 @@ def load_library():
         lib.spec_target_rope_append.argtypes = [vp, vp, vp]
         lib.spec_target_attention.argtypes = [vp, vp, vp]
         lib.spec_target_tree_mask.argtypes = [vp, vp, i32, i32, vp, vp]
+        for name in ("linear", "gated_linear", "block_norm", "log_probs"):
+            getattr(lib, f"spec_layer_{name}").argtypes = [vp, vp, vp]
         for name in EXPORTS:
             if name not in ("spec_verify_strerror", "spec_verify_destroy",
                             "spec_target_destroy"):
@@ -418,5 +421,5 @@ class SpecVerify:
             pass
 
 
-from .target import (ROPE_SCALINGS, SV_FP16, SV_MAX_HEAD_DIM, SV_SCALE_BLOCK,  # noqa: E402
-                     TargetOps, spec_target_rope_freqs)
+from .target import (ACTIVATIONS, ROPE_SCALINGS, SV_FP16, SV_MAX_HEAD_DIM,  # noqa: E402
+                     SV_MAX_TOP, SV_SCALE_BLOCK, TargetOps, spec_target_rope_freqs)

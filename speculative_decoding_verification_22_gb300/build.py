@@ -24,9 +24,9 @@ SOURCES = ["sv_api.cu", "sv_lmhead_tc.cu", "sv_lmhead_simt.cu", "sv_tail.cu", "s
            "sv_trunc.cu",
            "sv_ngram.cu",
            "sv_target_api.cu", "sv_norm.cu", "sv_rope.cu", "sv_matmul8.cu", "sv_attn.cu",
-           "sv_attn_tc.cu"]
+           "sv_attn_tc.cu", "sv_linear.cu", "sv_block_norm.cu", "sv_log_probs.cu"]
 HEADERS = ["sv_internal.cuh", "sv_kernels.h", "sv_target.cuh", "sv_attn.cuh",
-           "sv_tmem.cuh"]
+           "sv_tmem.cuh", "sv_linear.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
          "--expt-relaxed-constexpr", "-I", INCLUDE]
@@ -78,7 +78,7 @@ def build(force: bool = False, ptxas_verbose: bool = False, verbose: bool = Fals
     os.makedirs(BUILD, exist_ok=True)
     nvcc = _nvcc()
     hdrs = [os.path.join(CSRC, h) for h in HEADERS] + [
-        os.path.join(INCLUDE, h) for h in ("spec_verify.h", "spec_target.h")]
+        os.path.join(INCLUDE, h) for h in ("spec_verify.h", "spec_target.h", "spec_layer.h")]
     jobs = []
     objs = []
     for src in SOURCES:

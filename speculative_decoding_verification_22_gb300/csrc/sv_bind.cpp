@@ -1,6 +1,6 @@
 // sv_bind.cpp -- argument marshalling of the target-layer operators for
 // Python: checks of torch tensors, allocation of missing outputs, and the call
-// of the C entry points of include/spec_target.h.
+// of the C entry points of include/spec_target.h and include/spec_layer.h.
 //
 // A call on a few tokens takes the GPU 2 to 10 us, and reading the tensors'
 // attributes from Python alone took the host 5 to 8; here it takes well under
@@ -20,7 +20,7 @@
 #include <stdexcept>
 #include <string>
 
-#include "spec_target.h"
+#include "spec_layer.h"
 
 namespace {
 
@@ -504,6 +504,288 @@ PyObject *attention(PyObject *, PyObject *const *a, Py_ssize_t n) {
   });
 }
 
+// The weight, bias and output of the products.
+void check_weight(const Tensor &w, const Tensor &x, int64_t N, const char *what) {
+  need(w.dim() == 2 && w.size(0) == N && w.size(1) == x.size(1) &&
+           w.scalar_type() == x.scalar_type(),
+       what);
+}
+const void *bias_of(PyObject *o, const Tensor &x, int64_t N, Device &device, const char *what) {
+  if (!given(o)) return nullptr;
+  const Tensor &b = tensor(o, what);
+  need(b.dim() == 1 && b.size(0) == N && b.scalar_type() == x.scalar_type() &&
+           (b.is_contiguous()) && device.has(b),
+       what);
+  return b.data_ptr();
+}
+// The type named by its code, or x's where the code is -1.
+at::ScalarType out_type(long long code, const Tensor &x) {
+  return code == SV_BF16   ? at::kBFloat16
+         : code == SV_FP16 ? at::kHalf
+         : code == SV_FP32 ? at::kFloat
+                           : x.scalar_type();
+}
+
+// linear(self, x, w, bias, activation code, residual, out type code or -1, out,
+//        stream)
+PyObject *linear(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return guarded(n, 9, [&]() -> PyObject * {
+    const Tensor &x = tensor(a[1], "linear: x"), &w = tensor(a[2], "linear: weight");
+    need(x.dim() == 2 && w.dim() == 2, "linear: x [M, K] and weight [N, K]");
+    sv_linear_t r{};
+    r.M = x.size(0);
+    r.K = x.size(1);
+    r.N = w.size(0);
+    r.dtype = code_of(x.scalar_type(), "linear: x");
+    check_weight(w, x, r.N, "linear: weight must be [N, K] of x's type");
+    Device device(a[0]);
+    need(device.has(x, w), "linear: tensors must be on the GPU of the handle");
+    r.bias = bias_of(a[3], x, r.N, device, "linear: bias must be dense [N] of x's type");
+    const Stream stream(a[8], x);
+    Tensor made;
+    if (given(a[7])) {
+      const Tensor &o = tensor(a[7], "linear: out");
+      need(o.dim() == 2 && o.size(0) == r.M && o.size(1) == r.N && device.has(o),
+           "linear: out must be [M, N] on the GPU of the handle");
+    } else {
+      made = empty({r.M, r.N}, out_type(integer(a[6]), x), x);
+    }
+    const Tensor &out = given(a[7]) ? THPVariable_Unpack(a[7]) : made;
+    r.out_dtype = code_of(out.scalar_type(), "linear: out");
+    if (given(a[5])) {
+      const Tensor &res = tensor(a[5], "linear: residual");
+      need(res.dim() == 2 && res.size(0) == r.M && res.size(1) == r.N &&
+               res.scalar_type() == out.scalar_type() && device.has(res),
+           "linear: residual must be [M, N] of the output's type");
+      r.residual = res.data_ptr();
+      r.residual_stride = row_stride(res, "linear: residual");
+    }
+    r.x = x.data_ptr();
+    r.w = w.data_ptr();
+    r.out = out.data_ptr();
+    r.x_stride = row_stride(x, "linear: x");
+    r.w_stride = row_stride(w, "linear: weight");
+    r.out_stride = row_stride(out, "linear: out");
+    r.activation = size32(a[4]);
+    check(spec_layer_linear(handle(a[0]), &r, stream.get()), "spec_layer_linear");
+    return result(a[7], made);
+  });
+}
+
+// gated(self, x, w_gate, w_up, bias_gate, bias_up, activation code, out type
+//       code or -1, out, stream)
+PyObject *gated(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return guarded(n, 10, [&]() -> PyObject * {
+    const Tensor &x = tensor(a[1], "gated_linear: x"), &g = tensor(a[2], "gated_linear: w_gate");
+    const Tensor &u = tensor(a[3], "gated_linear: w_up");
+    need(x.dim() == 2 && g.dim() == 2, "gated_linear: x [M, K], w_gate and w_up [N, K]");
+    sv_gated_linear_t r{};
+    r.M = x.size(0);
+    r.K = x.size(1);
+    r.N = g.size(0);
+    r.dtype = code_of(x.scalar_type(), "gated_linear: x");
+    check_weight(g, x, r.N, "gated_linear: w_gate must be [N, K] of x's type");
+    check_weight(u, x, r.N, "gated_linear: w_up must be [N, K] of x's type");
+    Device device(a[0]);
+    need(device.has(x, g, u), "gated_linear: tensors must be on the GPU of the handle");
+    r.bias_gate = bias_of(a[4], x, r.N, device, "gated_linear: bias_gate must be dense [N]");
+    r.bias_up = bias_of(a[5], x, r.N, device, "gated_linear: bias_up must be dense [N]");
+    const Stream stream(a[9], x);
+    Tensor made;
+    if (given(a[8])) {
+      const Tensor &o = tensor(a[8], "gated_linear: out");
+      need(o.dim() == 2 && o.size(0) == r.M && o.size(1) == r.N && device.has(o),
+           "gated_linear: out must be [M, N] on the GPU of the handle");
+    } else {
+      made = empty({r.M, r.N}, out_type(integer(a[7]), x), x);
+    }
+    const Tensor &out = given(a[8]) ? THPVariable_Unpack(a[8]) : made;
+    r.out_dtype = code_of(out.scalar_type(), "gated_linear: out");
+    r.x = x.data_ptr();
+    r.w_gate = g.data_ptr();
+    r.w_up = u.data_ptr();
+    r.out = out.data_ptr();
+    r.x_stride = row_stride(x, "gated_linear: x");
+    r.gate_stride = row_stride(g, "gated_linear: w_gate");
+    r.up_stride = row_stride(u, "gated_linear: w_up");
+    r.out_stride = row_stride(out, "gated_linear: out");
+    r.activation = size32(a[6]);
+    check(spec_layer_gated_linear(handle(a[0]), &r, stream.get()), "spec_layer_gated_linear");
+    return result(a[8], made);
+  });
+}
+
+// block_norm(self, x, residual, weight, post_weight, gate, branch_scale, eps,
+//            group, out, scale, residual_out, stream); group: None for the
+// rows' type, 0 or 128 for E4M3.
+PyObject *block_norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return guarded(n, 13, [&]() -> PyObject * {
+    const Tensor &x = tensor(a[1], "block_norm: x"), &res = tensor(a[2], "block_norm: residual");
+    const Tensor &w = tensor(a[3], "block_norm: weight");
+    const at::ScalarType dt = x.scalar_type();
+    sv_block_norm_t r{};
+    r.dtype = code_of(dt, "block_norm");
+    need(x.dim() == 2, "block_norm: x must be [rows, d]");
+    Device device(a[0]);
+    need(device.has(x), "block_norm: tensors must be on the GPU of the handle");
+    r.rows = x.size(0);
+    r.d = x.size(1);
+    auto like_x = [&](const Tensor &t) {
+      return t.dim() == 2 && t.size(0) == r.rows && t.size(1) == r.d && t.scalar_type() == dt &&
+             device.has(t);
+    };
+    auto column = [&](const Tensor &t) {
+      return t.dim() == 1 && t.size(0) == r.d && t.scalar_type() == dt && t.is_contiguous() &&
+             device.has(t);
+    };
+    need(like_x(res), "block_norm: residual must have x's shape, type and device");
+    need(column(w), "block_norm: weight must be dense [d] of x's type and device");
+    if (given(a[4])) {
+      const Tensor &p = tensor(a[4], "block_norm: post_weight");
+      need(column(p), "block_norm: post_weight must be dense [d] of x's type and device");
+      r.post_weight = p.data_ptr();
+    }
+    if (given(a[5])) {
+      const Tensor &g = tensor(a[5], "block_norm: gate");
+      const int64_t dim = g.dim();
+      need((dim == 1 || dim == 2) && g.scalar_type() == dt && device.has(g),
+           "block_norm: gate must be [d], [1, d], [rows, 1] or [rows, d] of x's type and device");
+      const int64_t rows = dim == 2 ? g.size(0) : 1, cols = g.size(dim - 1);
+      need((rows == 1 || rows == r.rows) && (cols == 1 || cols == r.d),
+           "block_norm: gate must be [d], [1, d], [rows, 1] or [rows, d]");
+      r.gate = g.data_ptr();
+      r.gate_row = rows == 1 ? 0 : g.stride(0);
+      r.gate_col = cols == 1 ? 0 : g.stride(dim - 1);
+      need(r.gate_col <= 1, "block_norm: the gate's rows must be dense");
+    }
+    const Stream stream(a[12], x);
+    const bool quant = given(a[8]);
+    r.group = quant ? size32(a[8]) : -1;
+    need(!quant || r.group == 0 || r.group == SV_SCALE_BLOCK, "block_norm: group must be 0 or 128");
+    r.branch_scale = static_cast<float>(number(a[6]));
+    r.eps = static_cast<float>(number(a[7]));
+    Tensor made, made_scale, made_res;
+    if (given(a[9])) {
+      const Tensor &o = tensor(a[9], "block_norm: out");
+      if (quant)
+        need(o.dim() == 2 && o.size(0) == r.rows && o.size(1) == r.d && e4m3(o) &&
+                 o.is_contiguous() && device.has(o),
+             "block_norm_fp8: out must be dense float8_e4m3fn (or uint8) of x's shape");
+      else
+        need(like_x(o), "block_norm: out must have x's shape, type and device");
+    } else {
+      made = empty({r.rows, r.d}, quant ? at::kFloat8_e4m3fn : dt, x);
+    }
+    const Tensor &out = given(a[9]) ? THPVariable_Unpack(a[9]) : made;
+    if (quant) {
+      const int64_t groups = (r.d + SV_SCALE_BLOCK - 1) / SV_SCALE_BLOCK;
+      if (given(a[10])) {
+        const Tensor &s = tensor(a[10], "block_norm_fp8: scale");
+        need(s.scalar_type() == at::kFloat && s.is_contiguous() && device.has(s) &&
+                 s.dim() == (r.group ? 2 : 1) && s.size(0) == r.rows &&
+                 (!r.group || s.size(1) == groups),
+             "block_norm_fp8: scale must be float32 [rows, ceil(d/128)] or [rows]");
+        r.scale = s.data_ptr<float>();
+      } else {
+        made_scale = r.group ? empty({r.rows, groups}, at::kFloat, x)
+                             : empty({r.rows}, at::kFloat, x);
+        r.scale = made_scale.data_ptr<float>();
+      }
+    }
+    if (given(a[11])) {
+      need(like_x(tensor(a[11], "block_norm: residual_out")),
+           "block_norm: residual_out must have x's shape, type and device");
+    } else {
+      made_res = empty({r.rows, r.d}, dt, x);
+    }
+    const Tensor &ro = given(a[11]) ? THPVariable_Unpack(a[11]) : made_res;
+    r.x = x.data_ptr();
+    r.residual = res.data_ptr();
+    r.weight = w.data_ptr();
+    r.out = out.data_ptr();
+    r.residual_out = ro.data_ptr();
+    r.x_stride = row_stride(x, "block_norm: x");
+    r.residual_stride = row_stride(res, "block_norm: residual");
+    r.out_stride = row_stride(out, "block_norm: out");
+    r.residual_out_stride = row_stride(ro, "block_norm: residual_out");
+    check(spec_layer_block_norm(handle(a[0]), &r, stream.get()), "spec_layer_block_norm");
+    PyObject *list = PyList_New(quant ? 3 : 2);
+    if (!list) throw Raised();
+    PyList_SET_ITEM(list, 0, result(a[9], made));
+    if (quant) PyList_SET_ITEM(list, 1, result(a[10], made_scale));
+    PyList_SET_ITEM(list, quant ? 2 : 1, result(a[11], made_res));
+    return list;
+  });
+}
+
+// log_probs(self, logits, tokens, top, temperature, out, stream); out: None or
+// the sequence of tensors that is returned otherwise
+PyObject *log_probs(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return guarded(n, 7, [&]() -> PyObject * {
+    const Tensor &x = tensor(a[1], "log_probs: logits");
+    need(x.dim() == 2, "log_probs: logits must be [rows, V]");
+    sv_log_probs_t r{};
+    r.dtype = code_of(x.scalar_type(), "log_probs");
+    r.rows = x.size(0);
+    r.V = x.size(1);
+    Device device(a[0]);
+    need(device.has(x), "log_probs: tensors must be on the GPU of the handle");
+    if (given(a[2])) {
+      const Tensor &t = tensor(a[2], "log_probs: tokens");
+      need(t.dim() == 2 && t.size(0) == r.rows && t.scalar_type() == at::kInt &&
+               t.is_contiguous() && t.size(1) <= INT32_MAX && device.has(t),
+           "log_probs: tokens must be dense int32 [rows, n]");
+      r.tokens = t.data_ptr<int32_t>();
+      r.n = static_cast<int32_t>(t.size(1));
+    }
+    r.top = size32(a[3]);
+    need(r.top >= 0 && r.top <= SV_MAX_TOP && r.top <= std::max<int64_t>(r.V, 0),
+         "log_probs: top must be from 0 to 64 and at most V");
+    r.temperature = static_cast<float>(number(a[4]));
+    const Stream stream(a[6], x);
+    Tensor outs[4];
+    const int count = r.top ? 4 : 2;
+    if (given(a[5])) {
+      PyObject *seq = PySequence_Fast(a[5], "log_probs: out must be a sequence of tensors");
+      if (!seq) throw Raised();
+      struct Held {
+        PyObject *o;
+        ~Held() { Py_DECREF(o); }
+      } held{seq};
+      need(PySequence_Fast_GET_SIZE(seq) == count, "log_probs: out must hold two tensors, or four with top");
+      for (int i = 0; i < count; ++i)
+        outs[i] = tensor(PySequence_Fast_GET_ITEM(seq, i), "log_probs: out");
+      const int64_t cols[4] = {r.n, 1, r.top, r.top};
+      for (int i = 0; i < count; ++i)
+        need(outs[i].scalar_type() == (i == 2 ? at::kInt : at::kFloat) &&
+                 outs[i].is_contiguous() && device.has(outs[i]) &&
+                 outs[i].dim() == (i == 1 ? 1 : 2) && outs[i].size(0) == r.rows &&
+                 (i == 1 || outs[i].size(1) == cols[i]),
+             "log_probs: out must be float32 [rows, n], [rows], int32 and float32 [rows, top]");
+    } else {
+      outs[0] = empty({r.rows, r.n}, at::kFloat, x);
+      outs[1] = empty({r.rows}, at::kFloat, x);
+      if (r.top) {
+        outs[2] = empty({r.rows, r.top}, at::kInt, x);
+        outs[3] = empty({r.rows, r.top}, at::kFloat, x);
+      }
+    }
+    r.logits = x.data_ptr();
+    r.stride = row_stride(x, "log_probs: logits");
+    r.log_probs = outs[0].data_ptr<float>();
+    r.entropy = outs[1].data_ptr<float>();
+    if (r.top) {
+      r.top_ids = outs[2].data_ptr<int32_t>();
+      r.top_log_probs = outs[3].data_ptr<float>();
+    }
+    check(spec_layer_log_probs(handle(a[0]), &r, stream.get()), "spec_layer_log_probs");
+    PyObject *list = PyList_New(count);
+    if (!list) throw Raised();
+    for (int i = 0; i < count; ++i) PyList_SET_ITEM(list, i, THPVariable_Wrap(outs[i]));
+    return list;
+  });
+}
+
 PyObject *set_error(PyObject *, PyObject *cls) {
   Py_INCREF(cls);
   Py_XDECREF(g_error);
@@ -520,6 +802,14 @@ PyMethodDef g_methods[] = {
      "rope_append"},
     {"attention", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(&attention)),
      METH_FASTCALL, "attention"},
+    {"linear", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(&linear)), METH_FASTCALL,
+     "linear"},
+    {"gated", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(&gated)), METH_FASTCALL,
+     "gated_linear"},
+    {"block_norm", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(&block_norm)),
+     METH_FASTCALL, "block_norm and block_norm_fp8"},
+    {"log_probs", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(&log_probs)),
+     METH_FASTCALL, "log_probs"},
     {"set_error", set_error, METH_O, "the class raised for an entry point's error"},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_target_bind", nullptr, -1, g_methods,

@@ -1,10 +1,10 @@
-// sv_target.cuh -- definitions shared by the operators of spec_target.h:
+// sv_target.cuh -- definitions shared by the operators of spec_target.h and spec_layer.h:
 // the handle, launch interfaces, and element conversions.
 #pragma once
 
 #include <cuda_bf16.h>
 
-#include "../../include/spec_target.h"
+#include "../../include/spec_layer.h"
 #include "sv_internal.cuh"
 
 // The handle of the C ABI.
@@ -97,6 +97,22 @@ int launch_matmul_fp8(const spec_target &h, const MatmulParams &P, cudaStream_t 
 int launch_attention(const spec_target &h, const sv_attention_t &a, cudaStream_t stream);
 
 cudaError_t launch_tree_mask(const int32_t *parents, int B, int N, int32_t *mask, int *status,
+                             cudaStream_t stream);
+
+// linear (wu NULL) and gated linear: w is the weight, or the gate's.
+struct LinearParams {
+  const void *x, *w, *wu, *bias, *bias_u, *res;
+  void *out;
+  int64_t xs, ws, wus, rs, os;
+  int64_t M, N, K;
+  int dtype, out_dtype, act;
+};
+int launch_linear(const spec_target &h, const LinearParams &P, cudaStream_t stream);
+
+cudaError_t launch_block_norm(const sv_block_norm_t &a, int num_sms, cudaStream_t stream);
+
+int log_probs_checks(const sv_log_probs_t &a);
+cudaError_t launch_log_probs(const sv_log_probs_t &a, int num_sms, int *status,
                              cudaStream_t stream);
 
 // Launch with programmatic stream serialisation: the kernel waits for what

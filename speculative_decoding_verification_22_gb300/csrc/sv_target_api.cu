@@ -1,4 +1,4 @@
-// sv_target_api.cu -- the C ABI declared in include/spec_target.h: handle
+// sv_target_api.cu -- the C ABI declared in include/spec_target.h and spec_layer.h: handle
 // lifetime, argument checks and launches.
 #include <cmath>
 #include <cstdint>
@@ -39,6 +39,27 @@ int norm_checks(const void *x, int64_t xs, const void *res, int64_t rs, const vo
   if (!aligned(x, es) || !aligned(w, es) || (res && !aligned(res, es)) || (ro && !aligned(ro, es)))
     return SV_ERR_ALIGN;
   return SV_OK;
+}
+
+// Sizes and strides of a product; its pointers have been looked at.
+int linear_checks(const sv::LinearParams &p) {
+  constexpr int64_t kMost = int64_t(1) << 24, kStride = int64_t(1) << 36;
+  if (!float_type(p.dtype) || !float_type(p.out_dtype) || p.act < SV_ACT_NONE ||
+      p.act > SV_ACT_SILU)
+    return SV_ERR_ARG;
+  if (p.M < 0 || p.N < 1 || p.K < 1 || p.M > kMost || p.N > kMost || p.K > kMost)
+    return SV_ERR_SHAPE;
+  if (p.M == 0) return SV_OK;
+  auto stride = [&](int64_t s, int64_t row, int64_t rows) {
+    return rows <= 1 || (s >= row && s <= kStride);
+  };
+  if (!stride(p.xs, p.K, p.M) || !stride(p.ws, p.K, p.N) || !stride(p.os, p.N, p.M) ||
+      (p.wu && !stride(p.wus, p.K, p.N)) || (p.res && !stride(p.rs, p.N, p.M)))
+    return SV_ERR_SHAPE;
+  const size_t es = elem_size(p.dtype), eo = elem_size(p.out_dtype);
+  for (const void *q : {p.x, p.w, p.wu, p.bias, p.bias_u})
+    if (!aligned(q, es)) return SV_ERR_ALIGN;
+  return aligned(p.out, eo) && aligned(p.res, eo) ? SV_OK : SV_ERR_ALIGN;
 }
 
 }  // namespace
@@ -249,6 +270,59 @@ int spec_target_attention(spec_target_t *h, const sv_attention_t *a, void *strea
   const int c = check_handle(h);
   if (c != SV_OK) return c;
   return sv::launch_attention(*h, *a, static_cast<cudaStream_t>(stream));
+}
+
+int spec_layer_linear(spec_target_t *h, const sv_linear_t *a, void *stream) {
+  if (!h || !a) return SV_ERR_ARG;
+  if (a->M > 0 && (!a->x || !a->w || !a->out)) return SV_ERR_ARG;
+  const sv::LinearParams P{a->x, a->w, nullptr, a->bias, nullptr, a->residual, a->out,
+                           a->x_stride, a->w_stride, 0, a->residual_stride, a->out_stride,
+                           a->M, a->N, a->K, a->dtype, a->out_dtype, a->activation};
+  int c = linear_checks(P);
+  if (c != SV_OK || a->M == 0) return c;
+  if ((c = check_handle(h)) != SV_OK) return c;
+  return sv::launch_linear(*h, P, static_cast<cudaStream_t>(stream));
+}
+
+int spec_layer_gated_linear(spec_target_t *h, const sv_gated_linear_t *a, void *stream) {
+  if (!h || !a) return SV_ERR_ARG;
+  if (a->M > 0 && (!a->x || !a->w_gate || !a->w_up || !a->out)) return SV_ERR_ARG;
+  const sv::LinearParams P{a->x, a->w_gate, a->w_up, a->bias_gate, a->bias_up, nullptr, a->out,
+                           a->x_stride, a->gate_stride, a->up_stride, 0, a->out_stride,
+                           a->M, a->N, a->K, a->dtype, a->out_dtype, a->activation};
+  int c = linear_checks(P);
+  if (c != SV_OK || a->M == 0) return c;
+  if ((c = check_handle(h)) != SV_OK) return c;
+  return sv::launch_linear(*h, P, static_cast<cudaStream_t>(stream));
+}
+
+int spec_layer_block_norm(spec_target_t *h, const sv_block_norm_t *a, void *stream) {
+  if (!h || !a || (a->group != -1 && a->group != 0 && a->group != SV_SCALE_BLOCK) ||
+      !std::isfinite(a->branch_scale))
+    return SV_ERR_ARG;
+  const bool quant = a->group >= 0;
+  int c = norm_checks(a->x, a->x_stride, a->residual, a->residual_stride, a->weight, a->eps,
+                      a->rows, a->d, a->dtype, a->out, quant ? a->d : a->out_stride,
+                      a->residual_out, a->residual_out_stride);
+  if (c != SV_OK || a->rows == 0) return c;
+  if (!a->residual || (quant && !a->scale) ||
+      (a->gate && (a->gate_row < 0 || a->gate_col < 0 || a->gate_col > 1)))
+    return SV_ERR_ARG;
+  const size_t es = elem_size(a->dtype);
+  if ((!quant && !aligned(a->out, es)) || (quant && !aligned(a->scale, 4)) ||
+      !aligned(a->post_weight, es) || !aligned(a->gate, es))
+    return SV_ERR_ALIGN;
+  if ((c = check_handle(h)) != SV_OK) return c;
+  return done(sv::launch_block_norm(*a, h->num_sms, static_cast<cudaStream_t>(stream)));
+}
+
+int spec_layer_log_probs(spec_target_t *h, const sv_log_probs_t *a, void *stream) {
+  if (!h || !a) return SV_ERR_ARG;
+  int c = sv::log_probs_checks(*a);
+  if (c != SV_OK || a->rows == 0) return c;
+  if ((c = check_handle(h)) != SV_OK) return c;
+  return done(sv::launch_log_probs(*a, h->num_sms, h->status,
+                                   static_cast<cudaStream_t>(stream)));
 }
 
 int spec_target_tree_mask(spec_target_t *h, const int32_t *tree_parents, int32_t B, int32_t N,

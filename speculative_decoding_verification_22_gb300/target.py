@@ -18,13 +18,19 @@ from . import SV_BF16, SV_ERR_ARG, SV_FP32, SpecVerifyError, _check, load_librar
 SV_FP16 = 3
 SV_SCALE_BLOCK = 128
 SV_MAX_HEAD_DIM = 256
+SV_MAX_TOP = 64
 ROPE_SCALINGS = ("plain", "linear", "ntk", "banded", "yarn")
+ACTIVATIONS = {None: 0, "none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 
 _CODES = {torch.bfloat16: SV_BF16, torch.float32: SV_FP32, torch.float16: SV_FP16}
 
-# sv_rope_append_t and sv_attention_t, for callers that fill them from Python
+# sv_rope_append_t, sv_attention_t and so on, for callers that fill them from Python
 _ROPE = struct.Struct("@3P6q3P1P2q2P6q1q8i1f1i")
 _ATTN = struct.Struct("@8P1P4q6q1q1q10i1f1i")
+_LINEAR = struct.Struct("@5P4q3q4i")
+_GATED = struct.Struct("@6P4q3q4i")
+_BLOCK_NORM = struct.Struct("@8P6q2q2i2f")
+_LOG_PROBS = struct.Struct("@6P3q3i1f")
 
 
 class sv_rope_t(ctypes.Structure):
@@ -36,6 +42,21 @@ class sv_rope_t(ctypes.Structure):
 def _need(ok, message):
     if not ok:
         raise ValueError(message)
+
+
+def _activation(name):
+    code = ACTIVATIONS.get(name)
+    _need(code is not None, f"unknown activation {name!r}")
+    return code
+
+
+def _out_code(dtype):
+    """The code of an output type; -1: the inputs'."""
+    if dtype is None:
+        return -1
+    code = _CODES.get(dtype)
+    _need(code is not None, "the output must be bfloat16, float16 or float32")
+    return code
 
 
 def _binding():
@@ -166,6 +187,48 @@ class TargetOps:
         ``scale`` is 1 / sqrt(D) if not given.  Returns out [T, Hq, D]."""
         return _bound.attention(self, q, k_cache, v_cache, page_table, q_start, kv_len, scale,
                                 window, tree_mask, out, lse, stream)
+
+    def linear(self, x, weight, bias=None, activation=None, residual=None, out_dtype=None,
+               out=None, stream=None):
+        """act(x weight^T + bias) + residual, x [M, K], weight [N, K], bias [N] of one
+        type; ``activation`` one of ``ACTIVATIONS``.  The output [M, N] has
+        ``out_dtype`` (x's if not given), the residual the output's type; it may be
+        ``out`` itself."""
+        return _bound.linear(self, x, weight, bias, _activation(activation), residual,
+                             _out_code(out_dtype), out, stream)
+
+    def gated_linear(self, x, w_gate, w_up, bias_gate=None, bias_up=None, activation="silu",
+                     out_dtype=None, out=None, stream=None):
+        """act(x w_gate^T + bias_gate) * (x w_up^T + bias_up): the first half of a
+        gated feed-forward block, whose second is ``linear`` with the residual.
+        x [M, K], w_gate and w_up [N, K] (halves of one fused weight or two)."""
+        return _bound.gated(self, x, w_gate, w_up, bias_gate, bias_up, _activation(activation),
+                            _out_code(out_dtype), out, stream)
+
+    def block_norm(self, x, residual, weight, post_weight=None, gate=None, branch_scale=1.0,
+                   eps=1e-6, out=None, residual_out=None, stream=None):
+        """The norms after and before a block: y = x / rms(x) * post_weight (x without
+        one), h = residual + branch_scale * gate * y, out = h / rms(h) * weight, with
+        rms(v) = sqrt(mean(v^2) + eps).  ``gate``: [d], [1, d], [rows, 1] or [rows, d].
+        Returns [out, h]."""
+        return _bound.block_norm(self, x, residual, weight, post_weight, gate, branch_scale, eps,
+                                 None, out, None, residual_out, stream)
+
+    def block_norm_fp8(self, x, residual, weight, post_weight=None, gate=None, branch_scale=1.0,
+                       eps=1e-6, group=SV_SCALE_BLOCK, out=None, scale=None, residual_out=None,
+                       stream=None):
+        """``block_norm`` with out in E4M3 and its scales, group as in
+        ``rms_norm_fp8``.  Returns [out8, scale, h]."""
+        return _bound.block_norm(self, x, residual, weight, post_weight, gate, branch_scale, eps,
+                                 group, out, scale, residual_out, stream)
+
+    def log_probs(self, logits, tokens=None, top=0, temperature=1.0, out=None, stream=None):
+        """Log probabilities under softmax(logits / temperature) of the given tokens
+        (int32 [rows, n]; -1 is none and gets 0), and the entropies.  Returns
+        [log_probs [rows, n], entropy [rows]], with ``top`` > 0 also the most likely
+        ids int32 [rows, top] (of equal logits the smaller id first) and their log
+        probabilities.  ``out``: the same tensors to be filled."""
+        return _bound.log_probs(self, logits, tokens, top, temperature, out, stream)
 
     def tree_mask(self, tree_parents, out=None, stream=None):
         """The attention's mask for draft trees: int32 parents [B, N] as
