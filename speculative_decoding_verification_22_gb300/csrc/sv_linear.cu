@@ -6,7 +6,7 @@
 // fp32 arithmetic on operands of any type, stride and alignment: a block of 256
 // threads holds a 64 x 64 tile of the output, 4 x 4 a thread, and walks K in
 // steps of 16 through shared memory.
-#include "sv_linear.cuh"
+#include "sv_linear_tc.cuh"
 
 namespace sv {
 namespace {
@@ -88,6 +88,9 @@ cudaError_t launch_general(const LinearParams &P, cudaStream_t stream) {
 
 int launch_linear(const spec_target &h, const LinearParams &P, cudaStream_t stream) {
   cudaError_t e;
+  if (P.dtype != SV_FP32 && lin_rows_aligned(P.x, P.xs, P.M) && lin_rows_aligned(P.w, P.ws, P.N) &&
+      (!P.wu || lin_rows_aligned(P.wu, P.wus, P.N)))
+    return P.M <= 128 ? launch_linear_few(h, P, stream) : launch_linear_pair(h, P, stream);
   if ((P.M + kTile - 1) / kTile > 65535) return SV_ERR_SHAPE;
   switch (P.dtype) {
     case SV_BF16: e = launch_general<__nv_bfloat16>(P, stream); break;

@@ -1,0 +1,334 @@
+// sv_linear_few.cu -- products with an epilogue for few rows of x (up to 128):
+// the weight is streamed once through the tensor cores.
+//
+//  * The weight's rows are the 128 lanes of a tile, x's rows its columns
+//    (padded to 16), so nothing but the weight costs bytes.  Gated: 64 rows of
+//    each of the two weights, so that one tile holds both factors of 64
+//    columns of the output.
+//  * A cluster of up to eight CTAs shares a tile, each takes a part of K; the
+//    parts meet in distributed shared memory, where each CTA adds some of the
+//    columns in the order of K (repeatable, no scratch, no second launch) and
+//    stores them.  The adding of a tile runs beside the next one's products.
+//  * Warps 0-3: sums and epilogue; warp 4: TMA; warp 5: products.
+//
+// What bounds it: the bytes of the weight.
+#include "sv_linear_tc.cuh"
+
+namespace sv {
+namespace {
+
+constexpr int kEpiWarps = 4, kLoadWarp = 4, kMmaWarp = 5;
+constexpr int kThreads = 32 * 6;
+constexpr int kLanes = 128;
+constexpr int kMaxSplit = 8;
+constexpr int kMaxStages = 12;
+
+struct Args {
+  LinearParams p;
+  int *status;
+  uint64_t limit_ns;
+  int bn, tiles, split, kblocks, stages;
+  int bf16;
+};
+
+struct Ctl {
+  uint64_t full[kMaxStages], empty[kMaxStages];
+  uint64_t tfull[2], tempty[2];
+  uint64_t xfull, xempty;
+  uint64_t teardown;
+  uint32_t tmem;
+  int abort, issued, consumed;
+};
+
+// K blocks of a stage
+template <int kCols>
+constexpr int stage_blocks() { return kCols <= 64 ? 2 : 1; }
+template <int kCols>
+constexpr int stage_bytes() { return stage_blocks<kCols>() * (kLanes + kCols) * 128; }
+
+template <int kCols, bool kGated>
+__global__ void __launch_bounds__(kThreads, 1)
+    linear_few_kernel(const __grid_constant__ CUtensorMap tmW,
+                      const __grid_constant__ CUtensorMap tmU,
+                      const __grid_constant__ CUtensorMap tmX, const __grid_constant__ Args args) {
+  constexpr int kKb = stage_blocks<kCols>(), kStage = stage_bytes<kCols>();
+  constexpr int kRows = kGated ? 64 : 128;  // columns of the output in a tile
+  const LinearParams &p = args.p;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t *smem = smem_raw + (base - raw);
+  float *parts = reinterpret_cast<float *>(smem + args.stages * kStage);
+  const int M = static_cast<int>(p.M);
+  const int per = (M + args.split - 1) / args.split;  // columns that a CTA adds
+  Ctl *ctl = reinterpret_cast<Ctl *>(smem + args.stages * kStage + args.split * per * kLanes * 4);
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+  const LinAbort ab{args.status, args.limit_ns, &ctl->abort};
+
+  if (tid == 0) {
+    for (int i = 0; i < args.stages; ++i) {
+      mbar_init(smem_u32(&ctl->full[i]), 1);
+      mbar_init(smem_u32(&ctl->empty[i]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&ctl->tfull[i]), 1);
+      mbar_init(smem_u32(&ctl->tempty[i]), kEpiWarps);
+    }
+    mbar_init(smem_u32(&ctl->xfull), kEpiWarps * args.split);
+    mbar_init(smem_u32(&ctl->xempty), kEpiWarps * args.split);
+    mbar_init(smem_u32(&ctl->teardown), 1);
+    ctl->abort = ctl->issued = ctl->consumed = 0;
+    mbar_fence_init();
+  }
+  if (warp == kLoadWarp && lane == 0) {
+    tma_prefetch_desc(&tmW);
+    if (kGated) tma_prefetch_desc(&tmU);
+    tma_prefetch_desc(&tmX);
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(smem_u32(&ctl->tmem), 2 * kCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = __shfl_sync(0xffffffffu, ctl->tmem, 0);
+  if (args.split > 1) lin_cluster_sync();  // the barriers of all CTAs are set up
+  pdl_wait();
+  pdl_launch_dependents();
+
+  const int rank = args.split > 1 ? static_cast<int>(lin_cluster_rank()) : 0;
+  const int first = blockIdx.x / args.split, step = gridDim.x / args.split;
+  const int kb0 = static_cast<int>(static_cast<int64_t>(args.kblocks) * rank / args.split);
+  const int kb1 = static_cast<int>(static_cast<int64_t>(args.kblocks) * (rank + 1) / args.split);
+
+  if (warp < kEpiWarps) {
+    // ---------------- sums and epilogue ----------------
+    const int row = tid;
+    const uint32_t tacc = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+    uint32_t it = 0;
+    bool ok = true;
+    for (int tile = first; tile < args.tiles && ok; tile += step, ++it) {
+      const uint32_t slot = it & 1, phase = it >> 1 & 1;
+      if (!(ok = lin_wait(smem_u32(&ctl->tfull[slot]), phase, ab))) break;
+      tc_fence_after();
+      if (!(ok = lin_wait<true>(smem_u32(&ctl->xempty), (it & 1) ^ 1u, ab))) break;
+      // column c goes to CTA c / per, as its column c % per of this CTA's part
+      int q = 0, left = per;
+      uint32_t at = lin_remote(smem_u32(parts + (rank * per) * kLanes + row), 0);
+#pragma unroll
+      for (int c0 = 0; c0 < kCols; c0 += 16) {
+        if (c0 >= M) break;
+        uint32_t x[16];
+        tmem_ld16(tacc + slot * kCols + c0, x);
+        tmem_ld_wait();
+        tmem_reg_fence(x);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          if (c0 + e < M) {
+            lin_store_remote(at, __uint_as_float(x[e]));
+            at += kLanes * 4;
+            if (--left == 0 && c0 + e + 1 < M) {
+              left = per;
+              at = lin_remote(smem_u32(parts + (rank * per) * kLanes + row), ++q);
+            }
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(smem_u32(&ctl->tempty[slot]));
+        for (int c = 0; c < args.split; ++c) lin_arrive_remote(lin_remote(smem_u32(&ctl->xfull), c));
+      }
+      __syncwarp();
+      if (!(ok = lin_wait<true>(smem_u32(&ctl->xfull), it & 1, ab))) break;
+      const int mine = min(per, M - rank * per);
+      const int r = row % kRows;
+      const int64_t n = static_cast<int64_t>(tile) * kRows + r;
+      if (n < p.N) {
+        const float b = p.bias ? load_any(p.bias, n, p.dtype) : 0.0f;
+        const float bu = kGated && p.bias_u ? load_any(p.bias_u, n, p.dtype) : 0.0f;
+        for (int v = row / kRows; v < mine; v += kLanes / kRows) {
+          float y = 0.0f, u = 0.0f;
+          for (int s = 0; s < args.split; ++s) {
+            y += parts[(s * per + v) * kLanes + r];
+            if (kGated) u += parts[(s * per + v) * kLanes + 64 + r];
+          }
+          const int64_t m = rank * per + v;
+          y = activate(y + b, p.act);
+          if (kGated) y *= u + bu;
+          if (p.res) y += load_any(p.res, m * p.rs + n, p.out_dtype);
+          store_any(p.out, m * p.os + n, y, p.out_dtype);
+        }
+      }
+      __syncwarp();
+      if (lane == 0)
+        for (int c = 0; c < args.split; ++c)
+          lin_arrive_remote(lin_remote(smem_u32(&ctl->xempty), c));
+    }
+  } else if (warp == kLoadWarp) {
+    // ---------------- TMA ----------------
+    const uint64_t first_out = policy_evict_first(), keep = policy_evict_normal();
+    int stage = 0, issued = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int tile = first; tile < args.tiles && ok; tile += step) {
+      for (int kb = kb0; kb < kb1; kb += kKb) {
+        if (!(ok = lin_wait(smem_u32(&ctl->empty[stage]), phase ^ 1u, ab))) break;
+        if (lane == 0) {
+          const uint32_t full = smem_u32(&ctl->full[stage]);
+          const int blocks = min(kKb, kb1 - kb);
+          mbar_arrive_expect_tx(full, blocks * (kLanes + args.bn) * 128);
+          for (int j = 0; j < blocks; ++j) {
+            const uint32_t at = base + stage * kStage + j * (kLanes + kCols) * 128;
+            const int k = (kb + j) * kLinBlk;
+            tma_load_2d(at, &tmW, k, tile * kRows, full, first_out);
+            if (kGated) tma_load_2d(at + 64 * 128, &tmU, k, tile * kRows, full, first_out);
+            tma_load_2d(at + kLanes * 128, &tmX, k, 0, full, keep);
+          }
+          ctl->issued = ++issued;
+        }
+        __syncwarp();
+        if (++stage == args.stages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+  } else {
+    // ---------------- products ----------------
+    const uint32_t idesc = idesc_16(args.bf16, kLanes, args.bn, false);
+    int stage = 0, consumed = 0;
+    uint32_t phase = 0, it = 0;
+    bool ok = true;
+    for (int tile = first; tile < args.tiles && ok; tile += step, ++it) {
+      const uint32_t slot = it & 1;
+      if (!(ok = lin_wait(smem_u32(&ctl->tempty[slot]), (it >> 1 & 1) ^ 1u, ab))) break;
+      tc_fence_after();
+      for (int kb = kb0; kb < kb1; kb += kKb) {
+        if (!(ok = lin_wait(smem_u32(&ctl->full[stage]), phase, ab))) break;
+        if (lane == 0) ctl->consumed = ++consumed;
+        tc_fence_after();
+        if (elect_one()) {
+          const int blocks = min(kKb, kb1 - kb);
+          for (int j = 0; j < blocks; ++j) {
+            const uint32_t at = base + stage * kStage + j * (kLanes + kCols) * 128;
+            const uint64_t ad = sw128_desc(at), bd = sw128_desc(at + kLanes * 128);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              umma_16(tmem + slot * kCols, ad + 2u * k, bd + 2u * k, idesc,
+                      kb > kb0 || j > 0 || k > 0);
+          }
+          umma_commit(smem_u32(&ctl->empty[stage]));
+          if (kb + kKb >= kb1) umma_commit(smem_u32(&ctl->tfull[slot]));
+        }
+        __syncwarp();
+        if (++stage == args.stages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+    if (elect_one()) {
+      umma_commit(smem_u32(&ctl->teardown));
+      const int never = 0;
+      mbar_wait(smem_u32(&ctl->teardown), 0u, kLinCleanupNs, &never);
+    }
+    __syncwarp();
+  }
+
+  // ---------------- teardown ----------------
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kLoadWarp && lane == 0) {
+    // only after an abort can copies still be in flight
+    const int never = 0;
+    for (int i = ctl->consumed; i < ctl->issued; ++i)
+      mbar_wait(smem_u32(&ctl->full[i % args.stages]),
+                static_cast<uint32_t>((i / args.stages) & 1), kLinCleanupNs, &never);
+  }
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 2 * kCols);
+  }
+  if (args.split > 1) lin_cluster_sync();  // nobody writes to a CTA that is gone
+}
+
+template <int kCols, bool kGated>
+int launch(const spec_target &h, const LinearParams &P, cudaStream_t stream) {
+  constexpr int kRows = kGated ? 64 : 128;
+  if (!lin_encode_fn()) return SV_ERR_CUDA;
+  Args args{};
+  args.p = P;
+  args.status = h.status;
+  args.limit_ns = h.wait_limit_ns;
+  args.bf16 = P.dtype == SV_BF16;
+  args.bn = static_cast<int>((P.M + 15) / 16 * 16);
+  args.tiles = static_cast<int>((P.N + kRows - 1) / kRows);
+  args.kblocks = static_cast<int>((P.K + kLinBlk - 1) / kLinBlk);
+  // CTAs of a tile, by the K blocks that the longest-working one takes: waves of
+  // tiles over the clusters of a size that run at once (the product in 8 bits
+  // asked for these: one CTA an SM, as here).
+  int64_t best = INT64_MAX;
+  int clusters = 1;
+  for (int s = 1; s <= kMaxSplit && s <= args.kblocks; ++s) {
+    const int most = s == 1 ? h.num_sms : h.clusters[s];
+    if (most < 1) continue;
+    const int c = args.tiles < most ? args.tiles : most;
+    const int64_t time =
+        static_cast<int64_t>((args.tiles + c - 1) / c) * ((args.kblocks + s - 1) / s);
+    if (time < best) {
+      best = time;
+      args.split = s;
+      clusters = c;
+    }
+  }
+  const int per = (static_cast<int>(P.M) + args.split - 1) / args.split;
+  const int fixed = 1024 + args.split * per * kLanes * 4 + static_cast<int>(sizeof(Ctl));
+  args.stages = (h.smem_optin - fixed) / stage_bytes<kCols>();
+  if (args.stages > kMaxStages) args.stages = kMaxStages;
+  if (args.stages < 2) return SV_ERR_CUDA;
+  const int smem = fixed + args.stages * stage_bytes<kCols>();
+  CUtensorMap w, u, x;
+  if (!lin_encode(&w, P.w, P.ws, P.K, P.N, kRows) ||
+      !lin_encode(&u, kGated ? P.wu : P.w, kGated ? P.wus : P.ws, P.K, P.N, kRows) ||
+      !lin_encode(&x, P.x, P.xs, P.K, P.M, args.bn))
+    return SV_ERR_CUDA;
+  cudaError_t e = cudaFuncSetAttribute(linear_few_kernel<kCols, kGated>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, h.smem_optin);
+  if (e != cudaSuccess) return SV_ERR_CUDA;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = args.split;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(clusters * args.split);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  e = cudaLaunchKernelEx(&cfg, linear_few_kernel<kCols, kGated>, w, u, x, args);
+  return e == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+}
+
+template <bool kGated>
+int launch_cols(const spec_target &h, const LinearParams &P, cudaStream_t stream) {
+  if (P.M <= 16) return launch<16, kGated>(h, P, stream);
+  if (P.M <= 32) return launch<32, kGated>(h, P, stream);
+  if (P.M <= 64) return launch<64, kGated>(h, P, stream);
+  return launch<128, kGated>(h, P, stream);
+}
+
+}  // namespace
+
+int launch_linear_few(const spec_target &h, const LinearParams &P, cudaStream_t stream) {
+  return P.wu ? launch_cols<true>(h, P, stream) : launch_cols<false>(h, P, stream);
+}
+
+}  // namespace sv
