@@ -3,12 +3,178 @@
 //
 //   y = x / sqrt(mean(x^2) + eps) * post,  h = residual + s * gate * y,
 //   out = h / sqrt(mean(h^2) + eps) * weight
+//
+// One pass: a row stays in registers from its load to the stores, through two
+// sums (and the maximum of an E4M3 row), so every input is read once and every
+// output written once; HBM bounds it for many rows, the launch for few.  A thread
+// holds kVec vectors of eight elements; a row takes `wpr` whole warps, and a block
+// several short rows.  Sixteen lanes hold the 128 columns of one scale, so a
+// block's maximum is four shuffles.
 #include "sv_target.cuh"
 
 namespace sv {
 namespace {
 
-constexpr int kThreads = 512;
+// `red` holds one value for each of a row's wpr warps; all threads of the block
+// take part.
+template <class Op>
+__device__ __forceinline__ float row_reduce(float v, float *red, int wpr, int warp, int lane,
+                                            Op op) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = op(v, __shfl_xor_sync(0xffffffffu, v, o));
+  if (wpr == 1) return v;
+  if (lane == 0) red[warp] = v;
+  __syncthreads();
+  const int first = warp / wpr * wpr;
+  float r = red[first];
+  for (int i = 1; i < wpr; ++i) r = op(r, red[first + i]);
+  return r;
+}
+// scale = max(amax, 1e-30) / 448; y * (1 / scale) in place of y / scale is one
+// more rounding in fp32, 2^-24 against E4M3's 2^-4.
+__device__ __forceinline__ float e4m3_scale(float amax) { return max_nan(amax, 1e-30f) / 448.0f; }
+__device__ __forceinline__ uint2 to_e4m3x8(const float (&y)[8], float inv) {
+  uint32_t h[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    h[i] = __nv_cvt_float2_to_fp8x2(make_float2(y[2 * i] * inv, y[2 * i + 1] * inv),
+                                    __NV_SATFINITE, __NV_E4M3);
+  return make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
+}
+
+template <class T, int kVec, int kQuant, int kMost>
+__global__ void __launch_bounds__(kMost, kMost <= 256 && kVec == 2 ? 4 : 1)
+    block_norm_kernel(const sv_block_norm_t P, int wpr) {
+  __shared__ float red[3][32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * ((blockDim.x >> 5) / wpr) + warp / wpr;
+  const bool live = row < P.rows;
+  const int t0 = (warp % wpr) * 32 + lane, step = wpr * 32;
+  const int d = static_cast<int>(P.d), nvec = d >> 3;
+  const T *post = static_cast<const T *>(P.post_weight), *w = static_cast<const T *>(P.weight);
+  pdl_wait();
+  pdl_launch_dependents();
+  const auto add = [](float a, float b) { return a + b; };
+  float h[kVec][8];
+  Vec8<T> rv[kVec];
+  {
+    const T *x = static_cast<const T *>(P.x) + row * P.x_stride;
+    const T *r = static_cast<const T *>(P.residual) + row * P.residual_stride;
+    Vec8<T> xv[kVec];
+#pragma unroll
+    for (int v = 0; v < kVec; ++v) {
+      const int i = t0 + v * step;
+      if (live && i < nvec) {
+        xv[v] = load8(x + 8 * i);
+        rv[v] = load8(r + 8 * i);
+      }
+    }
+    float ss = 0.0f;
+#pragma unroll
+    for (int v = 0; v < kVec; ++v) {
+      const bool in = live && t0 + v * step < nvec;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        h[v][e] = in ? to_float(xv[v].e[e]) : 0.0f;
+        ss = fmaf(h[v][e], h[v][e], ss);
+      }
+    }
+    if (post) {
+      ss = row_reduce(ss, red[0], wpr, warp, lane, add);
+      const float inv = 1.0f / sqrtf(ss / static_cast<float>(d) + P.eps);
+#pragma unroll
+      for (int v = 0; v < kVec; ++v) {
+        const int i = t0 + v * step;
+        if (live && i < nvec) {
+          const Vec8<T> pv = load8(post + 8 * i);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) h[v][e] = h[v][e] * inv * to_float(pv.e[e]);
+        }
+      }
+    }
+  }
+  float scale = P.branch_scale;
+  const T *gate = P.gate ? static_cast<const T *>(P.gate) + row * P.gate_row : nullptr;
+  if (gate && P.gate_col == 0) {
+    if (live) scale *= to_float(gate[0]);
+    gate = nullptr;
+  }
+  float ss = 0.0f;
+#pragma unroll
+  for (int v = 0; v < kVec; ++v) {
+    const int i = t0 + v * step;
+    if (live && i < nvec) {
+      if (gate) {
+        const Vec8<T> gv = load8(gate + 8 * i);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) h[v][e] *= to_float(gv.e[e]);
+      }
+      Vec8<T> o;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        h[v][e] = fmaf(scale, h[v][e], to_float(rv[v].e[e]));
+        ss = fmaf(h[v][e], h[v][e], ss);
+        o.e[e] = from_float<T>(h[v][e]);
+      }
+      if (P.residual_out)
+        store8(static_cast<T *>(P.residual_out) + row * P.residual_out_stride + 8 * i, o);
+    }
+  }
+  ss = row_reduce(ss, red[1], wpr, warp, lane, add);
+  const float inv = 1.0f / sqrtf(ss / static_cast<float>(d) + P.eps);
+
+  float rmax = 0.0f;
+#pragma unroll
+  for (int v = 0; v < kVec; ++v) {
+    const int i = t0 + v * step;
+    const bool in = live && i < nvec;
+    if (in) {
+      const Vec8<T> wv = load8(w + 8 * i);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) h[v][e] = h[v][e] * inv * to_float(wv.e[e]);
+    }
+    if constexpr (kQuant == 0) {
+      if (in) {
+        Vec8<T> o;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o.e[e] = from_float<T>(h[v][e]);
+        store8(static_cast<T *>(P.out) + row * P.out_stride + 8 * i, o);
+      }
+    } else {
+      // lanes past the row hold zeros
+      float m = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) m = max_nan(m, fabsf(h[v][e]));
+      if constexpr (kQuant == 1) {
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+        const float s = e4m3_scale(m);
+        if (in) {
+          *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(P.out) + row * d + 8 * i) =
+              to_e4m3x8(h[v], 1.0f / s);
+          if ((i & 15) == 0) P.scale[row * ((d + 127) / 128) + (i >> 4)] = s;
+        }
+      } else {
+        rmax = max_nan(rmax, m);
+      }
+    }
+  }
+  if constexpr (kQuant == 2) {
+    rmax = row_reduce(rmax, red[2], wpr, warp, lane,
+                      [](float a, float b) { return max_nan(a, b); });
+    const float s = e4m3_scale(rmax), inv_s = 1.0f / s;
+#pragma unroll
+    for (int v = 0; v < kVec; ++v) {
+      const int i = t0 + v * step;
+      if (live && i < nvec)
+        *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(P.out) + row * d + 8 * i) =
+            to_e4m3x8(h[v], inv_s);
+    }
+    if (live && t0 == 0) P.scale[row] = s;
+  }
+}
+
+constexpr int kThreads = 512;  // of the form below
 
 template <class Op>
 __device__ __forceinline__ float block_reduce(float v, float *red, Op op) {
@@ -21,7 +187,7 @@ __device__ __forceinline__ float block_reduce(float v, float *red, Op op) {
   return r;
 }
 
-// One block a row, the row read once for each of the sums, the maximum (row
+// Rows of any width, stride and alignment: one block a row, the row read once for each of the sums, the maximum (row
 // scale) and the output.  A thread rereads only elements that it writes itself
 // and writes in the last pass alone, so the in-place forms hold.
 template <class T>
@@ -114,19 +280,55 @@ __global__ void __launch_bounds__(kThreads) block_norm_any_kernel(const sv_block
   });
 }
 
+template <class T, int kVec, int kMost>
+cudaError_t launch_block(const sv_block_norm_t &a, int wpr, int per_block, cudaStream_t stream) {
+  const dim3 grid(static_cast<unsigned>((a.rows + per_block - 1) / per_block));
+  const dim3 block(32 * wpr * per_block);
+  if (a.group < 0)
+    return launch_chained(block_norm_kernel<T, kVec, 0, kMost>, grid, block, 0, stream, a, wpr);
+  if (a.group > 0)
+    return launch_chained(block_norm_kernel<T, kVec, 1, kMost>, grid, block, 0, stream, a, wpr);
+  return launch_chained(block_norm_kernel<T, kVec, 2, kMost>, grid, block, 0, stream, a, wpr);
+}
+template <class T, int kVec>
+cudaError_t launch_vec(const sv_block_norm_t &a, cudaStream_t stream) {
+  const int wpr = static_cast<int>((a.d / 8 + 32 * kVec - 1) / (32 * kVec));
+  const int per_block = wpr >= 4 ? 1 : 4 / wpr;
+  return wpr * per_block <= 8 ? launch_block<T, kVec, 256>(a, wpr, per_block, stream)
+                              : launch_block<T, kVec, 1024>(a, wpr, per_block, stream);
+}
+
 template <class T>
-cudaError_t launch_typed(const sv_block_norm_t &a, cudaStream_t stream) {
-  return launch_chained(block_norm_any_kernel<T>, dim3(static_cast<unsigned>(a.rows)),
-                        dim3(kThreads), 0, stream, a);
+cudaError_t launch_typed(const sv_block_norm_t &a, int num_sms, cudaStream_t stream) {
+  auto ok = [&](const void *p, int64_t stride) {
+    return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 &&
+           (a.rows == 1 || stride * static_cast<int64_t>(sizeof(T)) % 16 == 0);
+  };
+  const bool vec = a.d % 8 == 0 && a.d <= 32768 && ok(a.x, a.x_stride) &&
+                   ok(a.residual, a.residual_stride) && ok(a.weight, 0) && ok(a.post_weight, 0) &&
+                   (a.gate_col == 0 || ok(a.gate, a.gate_row)) &&
+                   (!a.residual_out || ok(a.residual_out, a.residual_out_stride)) &&
+                   (a.group >= 0 ? (reinterpret_cast<uintptr_t>(a.out) & 7u) == 0
+                                 : ok(a.out, a.out_stride));
+  if (!vec)
+    return launch_chained(block_norm_any_kernel<T>, dim3(static_cast<unsigned>(a.rows)),
+                          dim3(kThreads), 0, stream, a);
+  const int64_t nvec = a.d / 8;
+  const int kvec = nvec > 2048 ? 4 : (a.rows <= num_sms && nvec <= 1024) || nvec <= 128 ? 1 : 2;
+  switch (kvec) {
+    case 1: return launch_vec<T, 1>(a, stream);
+    case 2: return launch_vec<T, 2>(a, stream);
+    default: return launch_vec<T, 4>(a, stream);
+  }
 }
 
 }  // namespace
 
 cudaError_t launch_block_norm(const sv_block_norm_t &a, int num_sms, cudaStream_t stream) {
   switch (a.dtype) {
-    case SV_BF16: return launch_typed<__nv_bfloat16>(a, stream);
-    case SV_FP16: return launch_typed<__half>(a, stream);
-    default: return launch_typed<float>(a, stream);
+    case SV_BF16: return launch_typed<__nv_bfloat16>(a, num_sms, stream);
+    case SV_FP16: return launch_typed<__half>(a, num_sms, stream);
+    default: return launch_typed<float>(a, num_sms, stream);
   }
 }
 
