@@ -16,7 +16,8 @@ namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kBytes = 16;          // of a load
-constexpr int kCap = 1024;          // candidates of a tile
+constexpr int kCap = 2048;          // candidates that wait to be ranked
+constexpr int kFlush = 128;         // of these are ranked
 constexpr int kMaxCluster = 8;
 
 // Order of the alternatives: the larger logit first, of equal ones the smaller
@@ -45,7 +46,7 @@ struct Shared {
   uint64_t list[2][SV_MAX_TOP];
   uint64_t cand[kCap + SV_MAX_TOP];
   float red[3][kWarps];
-  int count;
+  int count[3];  // candidates of the tiles, in turn
 };
 
 // A tile of a row in registers: kVec loads of 16 bytes a thread.
@@ -78,6 +79,16 @@ struct Tile {
           e[k] = j < end && e0 + k >= 0 && e0 + k < V ? row[e0 + k] : from_float<T>(-INFINITY);
         v[i] = *reinterpret_cast<const uint4 *>(e);
       }
+    }
+  }
+  // The largest element of each load (a NaN stays).
+  __device__ __forceinline__ void maxima(float (&most)[kVec]) const {
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) {
+      most[i] = max_nan(at(i * kWidth), at(i * kWidth + 1));
+#pragma unroll
+      for (int k = 2; k < kWidth; k += 2)
+        most[i] = max3_nan(most[i], at(i * kWidth + k), at(i * kWidth + k + 1));
     }
   }
   __device__ __forceinline__ static int index(int i, int first, int lead) {
@@ -120,7 +131,7 @@ __device__ __forceinline__ V remote(const V *p, uint32_t rank) {
 
 // One cluster a row, a part of it for each CTA.
 template <class T>
-__global__ void __launch_bounds__(kThreads, 3)
+__global__ void __launch_bounds__(kThreads, 2)
     log_probs_kernel(const sv_log_probs_t P, int *status) {
   using R = Tile<T>;
   __shared__ Shared sh;
@@ -142,15 +153,37 @@ __global__ void __launch_bounds__(kThreads, 3)
   float m = -INFINITY, s = 0.0f, t = 0.0f;  // of this thread's elements, d in log2
   int found = 0, cur = 0;                   // the list's keys and its buffer
   uint32_t lim = kLowest;                   // ordered values from here are candidates
+  // Candidates that wait to be ranked.  A tile counts its own in a counter of three
+  // in turn, which the next tile reads behind its barrier and the one after that
+  // clears, so that one barrier a tile serves.
+  int waiting = 0, turn = 0, last = -1;
+  if (tid < 3) sh.count[tid] = 0;
+  // Ranks the list's keys and the n candidates that wait.
+  auto rank_all = [&](int n) {
+    for (int i = tid; i < found; i += kThreads) sh.cand[n + i] = sh.list[cur][i];
+    __syncthreads();
+    n += found;
+    cur ^= 1;
+    rank_keys(sh.cand, n, top, sh.list[cur]);
+    __syncthreads();
+    waiting = 0;
+    last = -1;
+    found = min(n, top);
+    if (found == top) lim = max(lim, static_cast<uint32_t>(sh.list[cur][top - 1] >> 32) + 1);
+  };
+  R tile, next;
+  next.load(x, lead, V, begin + tid, end);
   for (int v0 = begin; v0 < end; v0 += kThreads * R::kVec) {
     const int first = v0 + tid;
-    R tile;
-    tile.load(x, lead, V, first, end);
-    float most = tile.at(0);
+    tile = next;
+    if (v0 + kThreads * R::kVec < end) next.load(x, lead, V, first + kThreads * R::kVec, end);
+    float mv[R::kVec];
+    tile.maxima(mv);
+    float most = mv[0];
 #pragma unroll
-    for (int i = 1; i < 32; ++i) most = max_nan(most, tile.at(i));
+    for (int i = 1; i < R::kVec; ++i) most = max_nan(most, mv[i]);
     const float m2 = max_nan(m, most);
-    if (!(m2 <= m) && m2 != m) {  // larger, or a NaN
+    if (!(m2 <= m)) {  // larger, or a NaN
       const float d = fmaxf((m - m2) * c2, -200.0f), e = ex2(d);
       t = e * fmaf(d, s, t);
       s *= e;
@@ -176,9 +209,18 @@ __global__ void __launch_bounds__(kThreads, 3)
     if (top == 0) continue;
 
     // ---- alternatives ----
-    uint32_t high = ordered(most);
-    int n = __syncthreads_count(high >= lim);
+    const uint32_t high = ordered(most);
+    int n = __syncthreads_count(high >= lim);  // and the last tile's candidates are there
+    if (last >= 0) waiting += sh.count[last];
+    last = -1;
+    turn = turn == 2 ? 0 : turn + 1;
+    if (tid == 0) sh.count[turn == 2 ? 0 : turn + 1] = 0;  // the next tile's
+    if (waiting > kFlush) {
+      rank_all(waiting);
+      n = __syncthreads_count(high >= lim);
+    }
     if (n == 0) continue;
+    last = turn;
     // As many threads have a candidate as there are alternatives: their maxima
     // bound the last one from below, and what lies under it is none.  Any bound
     // that `top` maxima reach will do, so the search ends early.
@@ -186,35 +228,39 @@ __global__ void __launch_bounds__(kThreads, 3)
       uint32_t lo = lim, hi = kHighest + 1;  // count(lo) >= top > count(hi)
       while (hi - lo > 1) {
         const uint32_t mid = lo + (hi - lo) / 2;
-        const int c = __syncthreads_count(high >= mid);
-        if (c >= top) {
+        n = __syncthreads_count(high >= mid);
+        if (n >= top) {
           lo = mid;
-          if (c <= top + 16) break;
+          if (n <= top + 16) break;
         } else {
           hi = mid;
         }
       }
       lim = lo;
+      n = kThreads;  // (as many as there may be, where the search ended on a tie)
     }
-    if (tid == 0) sh.count = 0;
-    __syncthreads();
     const float limf = from_ordered(lim);
     if (high >= lim) {
 #pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        const float y = tile.at(i);
-        const int id = R::index(i, first, lead);
-        if (y >= limf && id >= 0 && id < V && first + i / R::kWidth * kThreads < end) {
-          const int at = atomicAdd(&sh.count, 1);
+      for (int i = 0; i < R::kVec; ++i) {
+        if (!(mv[i] >= limf) && !isnan(mv[i])) continue;
+#pragma unroll
+        for (int k = 0; k < R::kWidth; ++k) {
+          const float y = tile.at(i * R::kWidth + k);
+          if (!(y >= limf)) continue;
+          const int id = R::index(i * R::kWidth + k, first, lead);
+          if (id < 0 || id >= V || first + i * kThreads >= end) continue;
+          const int at = waiting + atomicAdd(&sh.count[turn], 1);
           if (at < kCap) sh.cand[at] = order_key(y, id);
         }
       }
     }
+    if (waiting + n * 32 <= kCap) continue;  // there was room for all of them
     __syncthreads();
-    n = sh.count;
-    if (n > kCap) {
-      // Too many (equal) ones: the value of the last alternative among them, then
-      // the ids of those that equal it, by halving.
+    int all = waiting + sh.count[turn];
+    if (all > kCap) {
+      // Too many (equal) ones: the value of the tile's last alternative, then the
+      // ids of those that equal it, by halving.
       auto count = [&](auto &&want) {
         int c = 0;
 #pragma unroll
@@ -249,7 +295,9 @@ __global__ void __launch_bounds__(kThreads, 3)
         else
           below = mid;
       }
-      if (tid == 0) sh.count = 0;
+      // (what waited before stays; the tile's own take the places after it)
+      __syncthreads();
+      if (tid == 0) sh.count[turn] = 0;
       __syncthreads();
 #pragma unroll
       for (int i = 0; i < 32; ++i) {
@@ -258,19 +306,17 @@ __global__ void __launch_bounds__(kThreads, 3)
         const int id = R::index(i, first, lead);
         const bool in = id >= 0 && id < V && first + i / R::kWidth * kThreads < end;
         if (in && u <= kHighest && (u > lo || (u == lo && id <= upto)))
-          sh.cand[atomicAdd(&sh.count, 1)] = order_key(y, id);
+          sh.cand[waiting + atomicAdd(&sh.count[turn], 1)] = order_key(y, id);
       }
       __syncthreads();
-      n = sh.count;
+      all = waiting + sh.count[turn];
     }
-    for (int i = tid; i < found; i += kThreads) sh.cand[n + i] = sh.list[cur][i];
+    rank_all(all);
+  }
+  if (top) {
     __syncthreads();
-    n += found;
-    cur ^= 1;
-    rank_keys(sh.cand, n, top, sh.list[cur]);
-    __syncthreads();
-    found = min(n, top);
-    if (found == top) lim = static_cast<uint32_t>(sh.list[cur][top - 1] >> 32) + 1;
+    if (last >= 0) waiting += sh.count[last];
+    if (waiting) rank_all(waiting);
   }
 
   // ---- the parts of a CTA, then those of the row ----
