@@ -17,8 +17,9 @@ namespace {
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kBytes = 16;          // of a load
 constexpr int kCap = 2048;          // candidates that wait to be ranked
-constexpr int kFlush = 128;         // of these are ranked
-constexpr int kMaxCluster = 8;
+constexpr int kFew = 256;           // of these that are ranked after a last bound
+constexpr int kSlack = 8;           // alternatives more than asked for that a bound may leave
+constexpr int kMaxCluster = kWarps;
 
 // Order of the alternatives: the larger logit first, of equal ones the smaller
 // id.  The logit's bits become an unsigned number of the same order; -0 counts
@@ -44,17 +45,36 @@ struct Part {
 struct Shared {
   Part part;
   uint64_t list[2][SV_MAX_TOP];
-  uint64_t cand[kCap + SV_MAX_TOP];
+  uint64_t cand[kCap + SV_MAX_TOP], few[kFew];
   float red[3][kWarps];
-  int count[3];  // candidates of the tiles, in turn
+  int count, few_count;
 };
 
-// A tile of a row in registers: kVec loads of 16 bytes a thread.
+// Where a CTA's part of a row lies, in loads of 16 bytes; the row's elements
+// start `lead` into its first one.
+template <class T>
+struct Span {
+  static constexpr int kWidth = kBytes / sizeof(T);  // elements of a load
+  static constexpr int kVec = 32 / kWidth;           // loads of a thread in a tile
+  static constexpr int kTile = kThreads * kVec;      // of a tile
+  const T *row;
+  int lead, V, begin, end;
+  // Element i of a thread whose first load of the tile is `first`; negative or
+  // beyond the row where there is none.
+  __device__ __forceinline__ int id(int i, int first) const {
+    return (first + i / kWidth * kThreads) * kWidth + i % kWidth - lead;
+  }
+  __device__ __forceinline__ bool has(int i, int first) const {
+    const int e = id(i, first);
+    return e >= 0 && e < V && first + i / kWidth * kThreads < end;
+  }
+};
+
+// A tile in registers, 32 elements a thread.
 template <class T>
 struct Tile {
-  static constexpr int kWidth = kBytes / sizeof(T);  // elements of a load
-  static constexpr int kVec = 32 / kWidth;           // 32 elements a thread
-  uint4 v[kVec];
+  using S = Span<T>;
+  uint4 v[S::kVec];
   __device__ __forceinline__ float at(int i) const {
     const uint32_t *w = reinterpret_cast<const uint32_t *>(v);
     if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
@@ -64,47 +84,187 @@ struct Tile {
     const __half2 f = *reinterpret_cast<const __half2 *>(&h);
     return i & 1 ? __high2float(f) : __low2float(f);
   }
-  // Loads vectors first, first + kThreads, ... below `end`; the elements of a row
-  // of V start `lead` into its first vector.  What is outside is -inf.
-  __device__ __forceinline__ void load(const T *row, int lead, int V, int first, int end) {
+  // The tile from load v0 on.  What is outside the row or the part is -inf.
+  __device__ __forceinline__ void load(const S &s, int v0) {
+    const int first = v0 + threadIdx.x;
+    const bool inside = (v0 > 0 || s.lead == 0) && v0 + S::kTile <= s.end &&
+                        (v0 + S::kTile) * S::kWidth - s.lead <= s.V;
+    if (inside) {
+      const uint4 *p = reinterpret_cast<const uint4 *>(s.row + (first * S::kWidth - s.lead));
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) {
-      const int j = first + i * kThreads, e0 = j * kWidth - lead;
-      if (j < end && e0 >= 0 && e0 + kWidth <= V) {
-        v[i] = __ldcs(reinterpret_cast<const uint4 *>(row + e0));
+      for (int i = 0; i < S::kVec; ++i) v[i] = __ldcs(p + i * kThreads);
+      return;
+    }
+#pragma unroll
+    for (int i = 0; i < S::kVec; ++i) {
+      const int j = first + i * kThreads, e0 = j * S::kWidth - s.lead;
+      if (j < s.end && e0 >= 0 && e0 + S::kWidth <= s.V) {
+        v[i] = __ldcs(reinterpret_cast<const uint4 *>(s.row + e0));
       } else {
-        alignas(16) T e[kWidth];
+        alignas(16) T e[S::kWidth];
 #pragma unroll
-        for (int k = 0; k < kWidth; ++k)
-          e[k] = j < end && e0 + k >= 0 && e0 + k < V ? row[e0 + k] : from_float<T>(-INFINITY);
+        for (int k = 0; k < S::kWidth; ++k)
+          e[k] = j < s.end && e0 + k >= 0 && e0 + k < s.V ? s.row[e0 + k]
+                                                          : from_float<T>(-INFINITY);
         v[i] = *reinterpret_cast<const uint4 *>(e);
       }
     }
   }
   // The largest element of each load (a NaN stays).
-  __device__ __forceinline__ void maxima(float (&most)[kVec]) const {
+  __device__ __forceinline__ void maxima(float (&most)[S::kVec]) const {
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) {
-      most[i] = max_nan(at(i * kWidth), at(i * kWidth + 1));
+    for (int i = 0; i < S::kVec; ++i) {
+      most[i] = max_nan(at(i * S::kWidth), at(i * S::kWidth + 1));
 #pragma unroll
-      for (int k = 2; k < kWidth; k += 2)
-        most[i] = max3_nan(most[i], at(i * kWidth + k), at(i * kWidth + k + 1));
+      for (int k = 2; k < S::kWidth; k += 2)
+        most[i] = max3_nan(most[i], at(i * S::kWidth + k), at(i * S::kWidth + k + 1));
     }
   }
-  __device__ __forceinline__ static int index(int i, int first, int lead) {
-    return (first + i / kWidth * kThreads) * kWidth + i % kWidth - lead;
+  // Writes the elements from `lim` on as candidates; counts those that do not fit.
+  __device__ __forceinline__ void push(const S &s, int v0, const float (&most)[S::kVec],
+                                       uint32_t lim, Shared &sh) const {
+    const int first = v0 + threadIdx.x;
+    const float limf = from_ordered(lim);
+#pragma unroll
+    for (int i = 0; i < S::kVec; ++i) {
+      if (most[i] < limf) continue;  // (goes on with a NaN)
+#pragma unroll
+      for (int k = i * S::kWidth; k < (i + 1) * S::kWidth; ++k) {
+        if (!(at(k) >= limf) || !s.has(k, first)) continue;
+        const int j = atomicAdd(&sh.count, 1);
+        if (j < kCap) sh.cand[j] = order_key(at(k), s.id(k, first));
+      }
+    }
   }
 };
 
-// The `top` best of the list and the candidates, in order, by counting for each
-// key the greater ones (keys differ).
+// The `top` best of n keys, in order, by counting for each the greater ones (keys
+// differ).
 __device__ __forceinline__ void rank_keys(const uint64_t *keys, int n, int top, uint64_t *out) {
   for (int i = threadIdx.x; i < n; i += kThreads) {
     const uint64_t k = keys[i];
     int r = 0;
+#pragma unroll 4
     for (int j = 0; j < n; ++j) r += keys[j] > k;
     if (r < top) out[r] = k;
   }
+}
+
+// The best keys so far and the bound under which there are none.  All threads of
+// the block call its functions, which agree on n and on what is kept here.
+struct Best {
+  int top;
+  int found = 0, cur = 0;   // the list's keys and its buffer
+  uint32_t lim = kLowest;   // ordered values from here are candidates
+
+  // Ranks the n candidates with the list.
+  __device__ __forceinline__ void rank(int n, Shared &sh) {
+    for (int i = threadIdx.x; i < found; i += kThreads) sh.cand[n + i] = sh.list[cur][i];
+    __syncthreads();
+    n += found;
+    cur ^= 1;
+    rank_keys(sh.cand, n, top, sh.list[cur]);
+    if (threadIdx.x == 0) sh.count = 0;
+    __syncthreads();
+    found = min(n, top);
+    // (what comes later and equals the last one has a larger id)
+    if (found == top) lim = max(lim, static_cast<uint32_t>(sh.list[cur][top - 1] >> 32) + 1);
+  }
+  // As many threads have an element from a bound on as there are alternatives: what
+  // lies under it is none.  Found by halving, and not to the last: a few more than
+  // needed may stay.
+  __device__ __forceinline__ void raise(float most) {
+    const uint32_t high = ordered(most);
+    int n = __syncthreads_count(high >= lim);
+    if (n <= top + kSlack) return;
+    uint32_t lo = lim, hi = kHighest + 1;  // count(lo) >= top > count(hi)
+    while (hi - lo > 1) {
+      const uint32_t mid = lo + (hi - lo) / 2;
+      n = __syncthreads_count(high >= mid);
+      if (n >= top) {
+        lo = mid;
+        if (n <= top + kSlack) break;
+      } else {
+        hi = mid;
+      }
+    }
+    lim = lo;
+  }
+};
+
+// The best of a part whose tiles are taken one by one, however many of their
+// elements equal each other or rise.
+template <class T>
+__device__ __noinline__ Best best_of_each(const Span<T> s, Best best, Shared &sh) {
+  using S = Span<T>;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  best.rank(0, sh);
+  for (int v0 = s.begin; v0 < s.end; v0 += S::kTile) {
+    const int first = v0 + threadIdx.x;
+    Tile<T> tile;
+    tile.load(s, v0);
+    float mv[S::kVec];
+    tile.maxima(mv);
+    float most = mv[0];
+#pragma unroll
+    for (int i = 1; i < S::kVec; ++i) most = max_nan(most, mv[i]);
+    best.raise(most);
+    tile.push(s, v0, mv, best.lim, sh);
+    __syncthreads();
+    int n = sh.count;
+    if (n > kCap) {
+      // The value of the tile's last alternative, then the ids of those that equal
+      // it, by halving.
+      auto count = [&](auto &&want) {
+        int c = 0;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          const uint32_t u = ordered(tile.at(i));
+          c += s.has(i, first) && u <= kHighest && want(u, s.id(i, first));
+        }
+        c = __reduce_add_sync(0xffffffffu, c);
+        __syncthreads();
+        if (lane == 0) sh.red[0][warp] = __int_as_float(c);
+        __syncthreads();
+        c = 0;
+        for (int w = 0; w < kWarps; ++w) c += __float_as_int(sh.red[0][w]);
+        return c;
+      };
+      uint32_t lo = best.lim, hi = kHighest + 1;  // count(lo) >= top > count(hi)
+      while (hi - lo > 1) {
+        const uint32_t mid = lo + (hi - lo) / 2;
+        if (count([&](uint32_t u, int) { return u >= mid; }) >= best.top)
+          lo = mid;
+        else
+          hi = mid;
+      }
+      const int more = count([&](uint32_t u, int) { return u > lo; });
+      int below = -1, upto = s.V - 1;  // ids up to `upto` are enough, up to `below` too few
+      while (upto - below > 1) {
+        const int mid = below + (upto - below) / 2;
+        if (more + count([&](uint32_t u, int id) { return u == lo && id <= mid; }) >= best.top)
+          upto = mid;
+        else
+          below = mid;
+      }
+      __syncthreads();
+      if (threadIdx.x == 0) sh.count = 0;
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        const uint32_t u = ordered(tile.at(i));
+        const int id = s.id(i, first);
+        if (s.has(i, first) && u <= kHighest && (u > lo || (u == lo && id <= upto))) {
+          const int j = atomicAdd(&sh.count, 1);
+          if (j < kCap) sh.cand[j] = order_key(tile.at(i), id);
+        }
+      }
+      __syncthreads();
+      n = min(sh.count, kCap);
+    }
+    best.rank(n, sh);
+  }
+  return best;
 }
 
 // All threads of the cluster.
@@ -131,62 +291,50 @@ __device__ __forceinline__ V remote(const V *p, uint32_t rank) {
 
 // One cluster a row, a part of it for each CTA.
 template <class T>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 2 : 3)
     log_probs_kernel(const sv_log_probs_t P, int *status) {
-  using R = Tile<T>;
+  using S = Span<T>;
   __shared__ Shared sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   uint32_t rank, parts;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
   asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(parts));
   const int64_t row = blockIdx.x / parts;
-  const T *x = static_cast<const T *>(P.logits) + row * P.stride;
   const int V = static_cast<int>(P.V), top = P.top;
-  const int lead = static_cast<int>((reinterpret_cast<uintptr_t>(x) & (kBytes - 1)) / sizeof(T));
-  const int vecs = (lead + V + R::kWidth - 1) / R::kWidth;
-  const int begin = static_cast<int>(static_cast<int64_t>(vecs) * rank / parts);
-  const int end = static_cast<int>(static_cast<int64_t>(vecs) * (rank + 1) / parts);
+  S s;
+  s.row = static_cast<const T *>(P.logits) + row * P.stride;
+  s.V = V;
+  s.lead = static_cast<int>((reinterpret_cast<uintptr_t>(s.row) & (kBytes - 1)) / sizeof(T));
+  const int loads = (s.lead + V + S::kWidth - 1) / S::kWidth;
+  s.begin = static_cast<int>(static_cast<int64_t>(loads) * rank / parts);
+  s.end = static_cast<int>(static_cast<int64_t>(loads) * (rank + 1) / parts);
   const float c2 = 1.4426950408889634f / P.temperature;  // to powers of two
+  if (tid == 0) sh.count = 0;
   pdl_wait();
   pdl_launch_dependents();
 
-  float m = -INFINITY, s = 0.0f, t = 0.0f;  // of this thread's elements, d in log2
-  int found = 0, cur = 0;                   // the list's keys and its buffer
-  uint32_t lim = kLowest;                   // ordered values from here are candidates
-  // Candidates that wait to be ranked.  A tile counts its own in a counter of three
-  // in turn, which the next tile reads behind its barrier and the one after that
-  // clears, so that one barrier a tile serves.
-  int waiting = 0, turn = 0, last = -1;
-  if (tid < 3) sh.count[tid] = 0;
-  // Ranks the list's keys and the n candidates that wait.
-  auto rank_all = [&](int n) {
-    for (int i = tid; i < found; i += kThreads) sh.cand[n + i] = sh.list[cur][i];
-    __syncthreads();
-    n += found;
-    cur ^= 1;
-    rank_keys(sh.cand, n, top, sh.list[cur]);
-    __syncthreads();
-    waiting = 0;
-    last = -1;
-    found = min(n, top);
-    if (found == top) lim = max(lim, static_cast<uint32_t>(sh.list[cur][top - 1] >> 32) + 1);
-  };
-  R tile, next;
-  next.load(x, lead, V, begin + tid, end);
-  for (int v0 = begin; v0 < end; v0 += kThreads * R::kVec) {
-    const int first = v0 + tid;
+  float m = -INFINITY, sum = 0.0f, t = 0.0f;  // of this thread's elements, d in log2
+  Best best;
+  best.top = top;
+  // Candidates are written without a barrier between the tiles of a group, under
+  // a bound found at its start; the groups grow as candidates get rarer.
+  int next_start = 0;
+  Tile<T> tile, next;
+  next.load(s, s.begin);
+  int number = 0;
+  for (int v0 = s.begin; v0 < s.end; v0 += S::kTile, ++number) {
     tile = next;
-    if (v0 + kThreads * R::kVec < end) next.load(x, lead, V, first + kThreads * R::kVec, end);
-    float mv[R::kVec];
+    if (v0 + S::kTile < s.end) next.load(s, v0 + S::kTile);
+    float mv[S::kVec];
     tile.maxima(mv);
     float most = mv[0];
 #pragma unroll
-    for (int i = 1; i < R::kVec; ++i) most = max_nan(most, mv[i]);
+    for (int i = 1; i < S::kVec; ++i) most = max_nan(most, mv[i]);
     const float m2 = max_nan(m, most);
     if (!(m2 <= m)) {  // larger, or a NaN
       const float d = fmaxf((m - m2) * c2, -200.0f), e = ex2(d);
-      t = e * fmaf(d, s, t);
-      s *= e;
+      t = e * fmaf(d, sum, t);
+      sum *= e;
       m = m2;
     }
     if (m > -INFINITY) {
@@ -203,120 +351,38 @@ __global__ void __launch_bounds__(kThreads, 2)
         t2 = fma2(pair2(d.x, d.y), e, t2);
       }
       const float2 a = unpair2(s2), b = unpair2(t2);
-      s += a.x + a.y;
+      sum += a.x + a.y;
       t += b.x + b.y;
     }
-    if (top == 0) continue;
-
-    // ---- alternatives ----
-    const uint32_t high = ordered(most);
-    int n = __syncthreads_count(high >= lim);  // and the last tile's candidates are there
-    if (last >= 0) waiting += sh.count[last];
-    last = -1;
-    turn = turn == 2 ? 0 : turn + 1;
-    if (tid == 0) sh.count[turn == 2 ? 0 : turn + 1] = 0;  // the next tile's
-    if (waiting > kFlush) {
-      rank_all(waiting);
-      n = __syncthreads_count(high >= lim);
+    if (top) {
+      if (number == next_start) {
+        best.raise(m);
+        next_start = number == 0 ? 2 : number < 32 ? 4 * number : number + 32;
+      }
+      if (ordered(most) >= best.lim) tile.push(s, v0, mv, best.lim, sh);
     }
-    if (n == 0) continue;
-    last = turn;
-    // As many threads have a candidate as there are alternatives: their maxima
-    // bound the last one from below, and what lies under it is none.  Any bound
-    // that `top` maxima reach will do, so the search ends early.
-    if (n > top + 16) {
-      uint32_t lo = lim, hi = kHighest + 1;  // count(lo) >= top > count(hi)
-      while (hi - lo > 1) {
-        const uint32_t mid = lo + (hi - lo) / 2;
-        n = __syncthreads_count(high >= mid);
-        if (n >= top) {
-          lo = mid;
-          if (n <= top + 16) break;
-        } else {
-          hi = mid;
-        }
-      }
-      lim = lo;
-      n = kThreads;  // (as many as there may be, where the search ended on a tie)
-    }
-    const float limf = from_ordered(lim);
-    if (high >= lim) {
-#pragma unroll
-      for (int i = 0; i < R::kVec; ++i) {
-        if (!(mv[i] >= limf) && !isnan(mv[i])) continue;
-#pragma unroll
-        for (int k = 0; k < R::kWidth; ++k) {
-          const float y = tile.at(i * R::kWidth + k);
-          if (!(y >= limf)) continue;
-          const int id = R::index(i * R::kWidth + k, first, lead);
-          if (id < 0 || id >= V || first + i * kThreads >= end) continue;
-          const int at = waiting + atomicAdd(&sh.count[turn], 1);
-          if (at < kCap) sh.cand[at] = order_key(y, id);
-        }
-      }
-    }
-    if (waiting + n * 32 <= kCap) continue;  // there was room for all of them
-    __syncthreads();
-    int all = waiting + sh.count[turn];
-    if (all > kCap) {
-      // Too many (equal) ones: the value of the tile's last alternative, then the
-      // ids of those that equal it, by halving.
-      auto count = [&](auto &&want) {
-        int c = 0;
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          const int id = R::index(i, first, lead);
-          const bool in = id >= 0 && id < V && first + i / R::kWidth * kThreads < end;
-          const uint32_t u = ordered(tile.at(i));
-          c += in && u <= kHighest && want(u, id);
-        }
-        c = __reduce_add_sync(0xffffffffu, c);
-        __syncthreads();
-        if (lane == 0) sh.red[0][warp] = __int_as_float(c);
-        __syncthreads();
-        c = 0;
-        for (int w = 0; w < kWarps; ++w) c += __float_as_int(sh.red[0][w]);
-        return c;
-      };
-      uint32_t lo = lim, hi = kHighest + 1;  // count(lo) >= top > count(hi)
-      while (hi - lo > 1) {
-        const uint32_t mid = lo + (hi - lo) / 2;
-        if (count([&](uint32_t u, int) { return u >= mid; }) >= top)
-          lo = mid;
-        else
-          hi = mid;
-      }
-      const int more = count([&](uint32_t u, int) { return u > lo; });
-      int below = -1, upto = V - 1;  // ids up to `upto` are enough, up to `below` too few
-      while (upto - below > 1) {
-        const int mid = below + (upto - below) / 2;
-        if (more + count([&](uint32_t u, int id) { return u == lo && id <= mid; }) >= top)
-          upto = mid;
-        else
-          below = mid;
-      }
-      // (what waited before stays; the tile's own take the places after it)
-      __syncthreads();
-      if (tid == 0) sh.count[turn] = 0;
-      __syncthreads();
-#pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        const float y = tile.at(i);
-        const uint32_t u = ordered(y);
-        const int id = R::index(i, first, lead);
-        const bool in = id >= 0 && id < V && first + i / R::kWidth * kThreads < end;
-        if (in && u <= kHighest && (u > lo || (u == lo && id <= upto)))
-          sh.cand[waiting + atomicAdd(&sh.count[turn], 1)] = order_key(y, id);
-      }
-      __syncthreads();
-      all = waiting + sh.count[turn];
-    }
-    rank_all(all);
   }
   if (top) {
-    __syncthreads();
-    if (last >= 0) waiting += sh.count[last];
-    if (waiting) rank_all(waiting);
+    if (tid == 0) sh.few_count = 0;
+    best.raise(m);
+    const int n = sh.count;
+    if (n > kCap) {
+      best = best_of_each(s, best, sh);  // some were not written
+    } else {
+      for (int i = tid; i < n; i += kThreads) {
+        const uint64_t k = sh.cand[i];
+        if (k >> 32 < best.lim) continue;
+        const int j = atomicAdd(&sh.few_count, 1);
+        if (j < kFew) sh.few[j] = k;
+      }
+      __syncthreads();
+      const int few = sh.few_count;
+      if (few <= kFew)
+        rank_keys(sh.few, few, top, sh.list[0]);
+      else
+        rank_keys(sh.cand, n, top, sh.list[0]);
+      best.found = min(few, top);
+    }
   }
 
   // ---- the parts of a CTA, then those of the row ----
@@ -329,73 +395,81 @@ __global__ void __launch_bounds__(kThreads, 2)
   for (int w = 1; w < kWarps; ++w) mb = max_nan(mb, sh.red[0][w]);
   {
     const float d = fmaxf((m - mb) * c2, -200.0f), e = m > -INFINITY ? ex2(d) : 0.0f;
-    t = e * fmaf(d, s, t);
-    s *= e;
+    t = e * fmaf(d, sum, t);
+    sum *= e;
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
-    s += __shfl_xor_sync(0xffffffffu, s, o);
+    sum += __shfl_xor_sync(0xffffffffu, sum, o);
     t += __shfl_xor_sync(0xffffffffu, t, o);
   }
   if (lane == 0) {
-    sh.red[1][warp] = s;
+    sh.red[1][warp] = sum;
     sh.red[2][warp] = t;
   }
   __syncthreads();
-  if (tid == 0) {
-    s = t = 0.0f;
-    for (int w = 0; w < kWarps; ++w) {
-      s += sh.red[1][w];
-      t += sh.red[2][w];
-    }
-    sh.part.m = mb;
-    sh.part.s = s;
-    sh.part.t = t;
-    sh.part.found = found;
+  sum = t = 0.0f;
+  for (int w = 0; w < kWarps; ++w) {
+    sum += sh.red[1][w];
+    t += sh.red[2][w];
   }
-  for (int i = tid; i < found; i += kThreads) sh.part.best[i] = sh.list[cur][i];
-  if (parts > 1) cluster_sync();
-  else __syncthreads();
-  if (rank == 0) {
-    float rm = -INFINITY, rs = 0.0f, rt = 0.0f;
-    int keys = 0;
-    for (uint32_t q = 0; q < parts; ++q) rm = max_nan(rm, remote(&sh.part.m, q));
-    for (uint32_t q = 0; q < parts; ++q) {
-      const float pm = remote(&sh.part.m, q), ps = remote(&sh.part.s, q);
-      const float d = fmaxf((pm - rm) * c2, -200.0f), e = pm > -INFINITY ? ex2(d) : 0.0f;
-      rt += e * fmaf(d, ps, remote(&sh.part.t, q));
-      rs = fmaf(e, ps, rs);
-      const int f = remote(&sh.part.found, q);
-      for (int i = tid; i < f; i += kThreads) sh.cand[keys + i] = remote(&sh.part.best[i], q);
-      keys += f;
+  const uint64_t *keys = sh.list[best.cur];
+  if (parts > 1) {
+    if (tid == 0) {
+      sh.part.m = mb;
+      sh.part.s = sum;
+      sh.part.t = t;
+      sh.part.found = best.found;
     }
-    const bool fine = isfinite(rm);
-    const float log_s = fine ? logf(rs) : NAN, inv_t = 1.0f / P.temperature;
-    if (tid == 0 && P.entropy) P.entropy[row] = log_s - 0.69314718055994531f * (rt / rs);
-    for (int i = tid; i < P.n; i += kThreads) {
-      const int id = P.tokens[row * P.n + i];
-      float y = 0.0f;
-      if (id >= 0 && id < V) {
-        y = (to_float(x[id]) - rm) * inv_t - log_s;
-      } else if (id != -1) {
-        y = NAN;
-        set_status(status, SV_ERR_TOKEN);
+    for (int i = tid; i < best.found; i += kThreads) sh.part.best[i] = keys[i];
+    cluster_sync();
+    if (rank == 0) {
+      // a warp for each part; keys that a part lacks are 0, below every other
+      if (warp < static_cast<int>(parts)) {
+        if (lane == 0) sh.red[0][warp] = remote(&sh.part.m, warp);
+        if (lane == 1) sh.red[1][warp] = remote(&sh.part.s, warp);
+        if (lane == 2) sh.red[2][warp] = remote(&sh.part.t, warp);
+        const int f = remote(&sh.part.found, warp);
+        for (int i = lane; i < top; i += 32)
+          sh.cand[warp * top + i] = i < f ? remote(&sh.part.best[i], warp) : 0;
       }
-      P.log_probs[row * P.n + i] = y;
-    }
-    if (top) {
       __syncthreads();
-      rank_keys(sh.cand, keys, top, sh.list[0]);
-      __syncthreads();
-      for (int i = tid; i < top; i += kThreads) {
-        const uint64_t k = sh.list[0][i];
-        P.top_ids[row * top + i] = fine ? static_cast<int>(~static_cast<uint32_t>(k)) : -1;
-        P.top_log_probs[row * top + i] =
-            fine ? (from_ordered(static_cast<uint32_t>(k >> 32)) - rm) * inv_t - log_s : NAN;
+      mb = sh.red[0][0];
+      for (uint32_t q = 1; q < parts; ++q) mb = max_nan(mb, sh.red[0][q]);
+      sum = t = 0.0f;
+      for (uint32_t q = 0; q < parts; ++q) {
+        const float pm = sh.red[0][q];
+        const float d = fmaxf((pm - mb) * c2, -200.0f), e = pm > -INFINITY ? ex2(d) : 0.0f;
+        t += e * fmaf(d, sh.red[1][q], sh.red[2][q]);
+        sum = fmaf(e, sh.red[1][q], sum);
       }
+      keys = sh.list[0];
+      rank_keys(sh.cand, static_cast<int>(parts) * top, top, sh.list[0]);
+      __syncthreads();
     }
+    cluster_sync();  // nobody reads a CTA that is gone
   }
-  if (parts > 1) cluster_sync();  // nobody reads a CTA that is gone
+  if (rank != 0) return;
+  const bool fine = isfinite(mb);
+  const float log_s = fine ? logf(sum) : NAN, inv_t = 1.0f / P.temperature;
+  if (tid == 0 && P.entropy) P.entropy[row] = log_s - 0.69314718055994531f * (t / sum);
+  for (int i = tid; i < P.n; i += kThreads) {
+    const int id = P.tokens[row * P.n + i];
+    float y = 0.0f;
+    if (id >= 0 && id < V) {
+      y = (to_float(s.row[id]) - mb) * inv_t - log_s;
+    } else if (id != -1) {
+      y = NAN;
+      set_status(status, SV_ERR_TOKEN);
+    }
+    P.log_probs[row * P.n + i] = y;
+  }
+  for (int i = tid; i < top; i += kThreads) {
+    const uint64_t k = keys[i];
+    P.top_ids[row * top + i] = fine ? static_cast<int>(~static_cast<uint32_t>(k)) : -1;
+    P.top_log_probs[row * top + i] =
+        fine ? (from_ordered(static_cast<uint32_t>(k >> 32)) - mb) * inv_t - log_s : NAN;
+  }
 }
 
 template <class T>
