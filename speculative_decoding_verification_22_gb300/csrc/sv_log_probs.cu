@@ -16,9 +16,9 @@ namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kBytes = 16;          // of a load
-constexpr int kCap = 2048;          // candidates that wait to be ranked
-constexpr int kFew = 256;           // of these that are ranked after a last bound
-constexpr int kSlack = 8;           // alternatives more than asked for that a bound may leave
+constexpr int kStage = 1024;        // loads with candidates that a row keeps
+constexpr int kCap = 1024;          // candidates of a tile, where it is taken by itself
+constexpr int kFew = 256;           // candidates that are ranked
 constexpr int kMaxCluster = kWarps;
 
 // Order of the alternatives: the larger logit first, of equal ones the smaller
@@ -45,30 +45,46 @@ struct Part {
 struct Shared {
   Part part;
   uint64_t list[2][SV_MAX_TOP];
-  uint64_t cand[kCap + SV_MAX_TOP], few[kFew];
+  uint64_t few[kFew];
+  union {
+    struct {
+      uint4 load[kStage];
+      int at[kStage];
+    } stage;
+    uint64_t cand[kCap + SV_MAX_TOP];
+  };
   float red[3][kWarps];
+  uint32_t bound[2][kWarps];
   int count, few_count;
 };
 
-// Where a CTA's part of a row lies, in loads of 16 bytes; the row's elements
-// start `lead` into its first one.
+// The loads of 16 bytes of a CTA's part of a row: `row` is 16-byte aligned, and
+// its first element has the id `id0` (what lies before it and behind the last load
+// of the row are its edges).
 template <class T>
 struct Span {
   static constexpr int kWidth = kBytes / sizeof(T);  // elements of a load
   static constexpr int kVec = 32 / kWidth;           // loads of a thread in a tile
   static constexpr int kTile = kThreads * kVec;      // of a tile
   const T *row;
-  int lead, V, begin, end;
-  // Element i of a thread whose first load of the tile is `first`; negative or
-  // beyond the row where there is none.
+  int id0, begin, end;
+  __device__ __forceinline__ bool has(int load) const { return load < end; }
+  // The id of element i of a thread whose first load of the tile is `first`.
   __device__ __forceinline__ int id(int i, int first) const {
-    return (first + i / kWidth * kThreads) * kWidth + i % kWidth - lead;
-  }
-  __device__ __forceinline__ bool has(int i, int first) const {
-    const int e = id(i, first);
-    return e >= 0 && e < V && first + i / kWidth * kThreads < end;
+    return id0 + (first + i / kWidth * kThreads) * kWidth + i % kWidth;
   }
 };
+
+template <class T>
+__device__ __forceinline__ float element(const uint4 &v, int i) {
+  const uint32_t *w = reinterpret_cast<const uint32_t *>(&v);
+  if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
+  const uint32_t h = w[i / 2];
+  if constexpr (std::is_same<T, __nv_bfloat16>::value)
+    return __uint_as_float(i & 1 ? h & 0xFFFF0000u : h << 16);
+  const __half2 f = *reinterpret_cast<const __half2 *>(&h);
+  return i & 1 ? __high2float(f) : __low2float(f);
+}
 
 // A tile in registers, 32 elements a thread.
 template <class T>
@@ -76,38 +92,19 @@ struct Tile {
   using S = Span<T>;
   uint4 v[S::kVec];
   __device__ __forceinline__ float at(int i) const {
-    const uint32_t *w = reinterpret_cast<const uint32_t *>(v);
-    if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
-    const uint32_t h = w[i / 2];
-    if constexpr (std::is_same<T, __nv_bfloat16>::value)
-      return __uint_as_float(i & 1 ? h & 0xFFFF0000u : h << 16);
-    const __half2 f = *reinterpret_cast<const __half2 *>(&h);
-    return i & 1 ? __high2float(f) : __low2float(f);
+    return element<T>(v[i / S::kWidth], i % S::kWidth);
   }
-  // The tile from load v0 on.  What is outside the row or the part is -inf.
+  // The tile from load v0 on; -inf behind the part.
   __device__ __forceinline__ void load(const S &s, int v0) {
+    const T low = from_float<T>(-INFINITY);
+    uint32_t w = 0xFF800000u;
+    if constexpr (sizeof(T) == 2) w = *reinterpret_cast<const uint16_t *>(&low) * 0x10001u;
     const int first = v0 + threadIdx.x;
-    const bool inside = (v0 > 0 || s.lead == 0) && v0 + S::kTile <= s.end &&
-                        (v0 + S::kTile) * S::kWidth - s.lead <= s.V;
-    if (inside) {
-      const uint4 *p = reinterpret_cast<const uint4 *>(s.row + (first * S::kWidth - s.lead));
-#pragma unroll
-      for (int i = 0; i < S::kVec; ++i) v[i] = __ldcs(p + i * kThreads);
-      return;
-    }
+    const uint4 *p = reinterpret_cast<const uint4 *>(s.row) + first;
 #pragma unroll
     for (int i = 0; i < S::kVec; ++i) {
-      const int j = first + i * kThreads, e0 = j * S::kWidth - s.lead;
-      if (j < s.end && e0 >= 0 && e0 + S::kWidth <= s.V) {
-        v[i] = __ldcs(reinterpret_cast<const uint4 *>(s.row + e0));
-      } else {
-        alignas(16) T e[S::kWidth];
-#pragma unroll
-        for (int k = 0; k < S::kWidth; ++k)
-          e[k] = j < s.end && e0 + k >= 0 && e0 + k < s.V ? s.row[e0 + k]
-                                                          : from_float<T>(-INFINITY);
-        v[i] = *reinterpret_cast<const uint4 *>(e);
-      }
+      v[i] = make_uint4(w, w, w, w);
+      if (s.has(first + i * kThreads)) v[i] = __ldcs(p + i * kThreads);
     }
   }
   // The largest element of each load (a NaN stays).
@@ -118,22 +115,6 @@ struct Tile {
 #pragma unroll
       for (int k = 2; k < S::kWidth; k += 2)
         most[i] = max3_nan(most[i], at(i * S::kWidth + k), at(i * S::kWidth + k + 1));
-    }
-  }
-  // Writes the elements from `lim` on as candidates; counts those that do not fit.
-  __device__ __forceinline__ void push(const S &s, int v0, const float (&most)[S::kVec],
-                                       uint32_t lim, Shared &sh) const {
-    const int first = v0 + threadIdx.x;
-    const float limf = from_ordered(lim);
-#pragma unroll
-    for (int i = 0; i < S::kVec; ++i) {
-      if (most[i] < limf) continue;  // (goes on with a NaN)
-#pragma unroll
-      for (int k = i * S::kWidth; k < (i + 1) * S::kWidth; ++k) {
-        if (!(at(k) >= limf) || !s.has(k, first)) continue;
-        const int j = atomicAdd(&sh.count, 1);
-        if (j < kCap) sh.cand[j] = order_key(at(k), s.id(k, first));
-      }
     }
   }
 };
@@ -153,9 +134,10 @@ __device__ __forceinline__ void rank_keys(const uint64_t *keys, int n, int top, 
 // The best keys so far and the bound under which there are none.  All threads of
 // the block call its functions, which agree on n and on what is kept here.
 struct Best {
-  int top;
+  int top, warps;
   int found = 0, cur = 0;   // the list's keys and its buffer
   uint32_t lim = kLowest;   // ordered values from here are candidates
+  int turn = 0;             // of the bounds' two buffers
 
   // Ranks the n candidates with the list.
   __device__ __forceinline__ void rank(int n, Shared &sh) {
@@ -170,67 +152,67 @@ struct Best {
     // (what comes later and equals the last one has a larger id)
     if (found == top) lim = max(lim, static_cast<uint32_t>(sh.list[cur][top - 1] >> 32) + 1);
   }
-  // As many threads have an element from a bound on as there are alternatives: what
-  // lies under it is none.  Found by halving, and not to the last: a few more than
-  // needed may stay.
-  __device__ __forceinline__ void raise(float most) {
-    const uint32_t high = ordered(most);
-    int n = __syncthreads_count(high >= lim);
-    if (n <= top + kSlack) return;
-    uint32_t lo = lim, hi = kHighest + 1;  // count(lo) >= top > count(hi)
-    while (hi - lo > 1) {
-      const uint32_t mid = lo + (hi - lo) / 2;
-      n = __syncthreads_count(high >= mid);
-      if (n >= top) {
-        lo = mid;
-        if (n <= top + kSlack) break;
-      } else {
-        hi = mid;
-      }
+  // Each of the warps that have a load for every lane (or the first alone) has
+  // ceil(top / warps) elements, of different threads, from a bound on, so what lies
+  // under it is no alternative; the bound is the least of the warps' own.  One
+  // barrier; `most` is the thread's largest element so far.
+  __device__ __forceinline__ void raise(float most, Shared &sh) {
+    uint32_t u = ordered(most), bound = 0;
+    for (int r = (top + warps - 1) / warps; r > 0; --r) {
+      bound = __reduce_max_sync(0xffffffffu, u);
+      const uint32_t who = __ballot_sync(0xffffffffu, u == bound);
+      if ((threadIdx.x & 31) == __ffs(who) - 1) u = 0;
     }
-    lim = lo;
+    turn ^= 1;
+    if ((threadIdx.x & 31) == 0) sh.bound[turn][threadIdx.x >> 5] = bound;
+    __syncthreads();
+    bound = sh.bound[turn][0];
+    for (int w = 1; w < warps; ++w) bound = min(bound, sh.bound[turn][w]);
+    lim = max(lim, bound);
   }
 };
 
 // The best of a part whose tiles are taken one by one, however many of their
-// elements equal each other or rise.
+// elements equal each other or rise; `edges` keys of the row's edges lie in `few`
+// and come last, so that the tiles are met in the order of their ids.
 template <class T>
-__device__ __noinline__ Best best_of_each(const Span<T> s, Best best, Shared &sh) {
+__device__ __noinline__ Best best_of_each(const Span<T> s, int edges, Best best, Shared &sh) {
   using S = Span<T>;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  best.rank(0, sh);
+  __syncthreads();
+  if (threadIdx.x == 0) sh.count = 0;
   for (int v0 = s.begin; v0 < s.end; v0 += S::kTile) {
     const int first = v0 + threadIdx.x;
     Tile<T> tile;
     tile.load(s, v0);
-    float mv[S::kVec];
-    tile.maxima(mv);
-    float most = mv[0];
+    float most = tile.at(0);
 #pragma unroll
-    for (int i = 1; i < S::kVec; ++i) most = max_nan(most, mv[i]);
-    best.raise(most);
-    tile.push(s, v0, mv, best.lim, sh);
-    __syncthreads();
-    int n = sh.count;
+    for (int i = 1; i < 32; ++i) most = max_nan(most, tile.at(i));
+    best.raise(most, sh);
+    // Elements that `want` takes: how many there are, and writing them.
+    auto count = [&](auto &&want) {
+      int c = 0;
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        const uint32_t u = ordered(tile.at(i));
+        c += s.has(first + i / S::kWidth * kThreads) && u <= kHighest && want(u, s.id(i, first));
+      }
+      c = __reduce_add_sync(0xffffffffu, c);
+      __syncthreads();
+      if (lane == 0) sh.red[0][warp] = __int_as_float(c);
+      __syncthreads();
+      c = 0;
+      for (int w = 0; w < kWarps; ++w) c += __float_as_int(sh.red[0][w]);
+      return c;
+    };
+    uint32_t lo = best.lim;
+    int upto = s.id0 + s.end * S::kWidth;  // of those that equal lo
+    int n = count([&](uint32_t u, int) { return u >= lo; });
+    if (n == 0) continue;
     if (n > kCap) {
-      // The value of the tile's last alternative, then the ids of those that equal
-      // it, by halving.
-      auto count = [&](auto &&want) {
-        int c = 0;
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          const uint32_t u = ordered(tile.at(i));
-          c += s.has(i, first) && u <= kHighest && want(u, s.id(i, first));
-        }
-        c = __reduce_add_sync(0xffffffffu, c);
-        __syncthreads();
-        if (lane == 0) sh.red[0][warp] = __int_as_float(c);
-        __syncthreads();
-        c = 0;
-        for (int w = 0; w < kWarps; ++w) c += __float_as_int(sh.red[0][w]);
-        return c;
-      };
-      uint32_t lo = best.lim, hi = kHighest + 1;  // count(lo) >= top > count(hi)
+      // the value of the tile's last alternative, then the ids of those that equal
+      // it, by halving
+      uint32_t hi = kHighest + 1;  // count(lo) >= top > count(hi)
       while (hi - lo > 1) {
         const uint32_t mid = lo + (hi - lo) / 2;
         if (count([&](uint32_t u, int) { return u >= mid; }) >= best.top)
@@ -239,7 +221,7 @@ __device__ __noinline__ Best best_of_each(const Span<T> s, Best best, Shared &sh
           hi = mid;
       }
       const int more = count([&](uint32_t u, int) { return u > lo; });
-      int below = -1, upto = s.V - 1;  // ids up to `upto` are enough, up to `below` too few
+      int below = -1;  // ids up to `upto` are enough, up to `below` too few
       while (upto - below > 1) {
         const int mid = below + (upto - below) / 2;
         if (more + count([&](uint32_t u, int id) { return u == lo && id <= mid; }) >= best.top)
@@ -247,23 +229,25 @@ __device__ __noinline__ Best best_of_each(const Span<T> s, Best best, Shared &sh
         else
           below = mid;
       }
-      __syncthreads();
-      if (threadIdx.x == 0) sh.count = 0;
-      __syncthreads();
-#pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        const uint32_t u = ordered(tile.at(i));
-        const int id = s.id(i, first);
-        if (s.has(i, first) && u <= kHighest && (u > lo || (u == lo && id <= upto))) {
-          const int j = atomicAdd(&sh.count, 1);
-          if (j < kCap) sh.cand[j] = order_key(tile.at(i), id);
-        }
-      }
-      __syncthreads();
-      n = min(sh.count, kCap);
     }
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      const uint32_t u = ordered(tile.at(i));
+      const int id = s.id(i, first);
+      if (s.has(first + i / S::kWidth * kThreads) && u <= kHighest &&
+          (u > lo || (u == lo && id <= upto))) {
+        const int j = atomicAdd(&sh.count, 1);
+        if (j < kCap) sh.cand[j] = order_key(tile.at(i), id);
+      }
+    }
+    __syncthreads();
+    n = min(sh.count, kCap);
+    __syncthreads();
     best.rank(n, sh);
   }
+  __syncthreads();
+  for (int i = threadIdx.x; i < edges; i += kThreads) sh.cand[i] = sh.few[i];
+  best.rank(edges, sh);
   return best;
 }
 
@@ -300,28 +284,41 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 2 : 3)
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
   asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(parts));
   const int64_t row = blockIdx.x / parts;
+  const T *x = static_cast<const T *>(P.logits) + row * P.stride;
   const int V = static_cast<int>(P.V), top = P.top;
+  const float c2 = 1.4426950408889634f / P.temperature;  // to powers of two
   S s;
-  s.row = static_cast<const T *>(P.logits) + row * P.stride;
-  s.V = V;
-  s.lead = static_cast<int>((reinterpret_cast<uintptr_t>(s.row) & (kBytes - 1)) / sizeof(T));
-  const int loads = (s.lead + V + S::kWidth - 1) / S::kWidth;
+  s.id0 = static_cast<int>((0 - reinterpret_cast<uintptr_t>(x)) % kBytes / sizeof(T));
+  s.id0 = min(s.id0, V);
+  s.row = x + s.id0;
+  const int loads = (V - s.id0) / S::kWidth;
   s.begin = static_cast<int>(static_cast<int64_t>(loads) * rank / parts);
   s.end = static_cast<int>(static_cast<int64_t>(loads) * (rank + 1) / parts);
-  const float c2 = 1.4426950408889634f / P.temperature;  // to powers of two
-  if (tid == 0) sh.count = 0;
+  // the edges: one element for some of the first CTA's threads
+  const int tail = s.id0 + loads * S::kWidth;
+  const int edges = rank == 0 ? s.id0 + V - tail : 0;
+  if (tid == 0) {
+    sh.count = 0;
+    sh.few_count = edges;
+  }
   pdl_wait();
   pdl_launch_dependents();
 
-  float m = -INFINITY, sum = 0.0f, t = 0.0f;  // of this thread's elements, d in log2
-  Best best;
-  best.top = top;
-  // Candidates are written without a barrier between the tiles of a group, under
-  // a bound found at its start; the groups grow as candidates get rarer.
-  int next_start = 0;
   Tile<T> tile, next;
   next.load(s, s.begin);
-  int number = 0;
+  float m = -INFINITY, sum = 0.0f, t = 0.0f;  // of this thread's elements, d in log2
+  if (tid < edges) {
+    const int id = tid < s.id0 ? tid : tail + tid - s.id0;
+    m = to_float(x[id]);
+    sum = m > -INFINITY ? 1.0f : 0.0f;
+    sh.few[tid] = order_key(m, id);
+  }
+  Best best;
+  best.top = top;
+  best.warps = max(1, min(kWarps, (s.end - s.begin) / 32));
+  // Loads with candidates are kept without a barrier between the tiles of a group,
+  // under a bound found at its start; the groups grow as candidates get rarer.
+  int next_start = 0, number = 0;
   for (int v0 = s.begin; v0 < s.end; v0 += S::kTile, ++number) {
     tile = next;
     if (v0 + S::kTile < s.end) next.load(s, v0 + S::kTile);
@@ -356,31 +353,42 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 2 : 3)
     }
     if (top) {
       if (number == next_start) {
-        best.raise(m);
+        best.raise(m, sh);
         next_start = number == 0 ? 2 : number < 32 ? 4 * number : number + 32;
       }
-      if (ordered(most) >= best.lim) tile.push(s, v0, mv, best.lim, sh);
+      const float lim = from_ordered(best.lim);
+      if (!(most < lim)) {
+#pragma unroll
+        for (int i = 0; i < S::kVec; ++i) {
+          if (!(mv[i] >= lim) || !s.has(v0 + tid + i * kThreads)) continue;
+          const int j = atomicAdd(&sh.count, 1);
+          if (j < kStage) {
+            sh.stage.load[j] = tile.v[i];
+            sh.stage.at[j] = v0 + tid + i * kThreads;
+          }
+        }
+      }
     }
   }
   if (top) {
-    if (tid == 0) sh.few_count = 0;
-    best.raise(m);
+    best.raise(m, sh);
     const int n = sh.count;
-    if (n > kCap) {
-      best = best_of_each(s, best, sh);  // some were not written
-    } else {
-      for (int i = tid; i < n; i += kThreads) {
-        const uint64_t k = sh.cand[i];
-        if (k >> 32 < best.lim) continue;
-        const int j = atomicAdd(&sh.few_count, 1);
-        if (j < kFew) sh.few[j] = k;
+    const float lim = from_ordered(best.lim);
+    if (n <= kStage) {
+      for (int i = tid; i < n * S::kWidth; i += kThreads) {
+        const int j = i / S::kWidth, k = i % S::kWidth;
+        const float y = to_float(reinterpret_cast<const T *>(&sh.stage.load[j])[k]);
+        if (!(y >= lim)) continue;
+        const int at = atomicAdd(&sh.few_count, 1);
+        if (at < kFew) sh.few[at] = order_key(y, s.id0 + sh.stage.at[j] * S::kWidth + k);
       }
       __syncthreads();
-      const int few = sh.few_count;
-      if (few <= kFew)
-        rank_keys(sh.few, few, top, sh.list[0]);
-      else
-        rank_keys(sh.cand, n, top, sh.list[0]);
+    }
+    const int few = sh.few_count;
+    if (n > kStage || few > kFew) {
+      best = best_of_each(s, edges, best, sh);  // some were not kept
+    } else {
+      rank_keys(sh.few, few, top, sh.list[0]);
       best.found = min(few, top);
     }
   }
@@ -457,7 +465,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 2 : 3)
     const int id = P.tokens[row * P.n + i];
     float y = 0.0f;
     if (id >= 0 && id < V) {
-      y = (to_float(s.row[id]) - mb) * inv_t - log_s;
+      y = (to_float(x[id]) - mb) * inv_t - log_s;
     } else if (id != -1) {
       y = NAN;
       set_status(status, SV_ERR_TOKEN);
@@ -475,10 +483,19 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 2 : 3)
 template <class T>
 cudaError_t launch_typed(const sv_log_probs_t &a, int num_sms, int *status,
                          cudaStream_t stream) {
-  // Parts of a row: as many as fill the GPU, of at least one tile each.
+  // Parts of a row, of at least a tile each: waves of CTAs (two or three run on an
+  // SM), each of the time of its tiles and of about two more for its start and end.
   const int64_t tiles = (a.V + kThreads * 32 - 1) / (kThreads * 32);
+  const int64_t slots = num_sms * (sizeof(T) == 4 ? 2 : 3);
   int parts = 1;
-  while (parts < kMaxCluster && 2 * parts <= tiles && a.rows * parts < 4 * num_sms) parts *= 2;
+  int64_t best = INT64_MAX;
+  for (int p = 1; p <= kMaxCluster && p <= tiles; ++p) {
+    const int64_t time = (a.rows * p + slots - 1) / slots * ((tiles + p - 1) / p + 2);
+    if (time < best) {
+      best = time;
+      parts = p;
+    }
+  }
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
