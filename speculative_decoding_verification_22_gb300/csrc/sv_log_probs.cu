@@ -5,6 +5,7 @@
 //
 // With m the row's maximum and d = (x - m) / T <= 0, s = sum exp d and
 // t = sum d exp d: lse - m / T = log s and H = log s - t / s.
+#include <algorithm>
 #include <cmath>
 #include <type_traits>
 
@@ -14,12 +15,13 @@
 namespace sv {
 namespace {
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kVec = 4;             // loads of a thread in a tile
+constexpr int kResident = 24;       // warps on an SM (the registers are bounded for it)
 constexpr int kBytes = 16;          // of a load
 constexpr int kStage = 1024;        // loads with candidates that a row keeps
 constexpr int kCap = 1024;          // candidates of a tile, where it is taken by itself
 constexpr int kFew = 256;           // candidates that are ranked
-constexpr int kMaxCluster = kWarps;
+constexpr int kMaxCluster = 8;
 
 // Order of the alternatives: the larger logit first, of equal ones the smaller
 // id.  The logit's bits become an unsigned number of the same order; -0 counts
@@ -42,6 +44,7 @@ struct Part {
   int found;
   uint64_t best[SV_MAX_TOP];
 };
+template <int kWarps>
 struct Shared {
   Part part;
   uint64_t list[2][SV_MAX_TOP];
@@ -53,7 +56,7 @@ struct Shared {
     } stage;
     uint64_t cand[kCap + SV_MAX_TOP];
   };
-  float red[3][kWarps];
+  float red[3][kMaxCluster];
   uint32_t bound[2][kWarps];
   int count, few_count;
 };
@@ -61,10 +64,11 @@ struct Shared {
 // The loads of 16 bytes of a CTA's part of a row: `row` is 16-byte aligned, and
 // its first element has the id `id0` (what lies before it and behind the last load
 // of the row are its edges).
-template <class T>
+template <class T, int kWarps>
 struct Span {
+  static constexpr int kThreads = 32 * kWarps;
   static constexpr int kWidth = kBytes / sizeof(T);  // elements of a load
-  static constexpr int kVec = 32 / kWidth;           // loads of a thread in a tile
+  static constexpr int kPer = kVec * kWidth;         // elements of a thread in a tile
   static constexpr int kTile = kThreads * kVec;      // of a tile
   const T *row;
   int id0, begin, end;
@@ -86,11 +90,12 @@ __device__ __forceinline__ float element(const uint4 &v, int i) {
   return i & 1 ? __high2float(f) : __low2float(f);
 }
 
-// A tile in registers, 32 elements a thread.
-template <class T>
+// A tile in registers.
+template <class T, int kWarps>
 struct Tile {
-  using S = Span<T>;
-  uint4 v[S::kVec];
+  using S = Span<T, kWarps>;
+  static constexpr int kThreads = S::kThreads;
+  uint4 v[kVec];
   __device__ __forceinline__ float at(int i) const {
     return element<T>(v[i / S::kWidth], i % S::kWidth);
   }
@@ -102,15 +107,15 @@ struct Tile {
     const int first = v0 + threadIdx.x;
     const uint4 *p = reinterpret_cast<const uint4 *>(s.row) + first;
 #pragma unroll
-    for (int i = 0; i < S::kVec; ++i) {
+    for (int i = 0; i < kVec; ++i) {
       v[i] = make_uint4(w, w, w, w);
       if (s.has(first + i * kThreads)) v[i] = __ldcs(p + i * kThreads);
     }
   }
   // The largest element of each load (a NaN stays).
-  __device__ __forceinline__ void maxima(float (&most)[S::kVec]) const {
+  __device__ __forceinline__ void maxima(float (&most)[kVec]) const {
 #pragma unroll
-    for (int i = 0; i < S::kVec; ++i) {
+    for (int i = 0; i < kVec; ++i) {
       most[i] = max_nan(at(i * S::kWidth), at(i * S::kWidth + 1));
 #pragma unroll
       for (int k = 2; k < S::kWidth; k += 2)
@@ -122,7 +127,7 @@ struct Tile {
 // The `top` best of n keys, in order, by counting for each the greater ones (keys
 // differ).
 __device__ __forceinline__ void rank_keys(const uint64_t *keys, int n, int top, uint64_t *out) {
-  for (int i = threadIdx.x; i < n; i += kThreads) {
+  for (int i = threadIdx.x; i < n; i += blockDim.x) {
     const uint64_t k = keys[i];
     int r = 0;
 #pragma unroll 4
@@ -133,14 +138,17 @@ __device__ __forceinline__ void rank_keys(const uint64_t *keys, int n, int top, 
 
 // The best keys so far and the bound under which there are none.  All threads of
 // the block call its functions, which agree on n and on what is kept here.
+template <int kWarps>
 struct Best {
+  using Sh = Shared<kWarps>;
+  static constexpr int kThreads = 32 * kWarps;
   int top, warps;
   int found = 0, cur = 0;   // the list's keys and its buffer
   uint32_t lim = kLowest;   // ordered values from here are candidates
   int turn = 0;             // of the bounds' two buffers
 
   // Ranks the n candidates with the list.
-  __device__ __forceinline__ void rank(int n, Shared &sh) {
+  __device__ __forceinline__ void rank(int n, Sh &sh) {
     for (int i = threadIdx.x; i < found; i += kThreads) sh.cand[n + i] = sh.list[cur][i];
     __syncthreads();
     n += found;
@@ -156,7 +164,7 @@ struct Best {
   // ceil(top / warps) elements, of different threads, from a bound on, so what lies
   // under it is no alternative; the bound is the least of the warps' own.  One
   // barrier; `most` is the thread's largest element so far.
-  __device__ __forceinline__ void raise(float most, Shared &sh) {
+  __device__ __forceinline__ void raise(float most, Sh &sh) {
     uint32_t u = ordered(most), bound = 0;
     for (int r = (top + warps - 1) / warps; r > 0; --r) {
       bound = __reduce_max_sync(0xffffffffu, u);
@@ -175,25 +183,27 @@ struct Best {
 // The best of a part whose tiles are taken one by one, however many of their
 // elements equal each other or rise; `edges` keys of the row's edges lie in `few`
 // and come last, so that the tiles are met in the order of their ids.
-template <class T>
-__device__ __noinline__ Best best_of_each(const Span<T> s, int edges, Best best, Shared &sh) {
-  using S = Span<T>;
+template <class T, int kWarps>
+__device__ __noinline__ Best<kWarps> best_of_each(const Span<T, kWarps> s, int edges,
+                                                 Best<kWarps> best, Shared<kWarps> &sh) {
+  using S = Span<T, kWarps>;
+  constexpr int kThreads = S::kThreads;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   __syncthreads();
   if (threadIdx.x == 0) sh.count = 0;
   for (int v0 = s.begin; v0 < s.end; v0 += S::kTile) {
     const int first = v0 + threadIdx.x;
-    Tile<T> tile;
+    Tile<T, kWarps> tile;
     tile.load(s, v0);
     float most = tile.at(0);
 #pragma unroll
-    for (int i = 1; i < 32; ++i) most = max_nan(most, tile.at(i));
+    for (int i = 1; i < S::kPer; ++i) most = max_nan(most, tile.at(i));
     best.raise(most, sh);
     // Elements that `want` takes: how many there are, and writing them.
     auto count = [&](auto &&want) {
       int c = 0;
 #pragma unroll
-      for (int i = 0; i < 32; ++i) {
+      for (int i = 0; i < S::kPer; ++i) {
         const uint32_t u = ordered(tile.at(i));
         c += s.has(first + i / S::kWidth * kThreads) && u <= kHighest && want(u, s.id(i, first));
       }
@@ -231,7 +241,7 @@ __device__ __noinline__ Best best_of_each(const Span<T> s, int edges, Best best,
       }
     }
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
+    for (int i = 0; i < S::kPer; ++i) {
       const uint32_t u = ordered(tile.at(i));
       const int id = s.id(i, first);
       if (s.has(first + i / S::kWidth * kThreads) && u <= kHighest &&
@@ -274,11 +284,12 @@ __device__ __forceinline__ V remote(const V *p, uint32_t rank) {
 }
 
 // One cluster a row, a part of it for each CTA.
-template <class T>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 2 : 3)
+template <class T, int kWarps>
+__global__ void __launch_bounds__(32 * kWarps, kResident / kWarps)
     log_probs_kernel(const sv_log_probs_t P, int *status) {
-  using S = Span<T>;
-  __shared__ Shared sh;
+  using S = Span<T, kWarps>;
+  constexpr int kThreads = S::kThreads;
+  __shared__ Shared<kWarps> sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   uint32_t rank, parts;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
@@ -304,7 +315,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 2 : 3)
   pdl_wait();
   pdl_launch_dependents();
 
-  Tile<T> tile, next;
+  Tile<T, kWarps> tile, next;
   next.load(s, s.begin);
   float m = -INFINITY, sum = 0.0f, t = 0.0f;  // of this thread's elements, d in log2
   if (tid < edges) {
@@ -313,7 +324,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 2 : 3)
     sum = m > -INFINITY ? 1.0f : 0.0f;
     sh.few[tid] = order_key(m, id);
   }
-  Best best;
+  Best<kWarps> best;
   best.top = top;
   best.warps = max(1, min(kWarps, (s.end - s.begin) / 32));
   // Loads with candidates are kept without a barrier between the tiles of a group,
@@ -322,11 +333,11 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 2 : 3)
   for (int v0 = s.begin; v0 < s.end; v0 += S::kTile, ++number) {
     tile = next;
     if (v0 + S::kTile < s.end) next.load(s, v0 + S::kTile);
-    float mv[S::kVec];
+    float mv[kVec];
     tile.maxima(mv);
     float most = mv[0];
 #pragma unroll
-    for (int i = 1; i < S::kVec; ++i) most = max_nan(most, mv[i]);
+    for (int i = 1; i < kVec; ++i) most = max_nan(most, mv[i]);
     const float m2 = max_nan(m, most);
     if (!(m2 <= m)) {  // larger, or a NaN
       const float d = fmaxf((m - m2) * c2, -200.0f), e = ex2(d);
@@ -338,7 +349,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 2 : 3)
       const uint64_t neg = pair2(-m, -m), c = pair2(c2, c2);
       uint64_t s2 = 0, t2 = 0;
 #pragma unroll
-      for (int i = 0; i < 32; i += 2) {
+      for (int i = 0; i < S::kPer; i += 2) {
         float2 d = unpair2(mul2(add2(pair2(tile.at(i), tile.at(i + 1)), neg), c));
         // (2^-200 is 0 here, and 0 times it stays 0 where a logit is -inf)
         d.x = fmaxf(d.x, -200.0f);
@@ -359,7 +370,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 2 : 3)
       const float lim = from_ordered(best.lim);
       if (!(most < lim)) {
 #pragma unroll
-        for (int i = 0; i < S::kVec; ++i) {
+        for (int i = 0; i < kVec; ++i) {
           if (!(mv[i] >= lim) || !s.has(v0 + tid + i * kThreads)) continue;
           const int j = atomicAdd(&sh.count, 1);
           if (j < kStage) {
@@ -433,13 +444,13 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 2 : 3)
     cluster_sync();
     if (rank == 0) {
       // a warp for each part; keys that a part lacks are 0, below every other
-      if (warp < static_cast<int>(parts)) {
-        if (lane == 0) sh.red[0][warp] = remote(&sh.part.m, warp);
-        if (lane == 1) sh.red[1][warp] = remote(&sh.part.s, warp);
-        if (lane == 2) sh.red[2][warp] = remote(&sh.part.t, warp);
-        const int f = remote(&sh.part.found, warp);
+      for (int q = warp; q < static_cast<int>(parts); q += kWarps) {
+        if (lane == 0) sh.red[0][q] = remote(&sh.part.m, q);
+        if (lane == 1) sh.red[1][q] = remote(&sh.part.s, q);
+        if (lane == 2) sh.red[2][q] = remote(&sh.part.t, q);
+        const int f = remote(&sh.part.found, q);
         for (int i = lane; i < top; i += 32)
-          sh.cand[warp * top + i] = i < f ? remote(&sh.part.best[i], warp) : 0;
+          sh.cand[q * top + i] = i < f ? remote(&sh.part.best[i], q) : 0;
       }
       __syncthreads();
       mb = sh.red[0][0];
@@ -480,22 +491,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 2 : 3)
   }
 }
 
-template <class T>
-cudaError_t launch_typed(const sv_log_probs_t &a, int num_sms, int *status,
-                         cudaStream_t stream) {
-  // Parts of a row, of at least a tile each: waves of CTAs (two or three run on an
-  // SM), each of the time of its tiles and of about two more for its start and end.
-  const int64_t tiles = (a.V + kThreads * 32 - 1) / (kThreads * 32);
-  const int64_t slots = num_sms * (sizeof(T) == 4 ? 2 : 3);
-  int parts = 1;
-  int64_t best = INT64_MAX;
-  for (int p = 1; p <= kMaxCluster && p <= tiles; ++p) {
-    const int64_t time = (a.rows * p + slots - 1) / slots * ((tiles + p - 1) / p + 2);
-    if (time < best) {
-      best = time;
-      parts = p;
-    }
-  }
+template <class T, int kWarps>
+cudaError_t launch_warps(const sv_log_probs_t &a, int parts, int *status, cudaStream_t stream) {
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -504,11 +501,29 @@ cudaError_t launch_typed(const sv_log_probs_t &a, int num_sms, int *status,
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(a.rows * parts));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(32 * kWarps);
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = parts > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, log_probs_kernel<T>, a, status);
+  return cudaLaunchKernelEx(&cfg, log_probs_kernel<T, kWarps>, a, status);
+}
+template <class T>
+cudaError_t launch_typed(const sv_log_probs_t &a, int num_sms, int *status,
+                         cudaStream_t stream) {
+  // Eight warps a CTA where a row has eight of their tiles (128 KB), fewer for short
+  // rows, whose start and end then run beside more others': 4000 rows of 20000 in
+  // bf16 take 75 us with eight warps, 55 with four, 56 with two; 16000 of 2000 take
+  // 156, 82 and 56; 4095 of 128003 226, 216 and 261, 320 of 128256 in fp32 36.5, 50
+  // and 87.  Parts of a row only where rows leave SMs idle, as clusters start slowly:
+  // 40 rows of 128256 take 16.8 us in one part, 11.3 in six; 320 take 44 in one and
+  // 51 in two.
+  constexpr int64_t kTileBytes = 256 * kVec * kBytes;
+  const int64_t bytes = a.V * static_cast<int64_t>(sizeof(T));
+  const int64_t most = std::min<int64_t>(2 * num_sms / a.rows, (bytes - 1) / kTileBytes + 1);
+  const int parts = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(most, kMaxCluster)));
+  if (parts > 1 || bytes >= 8 * kTileBytes) return launch_warps<T, 8>(a, parts, status, stream);
+  if (bytes >= kTileBytes) return launch_warps<T, 4>(a, 1, status, stream);
+  return launch_warps<T, 2>(a, 1, status, stream);
 }
 
 }  // namespace
