@@ -28,13 +28,15 @@ struct Args {
   int *status;
   uint64_t limit_ns;
   int bn, tiles, split, kblocks, stages;
+  int bufs;  // for parts of sums: 1 or 2
+  int per;   // columns whose parts a CTA adds, a multiple of four
   int bf16;
 };
 
 struct Ctl {
   uint64_t full[kMaxStages], empty[kMaxStages];
   uint64_t tfull[2], tempty[2];
-  uint64_t xfull, xempty;
+  uint64_t xfull[2], xempty[2];
   uint64_t teardown;
   uint32_t tmem;
   int abort, issued, consumed;
@@ -42,7 +44,7 @@ struct Ctl {
 
 // K blocks of a stage
 template <int kCols>
-constexpr int stage_blocks() { return kCols <= 64 ? 2 : 1; }
+constexpr int stage_blocks() { return kCols == 64 ? 2 : 1; }
 template <int kCols>
 constexpr int stage_bytes() { return stage_blocks<kCols>() * (kLanes + kCols) * 128; }
 
@@ -60,8 +62,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t *smem = smem_raw + (base - raw);
   float *parts = reinterpret_cast<float *>(smem + args.stages * kStage);
   const int M = static_cast<int>(p.M);
-  const int per = (M + args.split - 1) / args.split;  // columns that a CTA adds
-  Ctl *ctl = reinterpret_cast<Ctl *>(smem + args.stages * kStage + args.split * per * kLanes * 4);
+  const int per = args.per;  // columns that a CTA adds
+  Ctl *ctl = reinterpret_cast<Ctl *>(smem + args.stages * kStage + args.bufs * args.split * per * kLanes * 4);
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const LinAbort ab{args.status, args.limit_ns, &ctl->abort};
@@ -75,15 +77,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&ctl->tfull[i]), 1);
       mbar_init(smem_u32(&ctl->tempty[i]), kEpiWarps);
     }
-    mbar_init(smem_u32(&ctl->xfull), kEpiWarps * args.split);
-    mbar_init(smem_u32(&ctl->xempty), kEpiWarps * args.split);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&ctl->xfull[i]), 1);
+      mbar_init(smem_u32(&ctl->xempty[i]), kEpiWarps * args.split);
+    }
     mbar_init(smem_u32(&ctl->teardown), 1);
     ctl->abort = ctl->issued = ctl->consumed = 0;
     mbar_fence_init();
   }
+  const int rank = args.split > 1 ? static_cast<int>(lin_cluster_rank()) : 0;
+  const int first = blockIdx.x / args.split, step = gridDim.x / args.split;
+  const int kb0 = static_cast<int>(static_cast<int64_t>(args.kblocks) * rank / args.split);
+  const int kb1 = static_cast<int>(static_cast<int64_t>(args.kblocks) * (rank + 1) / args.split);
   if (warp == kLoadWarp && lane == 0) {
-    tma_prefetch_desc(&tmW);
-    if (kGated) tma_prefetch_desc(&tmU);
+    // The first blocks of the weight come into L2 while what precedes this kernel
+    // ends (L2 is where all writes meet, so it does not matter who wrote them).
+    for (int kb = kb0; kb < min(kb1, kb0 + args.stages * kKb); ++kb) {
+      lin_prefetch(&tmW, kb * kLinBlk, first * kRows);
+      if (kGated) lin_prefetch(&tmU, kb * kLinBlk, first * kRows);
+    }
     tma_prefetch_desc(&tmX);
   }
   if (warp == kMmaWarp) {
@@ -98,11 +110,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_wait();
   pdl_launch_dependents();
 
-  const int rank = args.split > 1 ? static_cast<int>(lin_cluster_rank()) : 0;
-  const int first = blockIdx.x / args.split, step = gridDim.x / args.split;
-  const int kb0 = static_cast<int>(static_cast<int64_t>(args.kblocks) * rank / args.split);
-  const int kb1 = static_cast<int>(static_cast<int64_t>(args.kblocks) * (rank + 1) / args.split);
-
   if (warp < kEpiWarps) {
     // ---------------- sums and epilogue ----------------
     const int row = tid;
@@ -113,10 +120,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t slot = it & 1, phase = it >> 1 & 1;
       if (!(ok = lin_wait(smem_u32(&ctl->tfull[slot]), phase, ab))) break;
       tc_fence_after();
-      if (!(ok = lin_wait<true>(smem_u32(&ctl->xempty), (it & 1) ^ 1u, ab))) break;
-      // column c goes to CTA c / per, as its column c % per of this CTA's part
+      // The parts of the sum go to a buffer (two in turn where there is room), as
+      // [part][column / 4][lane][column % 4].  Column c goes to CTA c / per.
+      const uint32_t xslot = args.bufs == 2 ? slot : 0, xphase = args.bufs == 2 ? phase : it & 1;
+      if (!(ok = lin_wait<true>(smem_u32(&ctl->xempty[xslot]), xphase ^ 1u, ab))) break;
+      float *const buf = parts + xslot * args.split * per * kLanes;
+      const uint32_t bar = smem_u32(&ctl->xfull[xslot]);
+      const int mine = min(per, M - rank * per);
+      const int fours = mine > 0 ? (mine + 3) / 4 : 0;
+      if (tid == 0) mbar_arrive_expect_tx(bar, fours * args.split * kLanes * 16);
+      const uint32_t own = smem_u32(buf + rank * per * kLanes + row * 4);
       int q = 0, left = per;
-      uint32_t at = lin_remote(smem_u32(parts + (rank * per) * kLanes + row), 0);
+      uint32_t at = lin_remote(own, 0), to = lin_remote(bar, 0);
 #pragma unroll
       for (int c0 = 0; c0 < kCols; c0 += 16) {
         if (c0 >= M) break;
@@ -125,48 +140,55 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld_wait();
         tmem_reg_fence(x);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
+        for (int e = 0; e < 16; e += 4) {
           if (c0 + e < M) {
-            lin_store_remote(at, __uint_as_float(x[e]));
-            at += kLanes * 4;
-            if (--left == 0 && c0 + e + 1 < M) {
+            if (left == 0) {
               left = per;
-              at = lin_remote(smem_u32(parts + (rank * per) * kLanes + row), ++q);
+              at = lin_remote(own, ++q);
+              to = lin_remote(bar, q);
             }
+            lin_store_remote(at, x + e, to);
+            at += kLanes * 16;
+            left -= 4;
           }
         }
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(smem_u32(&ctl->tempty[slot]));
-        for (int c = 0; c < args.split; ++c) lin_arrive_remote(lin_remote(smem_u32(&ctl->xfull), c));
-      }
+      if (lane == 0) mbar_arrive(smem_u32(&ctl->tempty[slot]));
       __syncwarp();
-      if (!(ok = lin_wait<true>(smem_u32(&ctl->xfull), it & 1, ab))) break;
-      const int mine = min(per, M - rank * per);
+      if (!(ok = lin_wait<true>(bar, xphase, ab))) break;
       const int r = row % kRows;
       const int64_t n = static_cast<int64_t>(tile) * kRows + r;
       if (n < p.N) {
         const float b = p.bias ? load_any(p.bias, n, p.dtype) : 0.0f;
         const float bu = kGated && p.bias_u ? load_any(p.bias_u, n, p.dtype) : 0.0f;
-        for (int v = row / kRows; v < mine; v += kLanes / kRows) {
-          float y = 0.0f, u = 0.0f;
+        const float4 *in = reinterpret_cast<const float4 *>(buf);
+        for (int f = row / kRows; f < fours; f += kLanes / kRows) {
+          float y[4] = {}, u[4] = {};
           for (int s = 0; s < args.split; ++s) {
-            y += parts[(s * per + v) * kLanes + r];
-            if (kGated) u += parts[(s * per + v) * kLanes + 64 + r];
+            const float4 *part = in + (s * (per / 4) + f) * kLanes + r;
+            const float4 a = part[0];
+            y[0] += a.x, y[1] += a.y, y[2] += a.z, y[3] += a.w;
+            if (kGated) {
+              const float4 c = part[64];
+              u[0] += c.x, u[1] += c.y, u[2] += c.z, u[3] += c.w;
+            }
           }
-          const int64_t m = rank * per + v;
-          y = activate(y + b, p.act);
-          if (kGated) y *= u + bu;
-          if (p.res) y += load_any(p.res, m * p.rs + n, p.out_dtype);
-          store_any(p.out, m * p.os + n, y, p.out_dtype);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            if (4 * f + e >= mine) break;
+            const int64_t m = rank * per + 4 * f + e;
+            float v = activate(y[e] + b, p.act);
+            if (kGated) v *= u[e] + bu;
+            if (p.res) v += load_any(p.res, m * p.rs + n, p.out_dtype);
+            store_any(p.out, m * p.os + n, v, p.out_dtype);
+          }
         }
       }
       __syncwarp();
-      if (lane == 0)
-        for (int c = 0; c < args.split; ++c)
-          lin_arrive_remote(lin_remote(smem_u32(&ctl->xempty), c));
+      if (lane < args.split) lin_arrive_remote(lin_remote(smem_u32(&ctl->xempty[xslot]), lane));
+      __syncwarp();
     }
   } else if (warp == kLoadWarp) {
     // ---------------- TMA ----------------
@@ -254,7 +276,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, 2 * kCols);
   }
-  if (args.split > 1) lin_cluster_sync();  // nobody writes to a CTA that is gone
+  if (args.split > 1) {
+    // Parts can be on their way only after a role gave up: they are given a
+    // millisecond, a thousand times what they take.
+    if (*const_cast<volatile int *>(&ctl->abort)) {
+      const uint64_t t0 = globaltimer();
+      while (globaltimer() - t0 < 1000000) {
+      }
+    }
+    lin_cluster_sync();  // nobody writes to a CTA that is gone
+  }
 }
 
 template <int kCols, bool kGated>
@@ -286,9 +317,15 @@ int launch(const spec_target &h, const LinearParams &P, cudaStream_t stream) {
       clusters = c;
     }
   }
-  const int per = (static_cast<int>(P.M) + args.split - 1) / args.split;
-  const int fixed = 1024 + args.split * per * kLanes * 4 + static_cast<int>(sizeof(Ctl));
-  args.stages = (h.smem_optin - fixed) / stage_bytes<kCols>();
+  const int per = ((static_cast<int>(P.M) + args.split - 1) / args.split + 3) / 4 * 4;
+  args.per = per;
+  args.bufs = P.M <= 32 ? 2 : 1;
+  const int fixed =
+      1024 + args.bufs * args.split * per * kLanes * 4 + static_cast<int>(sizeof(Ctl));
+  // Up to 32 rows two CTAs share an SM, so that the next kernel of a stream starts
+  // and reads ahead while this one ends.
+  const int room = P.M <= 32 ? h.smem_optin / 2 - 1024 : h.smem_optin;
+  args.stages = (room - fixed) / stage_bytes<kCols>();
   if (args.stages > kMaxStages) args.stages = kMaxStages;
   if (args.stages < 2) return SV_ERR_CUDA;
   const int smem = fixed + args.stages * stage_bytes<kCols>();

@@ -75,11 +75,24 @@ __device__ __forceinline__ uint32_t lin_remote(uint32_t smem_addr, uint32_t rank
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_addr), "r"(rank));
   return at;
 }
-__device__ __forceinline__ void lin_store_remote(uint32_t at, float x) {
-  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(x) : "memory");
+// (the store counts its 16 bytes on a barrier of the same CTA, so that it needs no
+// fence and no arrival of its own)
+__device__ __forceinline__ void lin_store_remote(uint32_t at, const uint32_t *x, uint32_t bar) {
+  asm volatile(
+      "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];"
+      ::"r"(at), "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(bar)
+      : "memory");
 }
 __device__ __forceinline__ void lin_arrive_remote(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
+               : "memory");
+}
+
+// Brings a box into L2.
+__device__ __forceinline__ void lin_prefetch(const CUtensorMap *m, int32_t c0, int32_t c1) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global [%0, {%1, %2}];" ::"l"(
+                   reinterpret_cast<uint64_t>(m)),
+               "r"(c0), "r"(c1)
                : "memory");
 }
 
