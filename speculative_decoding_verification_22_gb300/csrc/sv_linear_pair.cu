@@ -11,6 +11,8 @@
 //    tile's products, in the other half of tensor memory.
 //  * Warp 8: TMA of its CTA; warp 9: products, in the first CTA of the pair alone.
 //  * The columns of a tile are chosen so that the tiles fill whole waves.
+#include <algorithm>
+
 #include "sv_linear_tc.cuh"
 
 namespace sv {
@@ -28,15 +30,16 @@ struct Args {
   uint64_t limit_ns;
   int bn;                      // columns of a tile: rows of the weight(s)
   int row_tiles, col_tiles, group;
+  int split;                   // pairs that share a tile, each a part of K
   int kblocks, stages;
-  int bf16, fast;              // fast: 16-byte accesses of the output's rows
-  int fast_res, fast_bias;
+  int bf16, fast_bias;
+  int wide;  // 16-byte accesses of the output's and the residual's rows
 };
 
 struct Ctl {
   uint64_t full[kMaxStages], empty[kMaxStages];
   uint64_t tfull[2], tempty[2];
-  uint64_t teardown;
+  uint64_t teardown, parts;
   uint32_t tmem;
   int abort;
 };
@@ -64,13 +67,13 @@ __device__ __forceinline__ void umma_pair(uint32_t d, uint64_t a, uint64_t b, ui
       "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-// Arrives on the barrier at this offset in both CTAs when the products issued so
-// far have completed.
-__device__ __forceinline__ void commit_pair(uint32_t bar) {
+// Arrives on the barrier at this offset in both CTAs of the pair (`mask`) when the
+// products issued so far have completed.
+__device__ __forceinline__ void commit_pair(uint32_t bar, uint16_t mask) {
   asm volatile(
       "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
       "[%0], %1;" ::"r"(bar),
-      "h"(static_cast<uint16_t>(3))
+      "h"(mask)
       : "memory");
 }
 // A load into this CTA that completes on a barrier of either.
@@ -175,8 +178,70 @@ __device__ __forceinline__ void place(const Args &a, int tile, int &tr, int &tc)
   tc = in / rows;
 }
 
+// Where an epilogue's rows go: the tile's rows of a warp and its piece of shared
+// memory.
+struct Rows {
+  int64_t m0;       // the warp's first row
+  float *piece;     // 32 x 32, for rows that are not written in wide stores
+};
+
+// 32 columns of a row a thread, from their sums to the output: y of x w^T (or of the
+// gate's), u of the second factor.  `in` columns from n on are inside.
 template <bool kGated>
-__global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
+__device__ __forceinline__ void finish(const Args &args, const Rows &rows, int64_t n, int in,
+                                       float (&y)[32], const uint32_t *u) {
+  const LinearParams &p = args.p;
+  const int lane = threadIdx.x & 31;
+  float b[32];
+  if (p.bias) {
+    load_row32(p.bias, n, in, p.dtype, args.fast_bias, b);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) y[i] += b[i];
+  }
+  activate32(y, p.act);
+  if constexpr (kGated) {
+    if (p.bias_u) {
+      load_row32(p.bias_u, n, in, p.dtype, args.fast_bias, b);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) y[i] *= __uint_as_float(u[i]) + b[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) y[i] *= __uint_as_float(u[i]);
+    }
+  }
+  if (args.wide) {
+    const int64_t m = rows.m0 + lane;
+    if (m < p.M) {
+      if (p.res) {
+        load_row32(p.res, m * p.rs + n, in, p.out_dtype, true, b);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) y[i] += b[i];
+      }
+      store_row32(p.out, m * p.os + n, in, p.out_dtype, true, y);
+    }
+  } else {
+    // through shared memory, a row at a time with a lane for each column (rows of an
+    // odd stride by single elements of 32 rows at once: 57 us of 205 x 8190 x 8192
+    // against 40)
+#pragma unroll
+    for (int i = 0; i < 32; ++i) rows.piece[lane * 32 + (i ^ lane)] = y[i];
+    __syncwarp();
+    const int live = static_cast<int>(min(static_cast<int64_t>(32), p.M - rows.m0));
+#pragma unroll 8
+    for (int r = 0; r < live; ++r) {
+      float v = rows.piece[r * 32 + (lane ^ r)];
+      const int64_t m = rows.m0 + r;
+      if (lane < in) {
+        if (p.res) v += load_any(p.res, m * p.rs + n + lane, p.out_dtype);
+        store_any(p.out, m * p.os + n + lane, v, p.out_dtype);
+      }
+    }
+  }
+  __syncwarp();
+}
+
+template <bool kGated>
+__global__ void __launch_bounds__(kThreads, 1)
     linear_pair_kernel(const __grid_constant__ CUtensorMap tmX,
                        const __grid_constant__ CUtensorMap tmW,
                        const __grid_constant__ CUtensorMap tmU, const __grid_constant__ Args args) {
@@ -184,10 +249,12 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
-  Ctl *ctl = reinterpret_cast<Ctl *>(smem_raw + (base - raw) + kMaxStages * kStage);
+  uint8_t *smem = smem_raw + (base - raw);
+  Ctl *ctl = reinterpret_cast<Ctl *>(smem + kMaxStages * kStage);
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
-  const int rank = static_cast<int>(lin_cluster_rank());
+  const int crank = static_cast<int>(lin_cluster_rank());
+  const int rank = crank & 1, part = crank >> 1;  // in the pair; the pair in the cluster
   const LinAbort ab{args.status, args.limit_ns, &ctl->abort};
 
   if (tid == 0) {
@@ -200,6 +267,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       mbar_init(smem_u32(&ctl->tempty[i]), 2 * kEpiWarps);
     }
     mbar_init(smem_u32(&ctl->teardown), 1);
+    mbar_init(smem_u32(&ctl->parts), 1);
     ctl->abort = 0;
     mbar_fence_init();
   }
@@ -213,69 +281,51 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, ctl->tmem, 0);
-  lin_cluster_sync();  // the barriers of both CTAs are set up
+  lin_cluster_sync();  // the barriers of all CTAs are set up
   pdl_wait();
   pdl_launch_dependents();
 
-  const int first = blockIdx.x / 2, step = gridDim.x / 2;
+  const int first = blockIdx.x / (2 * args.split), step = gridDim.x / (2 * args.split);
   const int tiles = args.row_tiles * args.col_tiles;
   const int half = args.bn / 2;                   // weight rows that a CTA loads
   const int cols = kGated ? half : args.bn;       // output columns of a tile
+  const int kb0 = static_cast<int>(static_cast<int64_t>(args.kblocks) * part / args.split);
+  const int kb1 = static_cast<int>(static_cast<int64_t>(args.kblocks) * (part + 1) / args.split);
+  // an epilogue warp's lanes of tensor memory and rows of the tile
+  const uint32_t tacc = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+  Rows rows;
+  rows.piece = reinterpret_cast<float *>(smem + (kMaxStages - 1) * kStage) + (warp & 7) * 1024;
+  auto inside = [&](int64_t n, int c) {  // columns of the output from n on, tile column c
+    return static_cast<int>(min(p.N - n, static_cast<int64_t>(min(32, cols - c))));
+  };
+  bool ok = true;
 
   if (warp < kEpiWarps) {
     // ---------------- epilogue ----------------
-    const int row = (warp & 3) * 32 + lane;
-    const uint32_t tacc = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-    const uint32_t tempty0 = lin_remote(smem_u32(&ctl->tempty[0]), 0);
+    const uint32_t tempty0 = lin_remote(smem_u32(&ctl->tempty[0]), crank & ~1);
     uint32_t it = 0;
-    bool ok = true;
     for (int tile = first; tile < tiles && ok; tile += step, ++it) {
       int tr, tc;
       place(args, tile, tr, tc);
       const uint32_t slot = it & 1;
       if (!(ok = lin_wait(smem_u32(&ctl->tfull[slot]), it >> 1 & 1, ab))) break;
+      if (args.split > 1) break;  // goes on below
       tc_fence_after();
-      const int64_t m = static_cast<int64_t>(tr) * 256 + rank * kLanes + row;
-      const bool live = m < p.M;
+      rows.m0 = static_cast<int64_t>(tr) * 256 + rank * kLanes + (warp & 3) * 32;
       for (int c = (warp >> 2) * 32; c < cols; c += 64) {
         const int64_t n = static_cast<int64_t>(tc) * cols + c;
-        const int in = static_cast<int>(min(p.N - n, static_cast<int64_t>(min(32, cols - c))));
+        const int in = inside(n, c);
         if (in <= 0) break;
         uint32_t x[32], u[kGated ? 32 : 1];
         tmem_ld32(tacc + slot * 256 + c, x);
         if (kGated) tmem_ld32(tacc + slot * 256 + half + c, u);
-        float b[32];
-        if (p.bias) load_row32(p.bias, n, in, p.dtype, args.fast_bias, b);
         tmem_ld_wait();
         tmem_reg_fence32(x);
         if (kGated) tmem_reg_fence32(u);
         float y[32];
 #pragma unroll
         for (int i = 0; i < 32; ++i) y[i] = __uint_as_float(x[i]);
-        if (p.bias) {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) y[i] += b[i];
-        }
-        activate32(y, p.act);
-        if (kGated) {
-          if (p.bias_u) {
-            load_row32(p.bias_u, n, in, p.dtype, args.fast_bias, b);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) y[i] *= __uint_as_float(u[i]) + b[i];
-          } else {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) y[i] *= __uint_as_float(u[i]);
-          }
-        }
-        if (live) {
-          if (p.res) {
-            load_row32(p.res, m * p.rs + n, in, p.out_dtype, args.fast_res, b);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) y[i] += b[i];
-          }
-          store_row32(p.out, m * p.os + n, in, p.out_dtype, args.fast, y);
-        }
-        __syncwarp();
+        finish<kGated>(args, rows, n, in, y, u);
       }
       tc_fence_before();
       __syncwarp();
@@ -286,16 +336,15 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     // ---------------- TMA ----------------
     const uint64_t policy = policy_evict_normal();
     const CUtensorMap *tmB = kGated && rank ? &tmU : &tmW;
-    const uint32_t full0 = lin_remote(smem_u32(&ctl->full[0]), 0);
+    const uint32_t full0 = lin_remote(smem_u32(&ctl->full[0]), crank & ~1);
     int stage = 0;
     uint32_t phase = 0;
-    bool ok = true;
     for (int tile = first; tile < tiles && ok; tile += step) {
       int tr, tc;
       place(args, tile, tr, tc);
       const int m0 = tr * 256 + rank * kLanes;
       const int n0 = kGated ? tc * half : tc * args.bn + rank * half;
-      for (int kb = 0; kb < args.kblocks; ++kb) {
+      for (int kb = kb0; kb < kb1; ++kb) {
         if (!(ok = lin_wait(smem_u32(&ctl->empty[stage]), phase ^ 1u, ab))) break;
         if (lane == 0) {
           // the first CTA's barrier counts the bytes of both
@@ -315,14 +364,14 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   } else if (rank == 0) {
     // ---------------- products ----------------
     const uint32_t idesc = idesc_16(args.bf16, 256, args.bn, false);
+    const uint16_t mask = static_cast<uint16_t>(3u << (crank & ~1));
     int stage = 0;
     uint32_t phase = 0, it = 0;
-    bool ok = true;
     for (int tile = first; tile < tiles && ok; tile += step, ++it) {
       const uint32_t slot = it & 1;
       if (!(ok = lin_wait<true>(smem_u32(&ctl->tempty[slot]), (it >> 1 & 1) ^ 1u, ab))) break;
       tc_fence_after();
-      for (int kb = 0; kb < args.kblocks; ++kb) {
+      for (int kb = kb0; kb < kb1; ++kb) {
         if (!(ok = lin_wait<true>(smem_u32(&ctl->full[stage]), phase, ab))) break;
         tc_fence_after();
         if (elect_one()) {
@@ -330,9 +379,9 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
           const uint64_t ad = sw128_desc(at), bd = sw128_desc(at + kLanes * 128);
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            umma_pair(tmem + slot * 256, ad + 2u * k, bd + 2u * k, idesc, kb > 0 || k > 0);
-          commit_pair(smem_u32(&ctl->empty[stage]));
-          if (kb == args.kblocks - 1) commit_pair(smem_u32(&ctl->tfull[slot]));
+            umma_pair(tmem + slot * 256, ad + 2u * k, bd + 2u * k, idesc, kb > kb0 || k > 0);
+          commit_pair(smem_u32(&ctl->empty[stage]), mask);
+          if (kb == kb1 - 1) commit_pair(smem_u32(&ctl->tfull[slot]), mask);
         }
         __syncwarp();
         if (++stage == args.stages) {
@@ -341,14 +390,85 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         }
       }
     }
-    if (elect_one()) commit_pair(smem_u32(&ctl->teardown));
+    if (elect_one()) commit_pair(smem_u32(&ctl->teardown), mask);
     __syncwarp();
+  }
+
+  if (args.split > 1) {
+    // ---------------- the parts of K meet ----------------
+    // Pair q of the cluster finishes the tile's columns [q own, (q + 1) own): the
+    // other pairs' sums of these come into its ring, which by now is idle, as
+    // [pair][column / 4][row][column % 4] (gated: of both factors).
+    lin_cluster_sync();
+    if (warp < kEpiWarps && ok) {
+      const int own = cols / args.split;
+      const int width = kGated ? 2 * own : own;  // columns of a part
+      const uint32_t bar = smem_u32(&ctl->parts);
+      if (tid == 0) mbar_arrive_expect_tx(bar, (args.split - 1) * width * kLanes * 4);
+      int tr, tc;
+      place(args, first, tr, tc);
+      tc_fence_after();
+      const int row = (warp & 3) * 32 + lane;
+      for (int d = 1; d < args.split; ++d) {
+        const int q = (part + d) % args.split;
+        // this pair's place among the parts of q
+        const int at = part < q ? part : part - 1;
+        const uint32_t to = lin_remote(base + (at * width * kLanes + row * 4) * 4, 2 * q + rank);
+        const uint32_t to_bar = lin_remote(bar, 2 * q + rank);
+        for (int v = (warp >> 2) * 32; v < width; v += 64) {
+          const int c = v < own ? q * own + v : half + q * own + v - own;
+          uint32_t x[32];
+          tmem_ld32(tacc + c, x);
+          tmem_ld_wait();
+          tmem_reg_fence32(x);
+#pragma unroll
+          for (int e = 0; e < 32; e += 4)
+            lin_store_remote(to + (v + e) * kLanes * 4, x + e, to_bar);
+        }
+      }
+      __syncwarp();
+      ok = lin_wait<true>(bar, 0, ab);
+      rows.m0 = static_cast<int64_t>(tr) * 256 + rank * kLanes + (warp & 3) * 32;
+      const float4 *in_parts = reinterpret_cast<const float4 *>(smem);
+      for (int v = (warp >> 2) * 32; v < own && ok; v += 64) {
+        const int64_t n = static_cast<int64_t>(tc) * cols + part * own + v;
+        const int in = inside(n, part * own + v);
+        if (in <= 0) break;
+        // the sums in the order of K
+        auto total = [&](int c, int at, float (&y)[32]) {
+          uint32_t x[32];
+          tmem_ld32(tacc + c, x);
+          tmem_ld_wait();
+          tmem_reg_fence32(x);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) y[e] = 0.0f;
+          for (int q = 0; q < args.split; ++q) {
+            if (q == part) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e) y[e] += __uint_as_float(x[e]);
+            } else {
+              const float4 *f =
+                  in_parts + ((q < part ? q : q - 1) * width + at) / 4 * kLanes + row;
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const float4 a = f[e * kLanes];
+                y[4 * e] += a.x, y[4 * e + 1] += a.y, y[4 * e + 2] += a.z, y[4 * e + 3] += a.w;
+              }
+            }
+          }
+        };
+        float y[32], u[32];
+        total(part * own + v, v, y);
+        if (kGated) total(half + part * own + v, own + v, u);
+        finish<kGated>(args, rows, n, in, y, reinterpret_cast<const uint32_t *>(u));
+      }
+    }
   }
 
   // ---------------- teardown ----------------
   // The products are done (their commit arrives in both CTAs); a copy can be in
-  // flight only after a role gave up, and then on a barrier of the other CTA: it
-  // is given a millisecond, a thousand times what it takes.
+  // flight only after a role gave up, and then on a barrier of another CTA: it is
+  // given a millisecond, a thousand times what it takes.
   if (warp == kLoadWarp) {
     const int never = 0;
     if (lane == 0) {
@@ -379,20 +499,29 @@ int launch(const spec_target &h, const LinearParams &P, cudaStream_t stream) {
   args.limit_ns = h.wait_limit_ns;
   args.bf16 = P.dtype == SV_BF16;
   args.kblocks = static_cast<int>((P.K + kLinBlk - 1) / kLinBlk);
-  args.stages = kMaxStages;
-  const int pairs = h.num_sms / 2;
   const int64_t row_tiles = (P.M + 255) / 256;
-  // Columns of a tile: whole waves of tiles, each of the time of its columns (and
-  // of 16 more for what a tile takes by itself).
+  // Columns of a tile, and pairs that share one: by the time of a K block, which is
+  // that of its products (two cycles a column) or of its loads (about 40 bytes a
+  // cycle), the waves of tiles, and what a tile takes besides.
   int64_t best = INT64_MAX, col_tiles = 0;
-  for (int bn = 256; bn >= 64; bn -= 32) {
-    const int cols = kGated ? bn / 2 : bn;
-    const int64_t ct = (P.N + cols - 1) / cols;
-    const int64_t time = (row_tiles * ct + pairs - 1) / pairs * (bn + 16);
-    if (time < best) {
-      best = time;
-      args.bn = bn;
-      col_tiles = ct;
+  for (int split = 1; split <= 4; split *= 2) {
+    const int64_t clusters = split == 1 ? h.num_sms / 2 : h.clusters[2 * split];
+    if (split > args.kblocks) break;
+    for (int bn = 256; bn >= 64; bn -= 32) {
+      const int cols = kGated ? bn / 2 : bn;
+      if (split > 1 && cols % (32 * split) != 0) continue;
+      const int64_t ct = (P.N + cols - 1) / cols, tiles = row_tiles * ct;
+      if (split > 1 && tiles > clusters) continue;  // a cluster takes one tile
+      const int64_t block = std::max(2 * bn, (kLanes + bn / 2) * 128 / 40);
+      const int64_t time = (tiles + clusters - 1) / clusters *
+                               ((args.kblocks + split - 1) / split * block + 16 * bn) +
+                           (split > 1 ? 4000 : 0);
+      if (time < best) {
+        best = time;
+        args.bn = bn;
+        args.split = split;
+        col_tiles = ct;
+      }
     }
   }
   if (row_tiles * col_tiles > (1 << 30)) return SV_ERR_SHAPE;
@@ -403,8 +532,8 @@ int launch(const spec_target &h, const LinearParams &P, cudaStream_t stream) {
   auto wide = [](const void *p, int64_t stride_bytes, int64_t rows) {
     return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && (rows <= 1 || stride_bytes % 16 == 0);
   };
-  args.fast = wide(P.out, P.os * es, P.M);
-  args.fast_res = wide(P.res, P.rs * es, P.M);
+  args.wide = wide(P.out, P.os * es, P.M) && wide(P.res, P.rs * es, P.M);
+  args.stages = args.wide || args.split > 1 ? kMaxStages : kMaxStages - 1;
   args.fast_bias = wide(P.bias, 0, 1) && wide(P.bias_u, 0, 1);
   CUtensorMap x, w, u;
   if (!lin_encode(&x, P.x, P.xs, P.K, P.M, kLanes) ||
@@ -415,9 +544,22 @@ int launch(const spec_target &h, const LinearParams &P, cudaStream_t stream) {
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
   if (e != cudaSuccess) return SV_ERR_CUDA;
   const int64_t tiles = row_tiles * col_tiles;
-  const int grid = 2 * static_cast<int>(tiles < pairs ? tiles : pairs);
-  e = launch_chained(linear_pair_kernel<kGated>, dim3(grid), dim3(kThreads), kSmemBytes, stream, x,
-                     w, u, args);
+  const int64_t pairs = args.split > 1 ? tiles * args.split
+                                       : std::min<int64_t>(tiles, h.num_sms / 2);
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2 * args.split;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  e = cudaLaunchKernelEx(&cfg, linear_pair_kernel<kGated>, x, w, u, args);
   return e == cudaSuccess ? SV_OK : SV_ERR_CUDA;
 }
 
