@@ -157,17 +157,33 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&ctl->tempty[slot]));
       __syncwarp();
-      if (!(ok = lin_wait<true>(bar, xphase, ab))) break;
+      // A thread finishes column n of the output, four rows of x at a time, one in
+      // kStep; what it adds to 16 of them is loaded while their parts arrive.
+      constexpr int kStep = kLanes / kRows, kFours = 4;
       const int r = row % kRows;
       const int64_t n = static_cast<int64_t>(tile) * kRows + r;
-      if (n < p.N) {
-        const float b = p.bias ? load_any(p.bias, n, p.dtype) : 0.0f;
-        const float bu = kGated && p.bias_u ? load_any(p.bias_u, n, p.dtype) : 0.0f;
-        const float4 *in = reinterpret_cast<const float4 *>(buf);
-        for (int f = row / kRows; f < fours; f += kLanes / kRows) {
+      const bool in = n < p.N;
+      const float b = in && p.bias ? load_any(p.bias, n, p.dtype) : 0.0f;
+      const float bu = kGated && in && p.bias_u ? load_any(p.bias_u, n, p.dtype) : 0.0f;
+      float res[4 * kFours];
+      auto load_res = [&](int f0) {
+#pragma unroll
+        for (int i = 0; i < 4 * kFours; ++i) {
+          const int v = 4 * (f0 + i / 4 * kStep) + i % 4;
+          res[i] = v < mine ? load_any(p.res, (rank * per + v) * p.rs + n, p.out_dtype) : 0.0f;
+        }
+      };
+      if (p.res && in) load_res(row / kRows);
+      if (!(ok = lin_wait<true>(bar, xphase, ab))) break;
+      const float4 *in_parts = reinterpret_cast<const float4 *>(buf) + r;
+      for (int f0 = row / kRows; f0 < fours && in; f0 += kFours * kStep) {
+#pragma unroll
+        for (int i = 0; i < kFours; ++i) {
+          const int f = f0 + i * kStep;
+          if (f >= fours) break;
           float y[4] = {}, u[4] = {};
           for (int s = 0; s < args.split; ++s) {
-            const float4 *part = in + (s * (per / 4) + f) * kLanes + r;
+            const float4 *part = in_parts + (s * (per / 4) + f) * kLanes;
             const float4 a = part[0];
             y[0] += a.x, y[1] += a.y, y[2] += a.z, y[3] += a.w;
             if (kGated) {
@@ -178,13 +194,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             if (4 * f + e >= mine) break;
-            const int64_t m = rank * per + 4 * f + e;
             float v = activate(y[e] + b, p.act);
             if (kGated) v *= u[e] + bu;
-            if (p.res) v += load_any(p.res, m * p.rs + n, p.out_dtype);
-            store_any(p.out, m * p.os + n, v, p.out_dtype);
+            if (p.res) v += res[4 * i + e];
+            store_any(p.out, (rank * per + 4 * f + e) * p.os + n, v, p.out_dtype);
           }
         }
+        if (p.res && f0 + kFours * kStep < fours) load_res(f0 + kFours * kStep);
       }
       __syncwarp();
       if (lane < args.split) lin_arrive_remote(lin_remote(smem_u32(&ctl->xempty[xslot]), lane));
