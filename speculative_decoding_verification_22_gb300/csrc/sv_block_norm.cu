@@ -11,6 +11,7 @@
 // several short rows.  Sixteen lanes hold the 128 columns of one scale, so a
 // block's maximum is four shuffles.
 #include "sv_target.cuh"
+#include "sv_tmem.cuh"
 
 namespace sv {
 namespace {
@@ -30,32 +31,64 @@ __device__ __forceinline__ float row_reduce(float v, float *red, int wpr, int wa
   for (int i = 1; i < wpr; ++i) r = op(r, red[first + i]);
   return r;
 }
-// scale = max(amax, 1e-30) / 448; y * (1 / scale) in place of y / scale is one
-// more rounding in fp32, 2^-24 against E4M3's 2^-4.
+// scale = max(amax, 1e-30) / 448
 __device__ __forceinline__ float e4m3_scale(float amax) { return max_nan(amax, 1e-30f) / 448.0f; }
-__device__ __forceinline__ uint2 to_e4m3x8(const float (&y)[8], float inv) {
+
+// Two neighbouring elements as fp32 pairs and back: the arithmetic below takes two
+// columns an instruction.
+template <class T>
+__device__ __forceinline__ uint64_t widen(const Vec8<T> &v, int i) {
+  return pair2(to_float(v.e[2 * i]), to_float(v.e[2 * i + 1]));
+}
+template <>
+__device__ __forceinline__ uint64_t widen(const Vec8<__nv_bfloat16> &v, int i) {
+  const uint32_t w = reinterpret_cast<const uint32_t *>(&v)[i];
+  return pair2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+__device__ __forceinline__ void narrow(Vec8<float> &o, int i, uint64_t x) {
+  const float2 f = unpair2(x);
+  o.e[2 * i] = f.x;
+  o.e[2 * i + 1] = f.y;
+}
+__device__ __forceinline__ void narrow(Vec8<__half> &o, int i, uint64_t x) {
+  const float2 f = unpair2(x);
+  reinterpret_cast<__half2 *>(&o)[i] = __floats2half2_rn(f.x, f.y);
+}
+__device__ __forceinline__ void narrow(Vec8<__nv_bfloat16> &o, int i, uint64_t x) {
+  const float2 f = unpair2(x);
+  reinterpret_cast<__nv_bfloat162 *>(&o)[i] = __floats2bfloat162_rn(f.x, f.y);
+}
+// y * (1 / scale) in place of y / scale: one more rounding in fp32, 2^-24 against
+// E4M3's 2^-4.
+__device__ __forceinline__ uint2 to_e4m3x8(const uint64_t (&y)[4], float inv) {
+  const uint64_t inv2 = pair2(inv, inv);
   uint32_t h[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    h[i] = __nv_cvt_float2_to_fp8x2(make_float2(y[2 * i] * inv, y[2 * i + 1] * inv),
-                                    __NV_SATFINITE, __NV_E4M3);
+    h[i] = __nv_cvt_float2_to_fp8x2(unpair2(mul2(y[i], inv2)), __NV_SATFINITE, __NV_E4M3);
   return make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
+}
+__device__ __forceinline__ float sum2(uint64_t x) {
+  const float2 f = unpair2(x);
+  return f.x + f.y;
 }
 
 template <class T, int kVec, int kQuant, int kMost>
-__global__ void __launch_bounds__(kMost, kMost <= 256 && kVec == 2 ? 4 : 1)
-    block_norm_kernel(const sv_block_norm_t P, int wpr) {
+__global__ void __launch_bounds__(kMost, kMost > 256 ? 1 : kVec >= 2 ? 4 : 1)
+    block_norm_kernel(const sv_block_norm_t P, int wpr, float inv_d) {
   __shared__ float red[3][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t row = static_cast<int64_t>(blockIdx.x) * ((blockDim.x >> 5) / wpr) + warp / wpr;
   const bool live = row < P.rows;
   const int t0 = (warp % wpr) * 32 + lane, step = wpr * 32;
-  const int d = static_cast<int>(P.d), nvec = d >> 3;
+  const int d = static_cast<int>(P.d);
+  const int nvec = live ? d >> 3 : 0;  // of this thread's row
   const T *post = static_cast<const T *>(P.post_weight), *w = static_cast<const T *>(P.weight);
+  const T *gate = P.gate ? static_cast<const T *>(P.gate) + row * P.gate_row : nullptr;
   pdl_wait();
   pdl_launch_dependents();
   const auto add = [](float a, float b) { return a + b; };
-  float h[kVec][8];
+  uint64_t h[kVec][4];
   Vec8<T> rv[kVec];
   {
     const T *x = static_cast<const T *>(P.x) + row * P.x_stride;
@@ -64,87 +97,92 @@ __global__ void __launch_bounds__(kMost, kMost <= 256 && kVec == 2 ? 4 : 1)
 #pragma unroll
     for (int v = 0; v < kVec; ++v) {
       const int i = t0 + v * step;
-      if (live && i < nvec) {
+      if (i < nvec) {
         xv[v] = load8(x + 8 * i);
         rv[v] = load8(r + 8 * i);
       }
     }
-    float ss = 0.0f;
+    uint64_t ss = 0;
 #pragma unroll
     for (int v = 0; v < kVec; ++v) {
-      const bool in = live && t0 + v * step < nvec;
+      const bool in = t0 + v * step < nvec;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        h[v][e] = in ? to_float(xv[v].e[e]) : 0.0f;
-        ss = fmaf(h[v][e], h[v][e], ss);
+      for (int e = 0; e < 4; ++e) {
+        h[v][e] = in ? widen(xv[v], e) : 0;
+        ss = fma2(h[v][e], h[v][e], ss);
       }
     }
     if (post) {
-      ss = row_reduce(ss, red[0], wpr, warp, lane, add);
-      const float inv = 1.0f / sqrtf(ss / static_cast<float>(d) + P.eps);
+      const float all = row_reduce(sum2(ss), red[0], wpr, warp, lane, add);
+      const float inv = rsqrtf(fmaf(all, inv_d, P.eps));
+      const uint64_t inv2 = pair2(inv, inv);
 #pragma unroll
       for (int v = 0; v < kVec; ++v) {
         const int i = t0 + v * step;
-        if (live && i < nvec) {
+        if (i < nvec) {
           const Vec8<T> pv = load8(post + 8 * i);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) h[v][e] = h[v][e] * inv * to_float(pv.e[e]);
+          for (int e = 0; e < 4; ++e) h[v][e] = mul2(mul2(h[v][e], inv2), widen(pv, e));
         }
       }
     }
   }
   float scale = P.branch_scale;
-  const T *gate = P.gate ? static_cast<const T *>(P.gate) + row * P.gate_row : nullptr;
   if (gate && P.gate_col == 0) {
     if (live) scale *= to_float(gate[0]);
     gate = nullptr;
   }
-  float ss = 0.0f;
+  const uint64_t scale2 = pair2(scale, scale);
+  uint64_t ss = 0;
 #pragma unroll
   for (int v = 0; v < kVec; ++v) {
     const int i = t0 + v * step;
-    if (live && i < nvec) {
+    if (i < nvec) {
       if (gate) {
         const Vec8<T> gv = load8(gate + 8 * i);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) h[v][e] *= to_float(gv.e[e]);
+        for (int e = 0; e < 4; ++e) h[v][e] = mul2(h[v][e], widen(gv, e));
       }
       Vec8<T> o;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        h[v][e] = fmaf(scale, h[v][e], to_float(rv[v].e[e]));
-        ss = fmaf(h[v][e], h[v][e], ss);
-        o.e[e] = from_float<T>(h[v][e]);
+      for (int e = 0; e < 4; ++e) {
+        h[v][e] = fma2(scale2, h[v][e], widen(rv[v], e));
+        ss = fma2(h[v][e], h[v][e], ss);
+        narrow(o, e, h[v][e]);
       }
       if (P.residual_out)
         store8(static_cast<T *>(P.residual_out) + row * P.residual_out_stride + 8 * i, o);
     }
   }
-  ss = row_reduce(ss, red[1], wpr, warp, lane, add);
-  const float inv = 1.0f / sqrtf(ss / static_cast<float>(d) + P.eps);
+  const float all = row_reduce(sum2(ss), red[1], wpr, warp, lane, add);
+  const float inv = rsqrtf(fmaf(all, inv_d, P.eps));
+  const uint64_t inv2 = pair2(inv, inv);
 
   float rmax = 0.0f;
 #pragma unroll
   for (int v = 0; v < kVec; ++v) {
     const int i = t0 + v * step;
-    const bool in = live && i < nvec;
+    const bool in = i < nvec;
     if (in) {
       const Vec8<T> wv = load8(w + 8 * i);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) h[v][e] = h[v][e] * inv * to_float(wv.e[e]);
+      for (int e = 0; e < 4; ++e) h[v][e] = mul2(mul2(h[v][e], inv2), widen(wv, e));
     }
     if constexpr (kQuant == 0) {
       if (in) {
         Vec8<T> o;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) o.e[e] = from_float<T>(h[v][e]);
+        for (int e = 0; e < 4; ++e) narrow(o, e, h[v][e]);
         store8(static_cast<T *>(P.out) + row * P.out_stride + 8 * i, o);
       }
     } else {
       // lanes past the row hold zeros
       float m = 0.0f;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) m = max_nan(m, fabsf(h[v][e]));
+      for (int e = 0; e < 4; ++e) {
+        const float2 f = unpair2(h[v][e]);
+        m = max3_nan(m, fabsf(f.x), fabsf(f.y));
+      }
       if constexpr (kQuant == 1) {
 #pragma unroll
         for (int o = 8; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
@@ -166,7 +204,7 @@ __global__ void __launch_bounds__(kMost, kMost <= 256 && kVec == 2 ? 4 : 1)
 #pragma unroll
     for (int v = 0; v < kVec; ++v) {
       const int i = t0 + v * step;
-      if (live && i < nvec)
+      if (i < nvec)
         *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(P.out) + row * d + 8 * i) =
             to_e4m3x8(h[v], inv_s);
     }
@@ -284,11 +322,15 @@ template <class T, int kVec, int kMost>
 cudaError_t launch_block(const sv_block_norm_t &a, int wpr, int per_block, cudaStream_t stream) {
   const dim3 grid(static_cast<unsigned>((a.rows + per_block - 1) / per_block));
   const dim3 block(32 * wpr * per_block);
+  const float inv_d = 1.0f / static_cast<float>(a.d);
   if (a.group < 0)
-    return launch_chained(block_norm_kernel<T, kVec, 0, kMost>, grid, block, 0, stream, a, wpr);
+    return launch_chained(block_norm_kernel<T, kVec, 0, kMost>, grid, block, 0, stream, a, wpr,
+                          inv_d);
   if (a.group > 0)
-    return launch_chained(block_norm_kernel<T, kVec, 1, kMost>, grid, block, 0, stream, a, wpr);
-  return launch_chained(block_norm_kernel<T, kVec, 2, kMost>, grid, block, 0, stream, a, wpr);
+    return launch_chained(block_norm_kernel<T, kVec, 1, kMost>, grid, block, 0, stream, a, wpr,
+                          inv_d);
+  return launch_chained(block_norm_kernel<T, kVec, 2, kMost>, grid, block, 0, stream, a, wpr,
+                          inv_d);
 }
 template <class T, int kVec>
 cudaError_t launch_vec(const sv_block_norm_t &a, cudaStream_t stream) {
@@ -314,7 +356,12 @@ cudaError_t launch_typed(const sv_block_norm_t &a, int num_sms, cudaStream_t str
     return launch_chained(block_norm_any_kernel<T>, dim3(static_cast<unsigned>(a.rows)),
                           dim3(kThreads), 0, stream, a);
   const int64_t nvec = a.d / 8;
-  const int kvec = nvec > 2048 ? 4 : (a.rows <= num_sms && nvec <= 1024) || nvec <= 128 ? 1 : 2;
+  // Few rows: one vector a thread, as many threads as that takes.  Many: four of 16-bit
+  // rows (16384 rows of 4096 in bf16 to E4M3 with a gate: 93 us, 5.1 TB/s; 112 with
+  // two; 4000 of 8192 to E4M3 49 against 65), two of fp32 rows (16384 of 4096 with a
+  // full gate: 212 us; 241 with four).
+  const int many = sizeof(T) == 2 || nvec > 2048 ? 4 : 2;
+  const int kvec = a.rows <= num_sms && nvec <= 1024 ? 1 : many;
   switch (kvec) {
     case 1: return launch_vec<T, 1>(a, stream);
     case 2: return launch_vec<T, 2>(a, stream);
