@@ -212,6 +212,112 @@ __global__ void __launch_bounds__(kMost, kMost > 256 ? 1 : kVec >= 2 ? 4 : 1)
   }
 }
 
+// Rows of any stride and alignment up to 8192 columns: one pass, as above, but an
+// element at a time.  A warp takes kGroups runs of 128 columns, lane l of them the
+// columns l, l + 32, ...
+template <class T, int kGroups>
+__global__ void __launch_bounds__(512, 2) block_norm_odd_kernel(const sv_block_norm_t P,
+                                                                float inv_d) {
+  constexpr int kEach = 4 * kGroups;
+  __shared__ float red[3][32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  const int64_t row = blockIdx.x;
+  const int d = static_cast<int>(P.d);
+  const T *x = static_cast<const T *>(P.x) + row * P.x_stride;
+  const T *r = static_cast<const T *>(P.residual) + row * P.residual_stride;
+  const T *gate = P.gate ? static_cast<const T *>(P.gate) + row * P.gate_row : nullptr;
+  const T *post = static_cast<const T *>(P.post_weight), *w = static_cast<const T *>(P.weight);
+  T *ro = P.residual_out ? static_cast<T *>(P.residual_out) + row * P.residual_out_stride
+                         : nullptr;
+  const int first = warp * (128 * kGroups) + lane;
+  pdl_wait();
+  pdl_launch_dependents();
+  const auto add = [](float a, float b) { return a + b; };
+  float h[kEach], res[kEach], ss = 0.0f;
+#pragma unroll
+  for (int k = 0; k < kEach; ++k) {
+    const int i = first + 32 * k;
+    h[k] = i < d ? to_float(x[i]) : 0.0f;
+    res[k] = i < d ? to_float(r[i]) : 0.0f;
+  }
+#pragma unroll
+  for (int k = 0; k < kEach; ++k) ss = fmaf(h[k], h[k], ss);
+  if (post) {
+    ss = row_reduce(ss, red[0], warps, warp, lane, add);
+    const float inv = rsqrtf(fmaf(ss, inv_d, P.eps));
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) {
+      const int i = first + 32 * k;
+      if (i < d) h[k] = h[k] * inv * to_float(post[i]);
+    }
+  }
+  float scale = P.branch_scale;
+  if (gate && P.gate_col == 0) {
+    scale *= to_float(gate[0]);
+    gate = nullptr;
+  }
+  ss = 0.0f;
+#pragma unroll
+  for (int k = 0; k < kEach; ++k) {
+    const int i = first + 32 * k;
+    if (i < d) {
+      if (gate) h[k] *= to_float(gate[i]);
+      h[k] = fmaf(scale, h[k], res[k]);
+      ss = fmaf(h[k], h[k], ss);
+      if (ro) ro[i] = from_float<T>(h[k]);
+    }
+  }
+  ss = row_reduce(ss, red[1], warps, warp, lane, add);
+  const float inv = rsqrtf(fmaf(ss, inv_d, P.eps));
+  float m = 0.0f;
+#pragma unroll
+  for (int k = 0; k < kEach; ++k) {
+    const int i = first + 32 * k;
+    if (i < d) {
+      h[k] = h[k] * inv * to_float(w[i]);
+      m = max_nan(m, fabsf(h[k]));
+    }
+  }
+  float s = 0.0f, inv_s = 0.0f;
+  if (P.group == 0) {
+    s = e4m3_scale(row_reduce(m, red[2], warps, warp, lane,
+                              [](float a, float b) { return max_nan(a, b); }));
+    inv_s = 1.0f / s;
+    if (threadIdx.x == 0) P.scale[row] = s;
+  }
+#pragma unroll
+  for (int g = 0; g < kGroups; ++g) {
+    const int block = warp * kGroups + g;
+    if (block * 128 >= d) break;
+    if (P.group > 0) {
+      float mb = 0.0f;
+#pragma unroll
+      for (int k = 4 * g; k < 4 * g + 4; ++k) mb = max_nan(mb, first + 32 * k < d ? fabsf(h[k]) : 0.0f);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) mb = max_nan(mb, __shfl_xor_sync(0xffffffffu, mb, o));
+      s = e4m3_scale(mb);
+      inv_s = 1.0f / s;
+      if (lane == 0) P.scale[row * ((d + 127) / 128) + block] = s;
+    }
+#pragma unroll
+    for (int k = 4 * g; k < 4 * g + 4; ++k) {
+      const int i = first + 32 * k;
+      if (i >= d) break;
+      if (P.group >= 0)
+        static_cast<uint8_t *>(P.out)[row * d + i] = static_cast<uint8_t>(
+            __nv_cvt_float_to_fp8(h[k] * inv_s, __NV_SATFINITE, __NV_E4M3));
+      else
+        static_cast<T *>(P.out)[row * P.out_stride + i] = from_float<T>(h[k]);
+    }
+  }
+}
+template <class T, int kGroups>
+cudaError_t launch_odd(const sv_block_norm_t &a, cudaStream_t stream) {
+  const int warps = static_cast<int>((a.d + 128 * kGroups - 1) / (128 * kGroups));
+  return launch_chained(block_norm_odd_kernel<T, kGroups>, dim3(static_cast<unsigned>(a.rows)),
+                        dim3(32 * warps), 0, stream, a, 1.0f / static_cast<float>(a.d));
+}
+
 constexpr int kThreads = 512;  // of the form below
 
 template <class Op>
@@ -225,7 +331,7 @@ __device__ __forceinline__ float block_reduce(float v, float *red, Op op) {
   return r;
 }
 
-// Rows of any width, stride and alignment: one block a row, the row read once for each of the sums, the maximum (row
+// What is left, rows of more columns: one block a row, the row read once for each of the sums, the maximum (row
 // scale) and the output.  A thread rereads only elements that it writes itself
 // and writes in the last pass alone, so the in-place forms hold.
 template <class T>
@@ -352,6 +458,9 @@ cudaError_t launch_typed(const sv_block_norm_t &a, int num_sms, cudaStream_t str
                    (!a.residual_out || ok(a.residual_out, a.residual_out_stride)) &&
                    (a.group >= 0 ? (reinterpret_cast<uintptr_t>(a.out) & 7u) == 0
                                  : ok(a.out, a.out_stride));
+  // One pass against the reads again: 16384 rows of 4095 in bf16 205 us against 295.
+  if (!vec && a.d <= 4096) return launch_odd<T, 2>(a, stream);
+  if (!vec && a.d <= 8192) return launch_odd<T, 4>(a, stream);
   if (!vec)
     return launch_chained(block_norm_any_kernel<T>, dim3(static_cast<unsigned>(a.rows)),
                           dim3(kThreads), 0, stream, a);
