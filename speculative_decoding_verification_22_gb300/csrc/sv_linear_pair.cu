@@ -32,14 +32,14 @@ struct Args {
   int row_tiles, col_tiles, group;
   int split;                   // pairs that share a tile, each a part of K
   int kblocks, stages;
-  int bf16, fast_bias;
-  int wide;  // 16-byte accesses of the output's and the residual's rows
+  int bf16;
+  int wide;  // whole chunks of 32 columns, 16-byte accesses of the output and residual
 };
 
 struct Ctl {
   uint64_t full[kMaxStages], empty[kMaxStages];
   uint64_t tfull[2], tempty[2];
-  uint64_t teardown, parts;
+  uint64_t teardown, parts, idle;
   uint32_t tmem;
   int abort;
 };
@@ -87,77 +87,74 @@ __device__ __forceinline__ void load_pair(uint32_t dst, const CUtensorMap *m, in
 }
 
 // ---- epilogue ---------------------------------------------------------------
-// Values of 32 consecutive elements, zero beyond n of them.
-__device__ __forceinline__ void load_row32(const void *p, int64_t at, int n, int dtype, bool fast,
-                                           float *v) {
-  if (fast && n >= 32) {
-    if (dtype == SV_FP32) {
-      const float4 *q = reinterpret_cast<const float4 *>(static_cast<const float *>(p) + at);
+// 32 consecutive elements of a row that is 16-byte aligned.
+__device__ __forceinline__ void load_row32(const void *p, int64_t at, int dtype, float *v) {
+  if (dtype == SV_FP32) {
+    const float4 *q = reinterpret_cast<const float4 *>(static_cast<const float *>(p) + at);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float4 f = q[i];
-        v[4 * i] = f.x, v[4 * i + 1] = f.y, v[4 * i + 2] = f.z, v[4 * i + 3] = f.w;
-      }
-    } else {
-      const uint4 *q = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p) + at);
+    for (int i = 0; i < 8; ++i) {
+      const float4 f = q[i];
+      v[4 * i] = f.x, v[4 * i + 1] = f.y, v[4 * i + 2] = f.z, v[4 * i + 3] = f.w;
+    }
+  } else {
+    const uint4 *q = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p) + at);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint4 u = q[i];
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    for (int i = 0; i < 4; ++i) {
+      const uint4 u = q[i];
+      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          float2 f;
-          if (dtype == SV_BF16)
-            f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w[j]));
-          else
-            f = __half22float2(*reinterpret_cast<const __half2 *>(&w[j]));
-          v[8 * i + 2 * j] = f.x;
-          v[8 * i + 2 * j + 1] = f.y;
-        }
+      for (int j = 0; j < 4; ++j) {
+        float2 f;
+        if (dtype == SV_BF16)
+          f = make_float2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xFFFF0000u));
+        else
+          f = __half22float2(*reinterpret_cast<const __half2 *>(&w[j]));
+        v[8 * i + 2 * j] = f.x;
+        v[8 * i + 2 * j + 1] = f.y;
       }
     }
-    return;
   }
-#pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = i < n ? load_any(p, at + i, dtype) : 0.0f;
 }
-__device__ __forceinline__ void store_row32(void *p, int64_t at, int n, int dtype, bool fast,
-                                            const float *v) {
-  if (fast && n >= 32) {
-    if (dtype == SV_FP32) {
-      float4 *q = reinterpret_cast<float4 *>(static_cast<float *>(p) + at);
+__device__ __forceinline__ void store_row32(void *p, int64_t at, int dtype, const float *v) {
+  if (dtype == SV_FP32) {
+    float4 *q = reinterpret_cast<float4 *>(static_cast<float *>(p) + at);
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        q[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-    } else {
-      uint4 *q = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p) + at);
+    for (int i = 0; i < 8; ++i)
+      q[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+  } else {
+    uint4 *q = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p) + at);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint32_t w[4];
+    for (int i = 0; i < 4; ++i) {
+      uint32_t w[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float a = v[8 * i + 2 * j], b = v[8 * i + 2 * j + 1];
-          if (dtype == SV_BF16) {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-            w[j] = *reinterpret_cast<const uint32_t *>(&h);
-          } else {
-            const __half2 h = __floats2half2_rn(a, b);
-            w[j] = *reinterpret_cast<const uint32_t *>(&h);
-          }
+      for (int j = 0; j < 4; ++j) {
+        const float a = v[8 * i + 2 * j], b = v[8 * i + 2 * j + 1];
+        if (dtype == SV_BF16) {
+          const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+          w[j] = *reinterpret_cast<const uint32_t *>(&h);
+        } else {
+          const __half2 h = __floats2half2_rn(a, b);
+          w[j] = *reinterpret_cast<const uint32_t *>(&h);
         }
-        q[i] = make_uint4(w[0], w[1], w[2], w[3]);
       }
+      q[i] = make_uint4(w[0], w[1], w[2], w[3]);
     }
-    return;
   }
-#pragma unroll
-  for (int i = 0; i < 32; ++i)
-    if (i < n) store_any(p, at + i, v[i], dtype);
+}
+// Four values at a time and no inlining: unrolled over 32 the activations are tens of
+// KB of code, which a tile that is a CTA's only one waits for.
+template <int kAct>
+__device__ __noinline__ float4 activate4(float4 v) {
+  return make_float4(activate<kAct>(v.x), activate<kAct>(v.y), activate<kAct>(v.z),
+                     activate<kAct>(v.w));
 }
 template <int kAct>
 __device__ __forceinline__ void activate32(float *v) {
 #pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = activate<kAct>(v[i]);
+  for (int i = 0; i < 32; i += 4) {
+    const float4 r = activate4<kAct>(make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]));
+    v[i] = r.x, v[i + 1] = r.y, v[i + 2] = r.z, v[i + 3] = r.w;
+  }
 }
 __device__ __forceinline__ void activate32(float *v, int act) {
   switch (act) {
@@ -167,6 +164,15 @@ __device__ __forceinline__ void activate32(float *v, int act) {
     case SV_ACT_SILU: activate32<SV_ACT_SILU>(v); break;
     default: break;
   }
+}
+// The biases of 32 columns, one a lane, of which the lanes hand each other theirs.
+__device__ __forceinline__ float load_bias(const void *p, int64_t n, int in, int dtype) {
+  const int lane = threadIdx.x & 31;
+  return p && lane < in ? load_any(p, n + lane, dtype) : 0.0f;
+}
+__device__ __forceinline__ void add_bias(float (&y)[32], float b) {
+#pragma unroll
+  for (int i = 0; i < 32; ++i) y[i] += __shfl_sync(0xffffffffu, b, i);
 }
 
 // Tiles in the order of the pairs: bands of `group` row tiles, within a band
@@ -178,59 +184,43 @@ __device__ __forceinline__ void place(const Args &a, int tile, int &tr, int &tc)
   tc = in / rows;
 }
 
-// Where an epilogue's rows go: the tile's rows of a warp and its piece of shared
-// memory.
-struct Rows {
-  int64_t m0;       // the warp's first row
-  float *piece;     // 32 x 32, for rows that are not written in wide stores
-};
-
 // 32 columns of a row a thread, from their sums to the output: y of x w^T (or of the
-// gate's), u of the second factor.  `in` columns from n on are inside.
+// gate's), u of the second factor.  `in` columns from n on are inside; m0: the warp's
+// first row; piece: its 32 x 32 floats of shared memory.
 template <bool kGated>
-__device__ __forceinline__ void finish(const Args &args, const Rows &rows, int64_t n, int in,
-                                       float (&y)[32], const uint32_t *u) {
+__device__ __forceinline__ void finish(const Args &args, int64_t m0, float *piece, int64_t n,
+                                       int in, float (&y)[32], float (&u)[32], float b, float bu) {
   const LinearParams &p = args.p;
   const int lane = threadIdx.x & 31;
-  float b[32];
-  if (p.bias) {
-    load_row32(p.bias, n, in, p.dtype, args.fast_bias, b);
-#pragma unroll
-    for (int i = 0; i < 32; ++i) y[i] += b[i];
-  }
+  if (p.bias) add_bias(y, b);
   activate32(y, p.act);
   if constexpr (kGated) {
-    if (p.bias_u) {
-      load_row32(p.bias_u, n, in, p.dtype, args.fast_bias, b);
+    if (p.bias_u) add_bias(u, bu);
 #pragma unroll
-      for (int i = 0; i < 32; ++i) y[i] *= __uint_as_float(u[i]) + b[i];
-    } else {
-#pragma unroll
-      for (int i = 0; i < 32; ++i) y[i] *= __uint_as_float(u[i]);
-    }
+    for (int i = 0; i < 32; ++i) y[i] *= u[i];
   }
   if (args.wide) {
-    const int64_t m = rows.m0 + lane;
+    const int64_t m = m0 + lane;
     if (m < p.M) {
       if (p.res) {
-        load_row32(p.res, m * p.rs + n, in, p.out_dtype, true, b);
+        load_row32(p.res, m * p.rs + n, p.out_dtype, u);
 #pragma unroll
-        for (int i = 0; i < 32; ++i) y[i] += b[i];
+        for (int i = 0; i < 32; ++i) y[i] += u[i];
       }
-      store_row32(p.out, m * p.os + n, in, p.out_dtype, true, y);
+      store_row32(p.out, m * p.os + n, p.out_dtype, y);
     }
   } else {
     // through shared memory, a row at a time with a lane for each column (rows of an
-    // odd stride by single elements of 32 rows at once: 57 us of 205 x 8190 x 8192
-    // against 40)
+    // odd stride by single elements of 32 rows at once: 54 us of 205 x 8190 x 8192
+    // without an activation against 38)
 #pragma unroll
-    for (int i = 0; i < 32; ++i) rows.piece[lane * 32 + (i ^ lane)] = y[i];
+    for (int i = 0; i < 32; ++i) piece[lane * 32 + (i ^ lane)] = y[i];
     __syncwarp();
-    const int live = static_cast<int>(min(static_cast<int64_t>(32), p.M - rows.m0));
-#pragma unroll 8
+    const int live = static_cast<int>(min(static_cast<int64_t>(32), p.M - m0));
+#pragma unroll 4
     for (int r = 0; r < live; ++r) {
-      float v = rows.piece[r * 32 + (lane ^ r)];
-      const int64_t m = rows.m0 + r;
+      float v = piece[r * 32 + (lane ^ r)];
+      const int64_t m = m0 + r;
       if (lane < in) {
         if (p.res) v += load_any(p.res, m * p.rs + n + lane, p.out_dtype);
         store_any(p.out, m * p.os + n + lane, v, p.out_dtype);
@@ -268,6 +258,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(smem_u32(&ctl->teardown), 1);
     mbar_init(smem_u32(&ctl->parts), 1);
+    mbar_init(smem_u32(&ctl->idle), kEpiWarps * (args.split > 1 ? args.split - 1 : 1));
     ctl->abort = 0;
     mbar_fence_init();
   }
@@ -293,39 +284,95 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int kb1 = static_cast<int>(static_cast<int64_t>(args.kblocks) * (part + 1) / args.split);
   // an epilogue warp's lanes of tensor memory and rows of the tile
   const uint32_t tacc = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-  Rows rows;
-  rows.piece = reinterpret_cast<float *>(smem + (kMaxStages - 1) * kStage) + (warp & 7) * 1024;
-  auto inside = [&](int64_t n, int c) {  // columns of the output from n on, tile column c
-    return static_cast<int>(min(p.N - n, static_cast<int64_t>(min(32, cols - c))));
-  };
+  float *piece = reinterpret_cast<float *>(smem + (kMaxStages - 1) * kStage) + (warp & 7) * 1024;
   bool ok = true;
 
   if (warp < kEpiWarps) {
     // ---------------- epilogue ----------------
     const uint32_t tempty0 = lin_remote(smem_u32(&ctl->tempty[0]), crank & ~1);
+    const int row = (warp & 3) * 32 + lane;
+    // Pair q of the cluster finishes the tile's columns [q own, (q + 1) own).
+    const int own = cols / args.split;
+    const int width = kGated ? 2 * own : own;  // columns of a part
+    const float4 *in_parts = reinterpret_cast<const float4 *>(smem);
     uint32_t it = 0;
     for (int tile = first; tile < tiles && ok; tile += step, ++it) {
       int tr, tc;
       place(args, tile, tr, tc);
       const uint32_t slot = it & 1;
       if (!(ok = lin_wait(smem_u32(&ctl->tfull[slot]), it >> 1 & 1, ab))) break;
-      if (args.split > 1) break;  // goes on below
       tc_fence_after();
-      rows.m0 = static_cast<int64_t>(tr) * 256 + rank * kLanes + (warp & 3) * 32;
-      for (int c = (warp >> 2) * 32; c < cols; c += 64) {
-        const int64_t n = static_cast<int64_t>(tc) * cols + c;
-        const int in = inside(n, c);
-        if (in <= 0) break;
-        uint32_t x[32], u[kGated ? 32 : 1];
-        tmem_ld32(tacc + slot * 256 + c, x);
-        if (kGated) tmem_ld32(tacc + slot * 256 + half + c, u);
-        tmem_ld_wait();
-        tmem_reg_fence32(x);
-        if (kGated) tmem_reg_fence32(u);
-        float y[32];
+      if (args.split > 1) {
+        // The other pairs' sums of the columns that this one finishes come into its
+        // ring, which by now is idle, as [pair][column / 4][row][column % 4] (gated: of
+        // both factors).  A cluster takes one tile, so this happens once.
+        const uint32_t bar = smem_u32(&ctl->parts), idle = smem_u32(&ctl->idle);
+        if (tid == 0) mbar_arrive_expect_tx(bar, (args.split - 1) * width * kLanes * 4);
+        for (int d = 1; d < args.split; ++d)
+          if (lane == 0)
+            lin_arrive_remote(lin_remote(idle, 2 * ((part + d) % args.split) + rank));
+        __syncwarp();
+        if (!(ok = lin_wait<true>(idle, 0, ab))) break;
+        for (int d = 1; d < args.split; ++d) {
+          const int q = (part + d) % args.split;
+          const int at = part < q ? part : part - 1;  // this pair's place among q's parts
+          const uint32_t to = lin_remote(base + (at * width * kLanes + row * 4) * 4, 2 * q + rank);
+          const uint32_t to_bar = lin_remote(bar, 2 * q + rank);
+          for (int v = (warp >> 2) * 32; v < width; v += 64) {
+            const int c = v < own ? q * own + v : half + q * own + v - own;
+            uint32_t x[32];
+            tmem_ld32(tacc + c, x);
+            tmem_ld_wait();
+            tmem_reg_fence32(x);
 #pragma unroll
-        for (int i = 0; i < 32; ++i) y[i] = __uint_as_float(x[i]);
-        finish<kGated>(args, rows, n, in, y, u);
+            for (int e = 0; e < 32; e += 4)
+              lin_store_remote(to + (v + e) * kLanes * 4, x + e, to_bar);
+          }
+        }
+        __syncwarp();
+        if (!(ok = lin_wait<true>(bar, 0, ab))) break;
+      }
+      const int64_t m0 = static_cast<int64_t>(tr) * 256 + rank * kLanes + (warp & 3) * 32;
+      for (int v = (warp >> 2) * 32; v < own; v += 64) {
+        const int c = part * own + v;  // column of the tile
+        const int64_t n = static_cast<int64_t>(tc) * cols + c;
+        const int in = static_cast<int>(min(p.N - n, static_cast<int64_t>(min(32, cols - c))));
+        if (in <= 0) break;
+        const float b = load_bias(p.bias, n, in, p.dtype);
+        const float bu = kGated ? load_bias(p.bias_u, n, in, p.dtype) : 0.0f;
+        uint32_t x[2][32];
+        tmem_ld32(tacc + slot * 256 + c, x[0]);
+        if (kGated) tmem_ld32(tacc + slot * 256 + half + c, x[1]);
+        tmem_ld_wait();
+        float y[2][32];
+#pragma unroll
+        for (int g = 0; g < (kGated ? 2 : 1); ++g) {
+          tmem_reg_fence32(x[g]);
+          if (args.split == 1) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) y[g][e] = __uint_as_float(x[g][e]);
+          } else {
+            // the sums in the order of K
+#pragma unroll
+            for (int e = 0; e < 32; ++e) y[g][e] = 0.0f;
+            for (int q = 0; q < args.split; ++q) {
+              if (q == part) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) y[g][e] += __uint_as_float(x[g][e]);
+              } else {
+                const float4 *f =
+                    in_parts + ((q < part ? q : q - 1) * width + g * own + v) / 4 * kLanes + row;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                  const float4 a = f[e * kLanes];
+                  y[g][4 * e] += a.x, y[g][4 * e + 1] += a.y;
+                  y[g][4 * e + 2] += a.z, y[g][4 * e + 3] += a.w;
+                }
+              }
+            }
+          }
+        }
+        finish<kGated>(args, m0, piece, n, in, y[0], y[1], b, bu);
       }
       tc_fence_before();
       __syncwarp();
@@ -392,77 +439,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (elect_one()) commit_pair(smem_u32(&ctl->teardown), mask);
     __syncwarp();
-  }
-
-  if (args.split > 1) {
-    // ---------------- the parts of K meet ----------------
-    // Pair q of the cluster finishes the tile's columns [q own, (q + 1) own): the
-    // other pairs' sums of these come into its ring, which by now is idle, as
-    // [pair][column / 4][row][column % 4] (gated: of both factors).
-    lin_cluster_sync();
-    if (warp < kEpiWarps && ok) {
-      const int own = cols / args.split;
-      const int width = kGated ? 2 * own : own;  // columns of a part
-      const uint32_t bar = smem_u32(&ctl->parts);
-      if (tid == 0) mbar_arrive_expect_tx(bar, (args.split - 1) * width * kLanes * 4);
-      int tr, tc;
-      place(args, first, tr, tc);
-      tc_fence_after();
-      const int row = (warp & 3) * 32 + lane;
-      for (int d = 1; d < args.split; ++d) {
-        const int q = (part + d) % args.split;
-        // this pair's place among the parts of q
-        const int at = part < q ? part : part - 1;
-        const uint32_t to = lin_remote(base + (at * width * kLanes + row * 4) * 4, 2 * q + rank);
-        const uint32_t to_bar = lin_remote(bar, 2 * q + rank);
-        for (int v = (warp >> 2) * 32; v < width; v += 64) {
-          const int c = v < own ? q * own + v : half + q * own + v - own;
-          uint32_t x[32];
-          tmem_ld32(tacc + c, x);
-          tmem_ld_wait();
-          tmem_reg_fence32(x);
-#pragma unroll
-          for (int e = 0; e < 32; e += 4)
-            lin_store_remote(to + (v + e) * kLanes * 4, x + e, to_bar);
-        }
-      }
-      __syncwarp();
-      ok = lin_wait<true>(bar, 0, ab);
-      rows.m0 = static_cast<int64_t>(tr) * 256 + rank * kLanes + (warp & 3) * 32;
-      const float4 *in_parts = reinterpret_cast<const float4 *>(smem);
-      for (int v = (warp >> 2) * 32; v < own && ok; v += 64) {
-        const int64_t n = static_cast<int64_t>(tc) * cols + part * own + v;
-        const int in = inside(n, part * own + v);
-        if (in <= 0) break;
-        // the sums in the order of K
-        auto total = [&](int c, int at, float (&y)[32]) {
-          uint32_t x[32];
-          tmem_ld32(tacc + c, x);
-          tmem_ld_wait();
-          tmem_reg_fence32(x);
-#pragma unroll
-          for (int e = 0; e < 32; ++e) y[e] = 0.0f;
-          for (int q = 0; q < args.split; ++q) {
-            if (q == part) {
-#pragma unroll
-              for (int e = 0; e < 32; ++e) y[e] += __uint_as_float(x[e]);
-            } else {
-              const float4 *f =
-                  in_parts + ((q < part ? q : q - 1) * width + at) / 4 * kLanes + row;
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const float4 a = f[e * kLanes];
-                y[4 * e] += a.x, y[4 * e + 1] += a.y, y[4 * e + 2] += a.z, y[4 * e + 3] += a.w;
-              }
-            }
-          }
-        };
-        float y[32], u[32];
-        total(part * own + v, v, y);
-        if (kGated) total(half + part * own + v, own + v, u);
-        finish<kGated>(args, rows, n, in, y, reinterpret_cast<const uint32_t *>(u));
-      }
-    }
   }
 
   // ---------------- teardown ----------------
@@ -532,9 +508,8 @@ int launch(const spec_target &h, const LinearParams &P, cudaStream_t stream) {
   auto wide = [](const void *p, int64_t stride_bytes, int64_t rows) {
     return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && (rows <= 1 || stride_bytes % 16 == 0);
   };
-  args.wide = wide(P.out, P.os * es, P.M) && wide(P.res, P.rs * es, P.M);
+  args.wide = P.N % 32 == 0 && wide(P.out, P.os * es, P.M) && wide(P.res, P.rs * es, P.M);
   args.stages = args.wide || args.split > 1 ? kMaxStages : kMaxStages - 1;
-  args.fast_bias = wide(P.bias, 0, 1) && wide(P.bias_u, 0, 1);
   CUtensorMap x, w, u;
   if (!lin_encode(&x, P.x, P.xs, P.K, P.M, kLanes) ||
       !lin_encode(&w, P.w, P.ws, P.K, P.N, args.bn / 2) ||
