@@ -57,7 +57,7 @@ struct Shared {
     uint64_t cand[kCap + SV_MAX_TOP];
   };
   float red[3][kMaxCluster];
-  uint32_t bound[2][kWarps];
+  uint32_t bound[kWarps];
   int count, few_count;
 };
 
@@ -145,7 +145,6 @@ struct Best {
   int top, warps;
   int found = 0, cur = 0;   // the list's keys and its buffer
   uint32_t lim = kLowest;   // ordered values from here are candidates
-  int turn = 0;             // of the bounds' two buffers
 
   // Ranks the n candidates with the list.
   __device__ __forceinline__ void rank(int n, Sh &sh) {
@@ -162,20 +161,24 @@ struct Best {
   }
   // Each of the warps that have a load for every lane (or the first alone) has
   // ceil(top / warps) elements, of different threads, from a bound on, so what lies
-  // under it is no alternative; the bound is the least of the warps' own.  One
-  // barrier; `most` is the thread's largest element so far.
-  __device__ __forceinline__ void raise(float most, Sh &sh) {
+  // under it is no alternative; the bound is the least of the warps' own.  `most` is
+  // the thread's largest element so far.  A warp's bound only rises, so a read without
+  // a barrier is of a bound too, maybe a lower one.
+  __device__ __forceinline__ void publish(float most, Sh &sh) const {
     uint32_t u = ordered(most), bound = 0;
     for (int r = (top + warps - 1) / warps; r > 0; --r) {
       bound = __reduce_max_sync(0xffffffffu, u);
       const uint32_t who = __ballot_sync(0xffffffffu, u == bound);
       if ((threadIdx.x & 31) == __ffs(who) - 1) u = 0;
     }
-    turn ^= 1;
-    if ((threadIdx.x & 31) == 0) sh.bound[turn][threadIdx.x >> 5] = bound;
-    __syncthreads();
-    bound = sh.bound[turn][0];
-    for (int w = 1; w < warps; ++w) bound = min(bound, sh.bound[turn][w]);
+    if ((threadIdx.x & 31) == 0)
+      *const_cast<volatile uint32_t *>(&sh.bound[threadIdx.x >> 5]) = bound;
+    __syncwarp();
+  }
+  __device__ __forceinline__ void raise(const Sh &sh) {
+    const volatile uint32_t *bounds = sh.bound;
+    uint32_t bound = bounds[0];
+    for (int w = 1; w < warps; ++w) bound = min(bound, bounds[w]);
     lim = max(lim, bound);
   }
 };
@@ -198,7 +201,10 @@ __device__ __noinline__ Best<kWarps> best_of_each(const Span<T, kWarps> s, int e
     float most = tile.at(0);
 #pragma unroll
     for (int i = 1; i < S::kPer; ++i) most = max_nan(most, tile.at(i));
-    best.raise(most, sh);
+    best.publish(most, sh);
+    __syncthreads();
+    best.raise(sh);
+    __syncthreads();
     // Elements that `want` takes: how many there are, and writing them.
     auto count = [&](auto &&want) {
       int c = 0;
@@ -294,10 +300,11 @@ __global__ void __launch_bounds__(32 * kWarps, kResident / kWarps)
   uint32_t rank, parts;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
   asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(parts));
-  const int64_t row = blockIdx.x / parts;
-  const T *x = static_cast<const T *>(P.logits) + row * P.stride;
   const int V = static_cast<int>(P.V), top = P.top;
   const float c2 = 1.4426950408889634f / P.temperature;  // to powers of two
+  const float inv_t = 1.0f / P.temperature;
+  const int64_t row = blockIdx.x / parts;
+  const T *x = static_cast<const T *>(P.logits) + row * P.stride;
   S s;
   s.id0 = static_cast<int>((0 - reinterpret_cast<uintptr_t>(x)) % kBytes / sizeof(T));
   s.id0 = min(s.id0, V);
@@ -324,11 +331,20 @@ __global__ void __launch_bounds__(32 * kWarps, kResident / kWarps)
     sum = m > -INFINITY ? 1.0f : 0.0f;
     sh.few[tid] = order_key(m, id);
   }
+  // the logit of a given token: NaN outside the vocabulary
+  auto given = [&](int i) {
+    const int id = P.tokens[row * P.n + i];
+    if (id >= 0 && id < V) return to_float(x[id]);
+    if (id == -1) return 0.0f;  // none
+    set_status(status, SV_ERR_TOKEN);
+    return NAN;
+  };
+  const float early = rank == 0 && tid < P.n ? given(tid) : 0.0f;
   Best<kWarps> best;
   best.top = top;
   best.warps = max(1, min(kWarps, (s.end - s.begin) / 32));
-  // Loads with candidates are kept without a barrier between the tiles of a group,
-  // under a bound found at its start; the groups grow as candidates get rarer.
+  // Loads with candidates are kept without a barrier between the tiles, under a bound
+  // that rises from time to time.
   int next_start = 0, number = 0;
   for (int v0 = s.begin; v0 < s.end; v0 += S::kTile, ++number) {
     tile = next;
@@ -364,8 +380,10 @@ __global__ void __launch_bounds__(32 * kWarps, kResident / kWarps)
     }
     if (top) {
       if (number == next_start) {
-        best.raise(m, sh);
-        next_start = number == 0 ? 2 : number < 32 ? 4 * number : number + 32;
+        best.publish(m, sh);
+        if (number == 0) __syncthreads();
+        best.raise(sh);
+        next_start = number == 0 ? 1 : number < 32 ? 2 * number : number + 32;
       }
       const float lim = from_ordered(best.lim);
       if (!(most < lim)) {
@@ -382,7 +400,9 @@ __global__ void __launch_bounds__(32 * kWarps, kResident / kWarps)
     }
   }
   if (top) {
-    best.raise(m, sh);
+    best.publish(m, sh);
+    __syncthreads();
+    best.raise(sh);
     const int n = sh.count;
     const float lim = from_ordered(best.lim);
     if (n <= kStage) {
@@ -468,26 +488,21 @@ __global__ void __launch_bounds__(32 * kWarps, kResident / kWarps)
     }
     cluster_sync();  // nobody reads a CTA that is gone
   }
-  if (rank != 0) return;
-  const bool fine = isfinite(mb);
-  const float log_s = fine ? logf(sum) : NAN, inv_t = 1.0f / P.temperature;
-  if (tid == 0 && P.entropy) P.entropy[row] = log_s - 0.69314718055994531f * (t / sum);
-  for (int i = tid; i < P.n; i += kThreads) {
-    const int id = P.tokens[row * P.n + i];
-    float y = 0.0f;
-    if (id >= 0 && id < V) {
-      y = (to_float(x[id]) - mb) * inv_t - log_s;
-    } else if (id != -1) {
-      y = NAN;
-      set_status(status, SV_ERR_TOKEN);
+  if (rank == 0) {
+    const bool fine = isfinite(mb);
+    const float log_s = fine ? logf(sum) : NAN;
+    if (tid == 0 && P.entropy) P.entropy[row] = log_s - 0.69314718055994531f * (t / sum);
+    for (int i = tid; i < P.n; i += kThreads) {
+      const float y = i == tid ? early : given(i);
+      const bool none = P.tokens[row * P.n + i] == -1;
+      P.log_probs[row * P.n + i] = none ? 0.0f : (y - mb) * inv_t - log_s;
     }
-    P.log_probs[row * P.n + i] = y;
-  }
-  for (int i = tid; i < top; i += kThreads) {
-    const uint64_t k = keys[i];
-    P.top_ids[row * top + i] = fine ? static_cast<int>(~static_cast<uint32_t>(k)) : -1;
-    P.top_log_probs[row * top + i] =
-        fine ? (from_ordered(static_cast<uint32_t>(k >> 32)) - mb) * inv_t - log_s : NAN;
+    for (int i = tid; i < top; i += kThreads) {
+      const uint64_t k = keys[i];
+      P.top_ids[row * top + i] = fine ? static_cast<int>(~static_cast<uint32_t>(k)) : -1;
+      P.top_log_probs[row * top + i] =
+          fine ? (from_ordered(static_cast<uint32_t>(k >> 32)) - mb) * inv_t - log_s : NAN;
+    }
   }
 }
 
