@@ -182,6 +182,29 @@ int spec_verify_status(spec_verify_t *h);
 /* Replaces the stream that later calls are enqueued on. */
 int spec_verify_set_stream(spec_verify_t *h, void *stream);
 
+/* What a service says of a round's answers: log probabilities under
+ * softmax(logits / temperature) of one token for each row of the last run's
+ * logits, the rows' entropies in nats and their most likely tokens, without
+ * reading the weight again.  Row b*(K+1)+i is the target's distribution after
+ * the first i drafted tokens of sequence b (of a tree: row 0 the root's, row
+ * 1+j node j's), so out_tokens of spec_verify_run is the argument that scores
+ * what was emitted: its -1 get 0.
+ *   tokens     device, int32 [B, K+1] or NULL; -1: none; another one outside
+ *              [0, V) gets NaN and sets SV_ERR_TOKEN
+ *   log_probs  device, fp32 [B, K+1] (with tokens)
+ *   entropy    device, fp32 [B, K+1] or NULL
+ *   top_ids    device, int32 [B, K+1, top], of equal logits the smaller id
+ *              first; top from 0 to 64 and V
+ *   top_log_probs  device, fp32 [B, K+1, top]
+ * The temperature is the caller's (a greedy round is scored at any), the cuts
+ * of a truncated run are not applied.  Enqueued on the handle's stream; rows
+ * without a finite largest logit get NaN and ids of -1.  Errors: SV_ERR_ARG
+ * (null handle or pointers, no run yet, a temperature that is not above 0 or
+ * not finite), SV_ERR_SHAPE (top), SV_ERR_ALIGN, SV_ERR_CUDA. */
+int spec_verify_log_probs(spec_verify_t *h, const int32_t *tokens, float temperature,
+                          int32_t top, float *log_probs, float *entropy, int32_t *top_ids,
+                          float *top_log_probs);
+
 /* Copies the last run's fp32 logits [B*(K+1), V] (row b*(K+1)+i) to dst
  * (host or device, B*(K+1)*V floats).  Synchronises.  For tests. */
 int spec_verify_debug_logits(spec_verify_t *h, float *dst);

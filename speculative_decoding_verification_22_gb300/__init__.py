@@ -45,6 +45,7 @@ EXPORTS = ("spec_verify_create", "spec_verify_run", "spec_verify_run_host",
            "spec_verify_run_noalloc", "spec_ngram_draft", "spec_verify_run_truncated",
            "spec_verify_tree_greedy", "spec_verify_run_fp8", "spec_verify_plan",
            "spec_verify_debug_stall", "spec_verify_submit_host", "spec_verify_wait_host",
+           "spec_verify_log_probs",
            "spec_target_create", "spec_target_destroy", "spec_target_status",
            "spec_target_set_wait_limit", "spec_target_rms_norm", "spec_target_rms_norm_fp8",
            "spec_target_matmul_fp8", "spec_target_rope_freqs", "spec_target_rope_append",
@@ -97,6 +98,7 @@ def load_library():
         lib.spec_verify_submit_host.argtypes = [vp, ctypes.c_int, vp, vp, vp, vp, vp, f32, vp,
                                                 vp]
         lib.spec_verify_wait_host.argtypes = [vp, ctypes.c_int]
+        lib.spec_verify_log_probs.argtypes = [vp, vp, f32, ctypes.c_int32, vp, vp, vp, vp]
         lib.spec_verify_timing.argtypes = [vp, ctypes.c_int]
         lib.spec_verify_timing_read.argtypes = [vp, ctypes.POINTER(ctypes.c_double),
                                                 ctypes.POINTER(i64)]
@@ -235,6 +237,14 @@ def spec_verify_set_stream(h, stream=None) -> None:
 def spec_verify_debug_logits(h, dst) -> None:
     _check(load_library().spec_verify_debug_logits(h, _ptr(dst)),
            "spec_verify_debug_logits")
+
+
+def spec_verify_log_probs(h, tokens, temperature: float, top: int, log_probs, entropy,
+                          top_ids, top_log_probs) -> None:
+    """Log probabilities, entropies and most likely tokens from the last run's logits."""
+    _check(load_library().spec_verify_log_probs(
+        h, _ptr(tokens), float(temperature), int(top), _ptr(log_probs), _ptr(entropy),
+        _ptr(top_ids), _ptr(top_log_probs)), "spec_verify_log_probs")
 
 
 def spec_verify_debug_lse(h, dst) -> None:
@@ -393,6 +403,27 @@ class SpecVerify:
         spec_verify_tree_greedy(self.h, hidden, W_lm, tree_tokens, tree_parents, out_t,
                                 out_nodes, out_n)
         return out_t, out_nodes[:, :self.K], out_n
+
+    def log_probs(self, tokens=None, top=0, temperature=1.0):
+        """What the last run's logits say of its answers: log probabilities
+        [B, K+1] of ``tokens`` (int32 [B, K+1], as ``run`` returns them; -1 gets 0),
+        the rows' entropies [B, K+1], and with ``top`` > 0 the most likely ids int32
+        [B, K+1, top] and their log probabilities."""
+        shape = (self.B, self.K + 1)
+        if tokens is not None and (tuple(tokens.shape) != shape or tokens.dtype != torch.int32
+                                   or tokens.device.type != "cuda"):
+            raise ValueError(f"log_probs: tokens must be int32 {shape} on the GPU")
+        if not 0 <= top <= min(64, self.V):
+            raise ValueError("log_probs: top must be from 0 to 64 and at most V")
+
+        def made(*more, dtype=torch.float32):
+            return torch.empty(shape + more, dtype=dtype, device=self.device)
+        out = [made() if tokens is not None else None, made()]
+        if top:
+            out += [made(top, dtype=torch.int32), made(top)]
+        spec_verify_log_probs(self.h, tokens, temperature, top, out[0], out[1],
+                              *(out[2:] or (None, None)))
+        return out
 
     def status(self) -> int:
         return spec_verify_status(self.h)

@@ -11,6 +11,7 @@
 
 #include "sv_internal.cuh"
 #include "sv_kernels.h"
+#include "sv_target.cuh"
 
 namespace {
 
@@ -757,6 +758,29 @@ int spec_verify_wait_host(spec_verify_t *h, int slot) {
   if (cudaEventSynchronize(sl.done) != cudaSuccess) return SV_ERR_CUDA;
   // a device-side error: read and clear the status word (synchronises)
   return *sl.status_host == 0 ? SV_OK : spec_verify_status(h);
+}
+
+int spec_verify_log_probs(spec_verify_t *h, const int32_t *tokens, float temperature,
+                          int32_t top, float *log_probs, float *entropy, int32_t *top_ids,
+                          float *top_log_probs) {
+  if (!h || h->epoch == 0) return SV_ERR_ARG;
+  sv_log_probs_t a{};
+  a.logits = h->w.logits;
+  a.tokens = tokens;
+  a.log_probs = log_probs;
+  a.entropy = entropy;
+  a.top_ids = top_ids;
+  a.top_log_probs = top_log_probs;
+  a.stride = a.V = h->dims.V;
+  a.rows = h->dims.R;
+  a.dtype = SV_FP32;
+  a.n = tokens ? 1 : 0;
+  a.top = top;
+  a.temperature = temperature;
+  const int c = sv::log_probs_checks(a);
+  if (c != SV_OK) return c;
+  return sv::launch_log_probs(a, h->num_sms, h->w.status, h->stream) == cudaSuccess ? SV_OK
+                                                                                   : SV_ERR_CUDA;
 }
 
 int spec_verify_debug_logits(spec_verify_t *h, float *dst) {

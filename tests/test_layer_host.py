@@ -135,3 +135,16 @@ def test_the_binding_refuses_wrong_tensors():
                 lambda: ops.log_probs(x), lambda: ops.block_norm(x, x, w[0])):
         with pytest.raises(ValueError, match="on the GPU"):
             far()
+
+
+def test_verify_log_probs_refusals(lib):
+    f = lib.spec_verify_log_probs
+    assert f(None, GOOD, 1.0, 0, GOOD, GOOD, None, None) == sv.SV_ERR_ARG
+    eng = sv.SpecVerify.__new__(sv.SpecVerify)  # no GPU, no handle
+    eng.B, eng.K, eng.V, eng.h = 2, 3, 40, None
+    for kw in (dict(tokens=torch.zeros(2, 3, dtype=torch.int32)),
+               dict(tokens=torch.zeros(2, 4, dtype=torch.int64)),
+               dict(tokens=torch.zeros(2, 4, dtype=torch.int32)),  # not on the GPU
+               dict(top=65), dict(top=41), dict(top=-1)):
+        with pytest.raises(ValueError):
+            eng.log_probs(**kw)
