@@ -292,16 +292,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, 2 * kCols);
   }
-  if (args.split > 1) {
-    // Parts can be on their way only after a role gave up: they are given a
-    // millisecond, a thousand times what they take.
-    if (*const_cast<volatile int *>(&ctl->abort)) {
-      const uint64_t t0 = globaltimer();
-      while (globaltimer() - t0 < 1000000) {
-      }
-    }
-    lin_cluster_sync();  // nobody writes to a CTA that is gone
-  }
+  if (args.split > 1) lin_leave(&ctl->abort, args.split);
 }
 
 template <int kCols, bool kGated>

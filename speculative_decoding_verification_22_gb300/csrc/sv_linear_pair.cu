@@ -442,24 +442,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 
   // ---------------- teardown ----------------
-  // The products are done (their commit arrives in both CTAs); a copy can be in
-  // flight only after a role gave up, and then on a barrier of another CTA: it is
-  // given a millisecond, a thousand times what it takes.
   if (warp == kLoadWarp) {
     const int never = 0;
-    if (lane == 0) {
-      mbar_wait(smem_u32(&ctl->teardown), 0u, kLinCleanupNs, &never);
-      if (*const_cast<volatile int *>(&ctl->abort)) {
-        const uint64_t t0 = globaltimer();
-        while (globaltimer() - t0 < 1000000) {
-        }
-      }
-    }
+    // the products are done: their commit arrives in both CTAs
+    if (lane == 0) mbar_wait(smem_u32(&ctl->teardown), 0u, kLinCleanupNs, &never);
     __syncwarp();
   }
   tc_fence_before();
   __syncthreads();
-  lin_cluster_sync();
+  lin_leave(&ctl->abort, 2 * args.split);
   if (warp == kMmaWarp) {
     tc_fence_after();
     dealloc_pair(tmem, 512);

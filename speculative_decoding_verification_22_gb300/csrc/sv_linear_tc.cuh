@@ -96,6 +96,25 @@ __device__ __forceinline__ void lin_prefetch(const CUtensorMap *m, int32_t c0, i
                : "memory");
 }
 
+// The end of a cluster of `ctas`, for all threads, after a __syncthreads: nobody goes
+// while another may still write to it or complete a copy on its barriers.  Without a
+// timeout everything on its way has been waited for; after one (in whichever CTA) what
+// may still be on its way is given a millisecond, a thousand times what it takes.
+__device__ __forceinline__ void lin_leave(int *abort, uint32_t ctas) {
+  volatile int *gave_up = abort;
+  if (threadIdx.x < ctas && *gave_up)
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(lin_remote(smem_u32(abort), threadIdx.x)),
+                 "r"(1)
+                 : "memory");
+  lin_cluster_sync();
+  if (*gave_up) {
+    const uint64_t t0 = globaltimer();
+    while (globaltimer() - t0 < 1000000) {
+    }
+    lin_cluster_sync();
+  }
+}
+
 inline PFN_cuTensorMapEncodeTiled_v12000 lin_encode_fn() {
   static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
     void *p = nullptr;

@@ -474,6 +474,29 @@ def test_the_block_of_a_layer(ops, M):
     assert ops.status() == sv.SV_OK
 
 
+@pytest.mark.parametrize("M,N,K", [(5, 1024, 4096), (40, 300, 2048), (120, 2048, 512),
+                                   (200, 512, 4096), (300, 3000, 1024), (700, 1030, 512)])
+def test_a_wait_limit_of_nothing(M, N, K):
+    """With a limit of nothing a wait that is not soon satisfied gives up: the call
+    ends, either with its result or with a status that says so, and the next call is
+    right."""
+    ops = sv.TargetOps()
+    g = gen(M)
+    x, w = randn(g, (M, K), torch.bfloat16), randn(g, (N, K), torch.bfloat16)
+    for call in (lambda: ops.linear(x, w), lambda: ops.gated_linear(x, w, w)):
+        want = call()
+        assert ops.status() == sv.SV_OK
+        ops.set_wait_limit(0)
+        for _ in range(10):
+            got = call()
+            code = ops.status()
+            assert code == sv.SV_ERR_TIMEOUT or (code == sv.SV_OK and torch.equal(got, want))
+        ops.set_wait_limit(10 ** 9)
+        assert torch.equal(call(), want)
+        assert ops.status() == sv.SV_OK
+    ops.close()
+
+
 def test_refused_before_anything_is_launched(ops):
     x, w = torch.ones(4, 64, device="cuda").bfloat16(), torch.ones(8, 64, device="cuda").bfloat16()
     r = torch.ones(4, 8, device="cuda").bfloat16()
