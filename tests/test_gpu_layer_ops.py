@@ -142,6 +142,37 @@ def test_products_of_other_layouts(ops, M, kind):
     assert ops.status() == sv.SV_OK
 
 
+@pytest.mark.parametrize("M,N,K", [(1, 1, 1), (1, 5, 3), (7, 9, 5), (3, 130, 1), (40, 33, 7),
+                                   (150, 70, 9), (260, 300, 3)])
+@pytest.mark.parametrize("aligned", [True, False])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_products_of_the_smallest_depths(ops, M, N, K, aligned, dtype):
+    """K below a 16-byte load, in rows that are aligned and in dense ones; whole
+    numbers, so exact."""
+    g = gen(M + N + K)
+    dt, width = DTYPES[dtype], 16 if aligned else K
+
+    def whole(rows):
+        t = torch.full((rows, width), math.nan, dtype=dt, device="cuda")  # nothing beside is read
+        t[:, :K] = torch.randint(-3, 4, (rows, K), generator=g, device="cuda").to(dt)
+        return t[:, :K]
+    x, w, u = whole(M), whole(N), whole(N)
+    want = x.double() @ w.double().t()
+    assert torch.equal(ops.linear(x, w, out_dtype=torch.float32).double(), want)
+    assert torch.equal(ops.gated_linear(x, w, u, activation="none", out_dtype=torch.float32)
+                       .double(), want * (x.double() @ u.double().t()))
+
+
+@pytest.mark.parametrize("M", [1, 3, 8, 9, 31, 32, 33, 100])
+@pytest.mark.parametrize("N,K", [(1, 40), (17, 1), (255, 1000), (600, 333)])
+def test_products_in_fp32(ops, M, N, K):
+    g = gen(M + N)
+    x, w = randn(g, (M, K)), randn(g, (N, K), scale=K ** -0.5)
+    u, b, r = randn(g, (N, K), scale=K ** -0.5), randn(g, (N,)), randn(g, (M, N))
+    within(ops.linear(x, w, b, "gelu_tanh", r), *linear_ref(x, w, b, "gelu_tanh", r))
+    within(ops.gated_linear(x, w, u, b, b), *gated_ref(x, w, u, b, b))
+
+
 @pytest.mark.parametrize("M", [4, 100, 260])
 def test_not_finite_inputs_stay_in_their_rows_and_columns(ops, M):
     g = gen(M)
@@ -193,6 +224,18 @@ def test_block_norm(ops, rows, d, dtype, gate):
         within(out, want, rounded(want, dout, dt))
         within(ho, h, rounded(h, dh, dt))
     assert ops.status() == sv.SV_OK
+
+
+@pytest.mark.parametrize("rows,d", [(1, 1), (6, 512), (5, 130), (200, 1024)])
+@pytest.mark.parametrize("gate", ["one row", "one"])
+def test_block_norm_gates_for_all_rows(ops, rows, d, gate):
+    g = gen(rows + d)
+    x, res, w = (randn(g, s, torch.bfloat16) for s in ((rows, d), (rows, d), (d,)))
+    gt = gate_of(g, gate, rows, d, torch.bfloat16)
+    want, h, dout, dh = block_norm_ref(x, res, w, None, gt, -1.5)
+    out, ho = ops.block_norm(x, res, w, None, gt, -1.5)
+    within(out, want, rounded(want, dout, torch.bfloat16))
+    within(ho, h, rounded(h, dh, torch.bfloat16))
 
 
 @pytest.mark.parametrize("rows,d", [(1, 128), (4, 200), (5, 4096), (33, 8192), (3, 4090), (2, 20000)])
