@@ -476,7 +476,7 @@ int launch(const spec_target &h, const LinearParams &P, cudaStream_t stream) {
     if (split > args.kblocks) break;
     for (int bn = 256; bn >= 64; bn -= 32) {
       const int cols = kGated ? bn / 2 : bn;
-      if (split > 1 && cols % (32 * split) != 0) continue;
+      if (cols % (32 * split) != 0) continue;  // the epilogue takes 32 columns at a time
       const int64_t ct = (P.N + cols - 1) / cols, tiles = row_tiles * ct;
       if (split > 1 && tiles > clusters) continue;  // a cluster takes one tile
       const int64_t block = std::max(2 * bn, (kLanes + bn / 2) * 128 / 40);

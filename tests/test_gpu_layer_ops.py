@@ -27,7 +27,8 @@ def ops():
 SIZES = [(1, 64, 64), (1, 1, 8), (5, 4096, 512), (5, 192, 4096), (8, 1000, 136), (16, 250, 1032),
          (17, 129, 72), (33, 640, 2048), (64, 257, 520), (65, 384, 256), (96, 8, 128),
          (128, 130, 192), (129, 513, 328), (200, 1024, 1000), (256, 256, 64), (257, 255, 72),
-         (300, 72, 4104), (513, 1030, 264), (1000, 520, 512), (2049, 264, 128)]
+         (300, 72, 4104), (513, 1030, 264), (1000, 520, 512), (2049, 264, 128), (800, 1408, 512),
+         (1500, 1120, 192), (260, 4000, 320)]
 
 
 @pytest.mark.parametrize("M,N,K", SIZES)
