@@ -381,7 +381,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == kLoadWarp) {
     // ---------------- TMA ----------------
+    // A weight that all its tiles read at about the same time leaves L2 first (3% of
+    // 205 to 2048 rows; more rows read it again later).
     const uint64_t policy = policy_evict_normal();
+    const uint64_t policy_w = args.row_tiles <= args.group ? policy_evict_first() : policy;
     const CUtensorMap *tmB = kGated && rank ? &tmU : &tmW;
     const uint32_t full0 = lin_remote(smem_u32(&ctl->full[0]), crank & ~1);
     int stage = 0;
@@ -399,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_arrive_expect_tx(smem_u32(&ctl->full[stage]), 2 * (kLanes + half) * 128);
           const uint32_t at = base + stage * kStage, full = full0 + stage * 8;
           load_pair(at, &tmX, kb * kLinBlk, m0, full, policy);
-          load_pair(at + kLanes * 128, tmB, kb * kLinBlk, n0, full, policy);
+          load_pair(at + kLanes * 128, tmB, kb * kLinBlk, n0, full, policy_w);
         }
         __syncwarp();
         if (++stage == args.stages) {
