@@ -6,7 +6,10 @@
 //
 // One pass: a row stays in registers from its load to the stores, through two
 // sums (and the maximum of an E4M3 row), so every input is read once and every
-// output written once; HBM bounds it for many rows, the launch for few.  A thread
+// output written once; HBM bounds it for many rows (16384 x 4096 in bf16 to bf16 89 us,
+// 6.0 TB/s; to E4M3 with a gate 93, where instructions count too: 71% of the SM's
+// issue), the launch for few (5 x 4096: 2.8 us).  Times in this file are of kernels in
+// a CUDA graph.  A thread
 // holds kVec vectors of eight elements; a row takes `wpr` whole warps, and a block
 // several short rows.  Sixteen lanes hold the 128 columns of one scale, so a
 // block's maximum is four shuffles.

@@ -9,8 +9,19 @@
 //    of tensor memory.
 //  * The pairs are persistent; a tile's epilogue (warps 0-7) runs beside the next
 //    tile's products, in the other half of tensor memory.
+//  * Fewer tiles than pairs: a cluster of two or four pairs shares a tile, each pair
+//    takes a part of K, and each finishes some of the columns: the others' sums of
+//    these come through distributed shared memory and are added in the order of K.
 //  * Warp 8: TMA of its CTA; warp 9: products, in the first CTA of the pair alone.
 //  * The columns of a tile are chosen so that the tiles fill whole waves.
+//
+// What bounds it (times of kernels in a CUDA graph): many rows the tensor cores (4096 x
+// 14336 x 4096 gated 497 us, 1.93 PFLOP/s, their pipe 97% active; 4096 x 4096 x 14336
+// 269 us, 1.79, in four waves of 224 columns; under the power cap of long runs 1.66 and
+// 1.53).  Few tiles: about 8 us of start, first load, exchange and epilogue, and x, whose
+// rows all tiles read at once: 205 x 8190 x 8192 takes 38 us (the weight's bytes 21), 43
+// if every load of x is of the same rows, 29 if the weight's are.  Other places in K for
+// each tile's start: 5 to 25% slower.
 #include <algorithm>
 
 #include "sv_linear_tc.cuh"

@@ -5,6 +5,21 @@
 //
 // With m the row's maximum and d = (x - m) / T <= 0, s = sum exp d and
 // t = sum d exp d: lse - m / T = log s and H = log s - t / s.
+//
+// One pass: a thread keeps the maximum of what it has read, s and t, and puts them on
+// a larger maximum when it meets one.  The alternatives come out of the same pass: the
+// threads' maxima give a bound under which there are none, loads that hold anything
+// from the bound on are kept in shared memory, and the few keys from the last bound on
+// are ranked at the end.  Rows whose ties or order make too many candidates are read
+// again by a form that halves its way to the exact one.  A row is read by one CTA, or,
+// where rows are few, by a cluster whose parts the first CTA joins.
+//
+// What bounds it (times of kernels in a CUDA graph): HBM in fp32 (320 x 128256 with 20
+// alternatives 37 us, 2000 x 128256 181 us, 5.7 TB/s; without alternatives 307 us for
+// 4095 x 128000, all of the copy rate), instructions in 16 bits (4095 x 128003 in bf16
+// 213 us with five alternatives, 4.9 TB/s, 73% of the SM's issue; 179 without), and
+// latencies for few rows: 5 x 128256 takes 8.8 us, 4.8 without alternatives.  A CTA that
+// goes on to the next row with its first tile on the way spills: 337 us against 226.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
