@@ -9,7 +9,7 @@
 //    parts meet in distributed shared memory, where each CTA adds some of the
 //    columns in the order of K (repeatable, no scratch, no second launch) and
 //    stores them.  The adding of a tile runs beside the next one's products.
-//  * Warps 0-3: sums and epilogue; warp 4: TMA; warp 5: products.
+//  * Warps 0-7: sums and epilogue; warp 8: TMA; warp 9: products.
 //
 // What bounds it (times of kernels in a CUDA graph): the bytes of the weight and about
 // 4 us of start, first load and exchange.  5 x 4096 x 4096 takes 10.4 us (its bytes
@@ -24,8 +24,8 @@
 namespace sv {
 namespace {
 
-constexpr int kEpiWarps = 4, kLoadWarp = 4, kMmaWarp = 5;
-constexpr int kThreads = 32 * 6;
+constexpr int kEpiWarps = 8, kLoadWarp = 8, kMmaWarp = 9;
+constexpr int kThreads = 32 * 10;
 constexpr int kLanes = 128;
 constexpr int kMaxSplit = 8;
 constexpr int kMaxStages = 12;
@@ -119,8 +119,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp < kEpiWarps) {
     // ---------------- sums and epilogue ----------------
-    const int row = tid;
-    const uint32_t tacc = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+    const int row = tid & 127;  // lane of tensor memory, which two warps read
+    const uint32_t tacc = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     uint32_t it = 0;
     bool ok = true;
     for (int tile = first; tile < args.tiles && ok; tile += step, ++it) {
@@ -137,26 +137,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int fours = mine > 0 ? (mine + 3) / 4 : 0;
       if (tid == 0) mbar_arrive_expect_tx(bar, fours * args.split * kLanes * 16);
       const uint32_t own = smem_u32(buf + rank * per * kLanes + row * 4);
-      int q = 0, left = per;
-      uint32_t at = lin_remote(own, 0), to = lin_remote(bar, 0);
 #pragma unroll
-      for (int c0 = 0; c0 < kCols; c0 += 16) {
-        if (c0 >= M) break;
+      for (int c0 = 0; c0 < kCols; c0 += 32) {
+        const int c1 = c0 + (warp >> 2) * 16;
+        if (c1 >= M || c1 >= kCols) break;
         uint32_t x[16];
-        tmem_ld16(tacc + slot * kCols + c0, x);
+        tmem_ld16(tacc + slot * kCols + c1, x);
         tmem_ld_wait();
         tmem_reg_fence(x);
 #pragma unroll
         for (int e = 0; e < 16; e += 4) {
-          if (c0 + e < M) {
-            if (left == 0) {
-              left = per;
-              at = lin_remote(own, ++q);
-              to = lin_remote(bar, q);
-            }
-            lin_store_remote(at, x + e, to);
-            at += kLanes * 16;
-            left -= 4;
+          if (c1 + e < M) {
+            const int q = (c1 + e) / per;
+            lin_store_remote(lin_remote(own, q) + (c1 + e - q * per) * kLanes * 4, x + e,
+                             lin_remote(bar, q));
           }
         }
       }
@@ -166,7 +160,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       // A thread finishes column n of the output, four rows of x at a time, one in
       // kStep; what it adds to 16 of them is loaded while their parts arrive.
-      constexpr int kStep = kLanes / kRows, kFours = 4;
+      constexpr int kStep = 32 * kEpiWarps / kRows, kFours = 4;
       const int r = row % kRows;
       const int64_t n = static_cast<int64_t>(tile) * kRows + r;
       const bool in = n < p.N;
@@ -180,10 +174,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           res[i] = v < mine ? load_any(p.res, (rank * per + v) * p.rs + n, p.out_dtype) : 0.0f;
         }
       };
-      if (p.res && in) load_res(row / kRows);
+      if (p.res && in) load_res(tid / kRows);
       if (!(ok = lin_wait<true>(bar, xphase, ab))) break;
       const float4 *in_parts = reinterpret_cast<const float4 *>(buf) + r;
-      for (int f0 = row / kRows; f0 < fours && in; f0 += kFours * kStep) {
+      for (int f0 = tid / kRows; f0 < fours && in; f0 += kFours * kStep) {
 #pragma unroll
         for (int i = 0; i < kFours; ++i) {
           const int f = f0 + i * kStep;
