@@ -57,6 +57,23 @@ __device__ __forceinline__ float activate(float v, int act) {
   }
 }
 
+// Four values at a time and no inlining: unrolled over an epilogue's values the
+// activations are tens of KB of code, which a tile that is a CTA's only one waits for.
+template <int kAct>
+__device__ __noinline__ float4 activate4_call(float4 v) {
+  return make_float4(activate<kAct>(v.x), activate<kAct>(v.y), activate<kAct>(v.z),
+                     activate<kAct>(v.w));
+}
+__device__ __forceinline__ float4 activate4(float4 v, int act) {
+  switch (act) {
+    case SV_ACT_RELU: return activate4_call<SV_ACT_RELU>(v);
+    case SV_ACT_GELU: return activate4_call<SV_ACT_GELU>(v);
+    case SV_ACT_GELU_TANH: return activate4_call<SV_ACT_GELU_TANH>(v);
+    case SV_ACT_SILU: return activate4_call<SV_ACT_SILU>(v);
+    default: return v;
+  }
+}
+
 __device__ __forceinline__ float load_any(const void *p, int64_t at, int dtype) {
   if (dtype == SV_BF16) return __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[at]);
   if (dtype == SV_FP16) return __half2float(static_cast<const __half *>(p)[at]);

@@ -137,10 +137,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int fours = mine > 0 ? (mine + 3) / 4 : 0;
       if (tid == 0) mbar_arrive_expect_tx(bar, fours * args.split * kLanes * 16);
       const uint32_t own = smem_u32(buf + rank * per * kLanes + row * 4);
-#pragma unroll
-      for (int c0 = 0; c0 < kCols; c0 += 32) {
-        const int c1 = c0 + (warp >> 2) * 16;
-        if (c1 >= M || c1 >= kCols) break;
+#pragma unroll 1
+      for (int c1 = (warp >> 2) * 16; c1 < M; c1 += 32) {
         uint32_t x[16];
         tmem_ld16(tacc + slot * kCols + c1, x);
         tmem_ld_wait();
@@ -166,13 +164,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool in = n < p.N;
       const float b = in && p.bias ? load_any(p.bias, n, p.dtype) : 0.0f;
       const float bu = kGated && in && p.bias_u ? load_any(p.bias_u, n, p.dtype) : 0.0f;
-      float res[4 * kFours];
+      const bool wide_out = p.out_dtype == SV_FP32, bf_out = p.out_dtype == SV_BF16;
+      uint32_t res[4 * kFours];  // as they lie in memory
       auto load_res = [&](int f0) {
 #pragma unroll
         for (int i = 0; i < 4 * kFours; ++i) {
           const int v = 4 * (f0 + i / 4 * kStep) + i % 4;
-          res[i] = v < mine ? load_any(p.res, (rank * per + v) * p.rs + n, p.out_dtype) : 0.0f;
+          const int64_t at = (rank * per + v) * p.rs + n;
+          res[i] = 0;
+          if (v < mine)
+            res[i] = wide_out ? static_cast<const uint32_t *>(p.res)[at]
+                              : static_cast<const uint16_t *>(p.res)[at];
         }
+      };
+      auto widen = [&](uint32_t x) {
+        if (wide_out) return __uint_as_float(x);
+        return bf_out ? __uint_as_float(x << 16)
+                      : __half2float(__ushort_as_half(static_cast<unsigned short>(x)));
       };
       if (p.res && in) load_res(tid / kRows);
       if (!(ok = lin_wait<true>(bar, xphase, ab))) break;
@@ -192,13 +200,21 @@ __global__ void __launch_bounds__(kThreads, 1)
               u[0] += c.x, u[1] += c.y, u[2] += c.z, u[3] += c.w;
             }
           }
+          const float4 a4 = activate4(make_float4(y[0] + b, y[1] + b, y[2] + b, y[3] + b), p.act);
+          y[0] = a4.x, y[1] = a4.y, y[2] = a4.z, y[3] = a4.w;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             if (4 * f + e >= mine) break;
-            float v = activate(y[e] + b, p.act);
+            float v = y[e];
             if (kGated) v *= u[e] + bu;
-            if (p.res) v += res[4 * i + e];
-            store_any(p.out, (rank * per + 4 * f + e) * p.os + n, v, p.out_dtype);
+            if (p.res) v += widen(res[4 * i + e]);
+            const int64_t at = (rank * per + 4 * f + e) * p.os + n;
+            if (wide_out)
+              static_cast<float *>(p.out)[at] = v;
+            else
+              static_cast<uint16_t *>(p.out)[at] =
+                  bf_out ? __bfloat16_as_ushort(__float2bfloat16_rn(v))
+                         : __half_as_ushort(__float2half_rn(v));
           }
         }
         if (p.res && f0 + kFours * kStep < fours) load_res(f0 + kFours * kStep);

@@ -152,28 +152,12 @@ __device__ __forceinline__ void store_row32(void *p, int64_t at, int dtype, cons
     }
   }
 }
-// Four values at a time and no inlining: unrolled over 32 the activations are tens of
-// KB of code, which a tile that is a CTA's only one waits for.
-template <int kAct>
-__device__ __noinline__ float4 activate4(float4 v) {
-  return make_float4(activate<kAct>(v.x), activate<kAct>(v.y), activate<kAct>(v.z),
-                     activate<kAct>(v.w));
-}
-template <int kAct>
-__device__ __forceinline__ void activate32(float *v) {
+__device__ __forceinline__ void activate32(float *v, int act) {
+  if (act == SV_ACT_NONE) return;
 #pragma unroll
   for (int i = 0; i < 32; i += 4) {
-    const float4 r = activate4<kAct>(make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]));
+    const float4 r = activate4(make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]), act);
     v[i] = r.x, v[i + 1] = r.y, v[i + 2] = r.z, v[i + 3] = r.w;
-  }
-}
-__device__ __forceinline__ void activate32(float *v, int act) {
-  switch (act) {
-    case SV_ACT_RELU: activate32<SV_ACT_RELU>(v); break;
-    case SV_ACT_GELU: activate32<SV_ACT_GELU>(v); break;
-    case SV_ACT_GELU_TANH: activate32<SV_ACT_GELU_TANH>(v); break;
-    case SV_ACT_SILU: activate32<SV_ACT_SILU>(v); break;
-    default: break;
   }
 }
 // The biases of 32 columns, one a lane, of which the lanes hand each other theirs.
