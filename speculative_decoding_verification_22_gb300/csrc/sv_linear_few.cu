@@ -137,18 +137,29 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int fours = mine > 0 ? (mine + 3) / 4 : 0;
       if (tid == 0) mbar_arrive_expect_tx(bar, fours * args.split * kLanes * 16);
       const uint32_t own = smem_u32(buf + rank * per * kLanes + row * 4);
+      {
+        // the first half of the chunks of 16 columns is that of warps 0-3
+        const int mid = ((M + 15) / 16 + 1) / 2 * 16;
+        const int c_end = warp < 4 ? min(mid, M) : M;
+        int c = warp < 4 ? 0 : mid, q = c / per, left = per - (c - q * per);
+        uint32_t at = lin_remote(own, q) + (per - left) * kLanes * 4, to = lin_remote(bar, q);
 #pragma unroll 1
-      for (int c1 = (warp >> 2) * 16; c1 < M; c1 += 32) {
-        uint32_t x[16];
-        tmem_ld16(tacc + slot * kCols + c1, x);
-        tmem_ld_wait();
-        tmem_reg_fence(x);
+        for (; c < c_end; c += 16) {
+          uint32_t x[16];
+          tmem_ld16(tacc + slot * kCols + c, x);
+          tmem_ld_wait();
+          tmem_reg_fence(x);
 #pragma unroll
-        for (int e = 0; e < 16; e += 4) {
-          if (c1 + e < M) {
-            const int q = (c1 + e) / per;
-            lin_store_remote(lin_remote(own, q) + (c1 + e - q * per) * kLanes * 4, x + e,
-                             lin_remote(bar, q));
+          for (int e = 0; e < 16; e += 4) {
+            if (c + e >= M) break;
+            if (left == 0) {
+              left = per;
+              at = lin_remote(own, ++q);
+              to = lin_remote(bar, q);
+            }
+            lin_store_remote(at, x + e, to);
+            at += kLanes * 16;
+            left -= 4;
           }
         }
       }
@@ -165,34 +176,45 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float b = in && p.bias ? load_any(p.bias, n, p.dtype) : 0.0f;
       const float bu = kGated && in && p.bias_u ? load_any(p.bias_u, n, p.dtype) : 0.0f;
       const bool wide_out = p.out_dtype == SV_FP32, bf_out = p.out_dtype == SV_BF16;
+      const int shift = wide_out ? 2 : 1;
+      const int f_first = tid / kRows;
+      const int64_t m_first = rank * per + 4 * f_first;
+      const int64_t os = p.os << shift, rs = p.rs << shift;  // in bytes
+      char *out = static_cast<char *>(p.out) + ((m_first * p.os + n) << shift);
+      const char *from = static_cast<const char *>(p.res) + ((m_first * p.rs + n) << shift);
       uint32_t res[4 * kFours];  // as they lie in memory
       auto load_res = [&](int f0) {
+        const int rows = mine - 4 * f0;
 #pragma unroll
-        for (int i = 0; i < 4 * kFours; ++i) {
-          const int v = 4 * (f0 + i / 4 * kStep) + i % 4;
-          const int64_t at = (rank * per + v) * p.rs + n;
-          res[i] = 0;
-          if (v < mine)
-            res[i] = wide_out ? static_cast<const uint32_t *>(p.res)[at]
-                              : static_cast<const uint16_t *>(p.res)[at];
+        for (int i = 0; i < kFours; ++i) {
+          const char *at = from + 4 * i * kStep * rs;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            res[4 * i + e] = 0;
+            if (4 * i * kStep + e < rows)
+              res[4 * i + e] = wide_out ? *reinterpret_cast<const uint32_t *>(at)
+                                        : *reinterpret_cast<const uint16_t *>(at);
+            at += rs;
+          }
         }
+        from += 4 * kFours * kStep * rs;
       };
       auto widen = [&](uint32_t x) {
         if (wide_out) return __uint_as_float(x);
         return bf_out ? __uint_as_float(x << 16)
                       : __half2float(__ushort_as_half(static_cast<unsigned short>(x)));
       };
-      if (p.res && in) load_res(tid / kRows);
+      if (p.res && in) load_res(f_first);
       if (!(ok = lin_wait<true>(bar, xphase, ab))) break;
       const float4 *in_parts = reinterpret_cast<const float4 *>(buf) + r;
-      for (int f0 = tid / kRows; f0 < fours && in; f0 += kFours * kStep) {
+      for (int f0 = f_first; f0 < fours && in; f0 += kFours * kStep) {
 #pragma unroll
         for (int i = 0; i < kFours; ++i) {
-          const int f = f0 + i * kStep;
-          if (f >= fours) break;
+          const int f = f0 + i * kStep, rows = mine - 4 * f;
+          if (rows <= 0) break;
           float y[4] = {}, u[4] = {};
-          for (int s = 0; s < args.split; ++s) {
-            const float4 *part = in_parts + (s * (per / 4) + f) * kLanes;
+          const float4 *part = in_parts + f * kLanes;
+          for (int s = 0; s < args.split; ++s, part += per / 4 * kLanes) {
             const float4 a = part[0];
             y[0] += a.x, y[1] += a.y, y[2] += a.z, y[3] += a.w;
             if (kGated) {
@@ -204,18 +226,33 @@ __global__ void __launch_bounds__(kThreads, 1)
           y[0] = a4.x, y[1] = a4.y, y[2] = a4.z, y[3] = a4.w;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            if (4 * f + e >= mine) break;
-            float v = y[e];
-            if (kGated) v *= u[e] + bu;
-            if (p.res) v += widen(res[4 * i + e]);
-            const int64_t at = (rank * per + 4 * f + e) * p.os + n;
-            if (wide_out)
-              static_cast<float *>(p.out)[at] = v;
-            else
-              static_cast<uint16_t *>(p.out)[at] =
-                  bf_out ? __bfloat16_as_ushort(__float2bfloat16_rn(v))
-                         : __half_as_ushort(__float2half_rn(v));
+            if (kGated) y[e] *= u[e] + bu;
+            if (p.res) y[e] += widen(res[4 * i + e]);
           }
+          char *at = out;
+          if (wide_out) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e, at += os)
+              if (e < rows) *reinterpret_cast<float *>(at) = y[e];
+          } else {
+            uint32_t two[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              if (bf_out) {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(y[2 * e], y[2 * e + 1]);
+                two[e] = *reinterpret_cast<const uint32_t *>(&h);
+              } else {
+                const __half2 h = __floats2half2_rn(y[2 * e], y[2 * e + 1]);
+                two[e] = *reinterpret_cast<const uint32_t *>(&h);
+              }
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e, at += os)
+              if (e < rows)
+                *reinterpret_cast<uint16_t *>(at) =
+                    static_cast<uint16_t>(e & 1 ? two[e / 2] >> 16 : two[e / 2]);
+          }
+          out += 4 * kStep * os;
         }
         if (p.res && f0 + kFours * kStep < fours) load_res(f0 + kFours * kStep);
       }
