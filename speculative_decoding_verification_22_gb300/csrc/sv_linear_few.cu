@@ -9,7 +9,8 @@
 //    parts meet in distributed shared memory, where each CTA adds some of the
 //    columns in the order of K (repeatable, no scratch, no second launch) and
 //    stores them.  The adding of a tile runs beside the next one's products.
-//  * Warps 0-7: sums and epilogue; warp 8: TMA; warp 9: products.
+//  * Warps 0-7 (0-15 from 33 rows on): sums and epilogue; then one each for TMA and
+//    for the products.
 //
 // What bounds it (times of kernels in a CUDA graph): the bytes of the weight and about
 // 4 us of start, first load and exchange.  5 x 4096 x 4096 takes 10.4 us (its bytes
@@ -24,8 +25,12 @@
 namespace sv {
 namespace {
 
-constexpr int kEpiWarps = 8, kLoadWarp = 8, kMmaWarp = 9;
-constexpr int kThreads = 32 * 10;
+// Warps of the epilogue: more of them for wider tiles (128 x 16384 x 64 takes 9.5 us
+// with sixteen, 12.5 with eight), fewer where two CTAs are to fit an SM.
+template <int kCols>
+constexpr int epi_warps() { return kCols <= 32 ? 8 : 16; }
+template <int kCols>
+constexpr int threads() { return 32 * (epi_warps<kCols>() + 2); }
 constexpr int kLanes = 128;
 constexpr int kMaxSplit = 8;
 constexpr int kMaxStages = 12;
@@ -56,10 +61,11 @@ template <int kCols>
 constexpr int stage_bytes() { return stage_blocks<kCols>() * (kLanes + kCols) * 128; }
 
 template <int kCols, bool kGated>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(threads<kCols>(), 1)
     linear_few_kernel(const __grid_constant__ CUtensorMap tmW,
                       const __grid_constant__ CUtensorMap tmU,
                       const __grid_constant__ CUtensorMap tmX, const __grid_constant__ Args args) {
+  constexpr int kEpiWarps = epi_warps<kCols>(), kLoadWarp = kEpiWarps, kMmaWarp = kEpiWarps + 1;
   constexpr int kKb = stage_blocks<kCols>(), kStage = stage_bytes<kCols>();
   constexpr int kRows = kGated ? 64 : 128;  // columns of the output in a tile
   const LinearParams &p = args.p;
@@ -119,7 +125,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp < kEpiWarps) {
     // ---------------- sums and epilogue ----------------
-    const int row = tid & 127;  // lane of tensor memory, which two warps read
+    const int row = tid & 127;  // lane of tensor memory
     const uint32_t tacc = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     uint32_t it = 0;
     bool ok = true;
@@ -138,10 +144,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (tid == 0) mbar_arrive_expect_tx(bar, fours * args.split * kLanes * 16);
       const uint32_t own = smem_u32(buf + rank * per * kLanes + row * 4);
       {
-        // the first half of the chunks of 16 columns is that of warps 0-3
-        const int mid = ((M + 15) / 16 + 1) / 2 * 16;
-        const int c_end = warp < 4 ? min(mid, M) : M;
-        int c = warp < 4 ? 0 : mid, q = c / per, left = per - (c - q * per);
+        // each four warps take a share of the chunks of 16 columns
+        constexpr int kShares = kEpiWarps / 4;
+        const int chunks = (M + 15) / 16, share = warp >> 2;
+        const int c_end = min(chunks * (share + 1) / kShares * 16, M);
+        int c = chunks * share / kShares * 16, q = c / per, left = per - (c - q * per);
         uint32_t at = lin_remote(own, q) + (per - left) * kLanes * 4, to = lin_remote(bar, q);
 #pragma unroll 1
         for (; c < c_end; c += 16) {
@@ -410,7 +417,7 @@ int launch(const spec_target &h, const LinearParams &P, cudaStream_t stream) {
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(clusters * args.split);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(threads<kCols>());
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cfg.attrs = attr;
