@@ -492,7 +492,12 @@ int launch(const spec_target &h, const LinearParams &P, cudaStream_t stream) {
   if (row_tiles * col_tiles > (1 << 30)) return SV_ERR_SHAPE;
   args.row_tiles = static_cast<int>(row_tiles);
   args.col_tiles = static_cast<int>(col_tiles);
-  args.group = static_cast<int>(row_tiles < 8 ? row_tiles : 8);
+  // Row tiles of a band: eight, and up to sixteen where their rows of x (36 MB) stay in
+  // L2 while the weight passes, which then comes from HBM once a band (under the power
+  // cap 4096 x 14336 x 4096 gated takes 557 us with sixteen, 580 with eight; 8192 x 8192
+  // x 8192 693 and 680).
+  const int64_t fit = (int64_t(36) << 20) / (512 * P.K);
+  args.group = static_cast<int>(std::min(row_tiles, std::clamp<int64_t>(fit, 8, 16)));
   const int es = P.out_dtype == SV_FP32 ? 4 : 2;
   auto wide = [](const void *p, int64_t stride_bytes, int64_t rows) {
     return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && (rows <= 1 || stride_bytes % 16 == 0);
