@@ -44,7 +44,7 @@ struct Args {
   int split;                   // pairs that share a tile, each a part of K
   int kblocks, stages;
   int bf16;
-  int wide;  // whole chunks of 32 columns, 16-byte accesses of the output and residual
+  int wide;  // 16-byte accesses of the output's and the residual's rows
 };
 
 struct Ctl {
@@ -152,6 +152,41 @@ __device__ __forceinline__ void store_row32(void *p, int64_t at, int dtype, cons
     }
   }
 }
+// One element of each of 32 rows, `live` of them inside.
+__device__ __forceinline__ void load_rows32(const void *p, int64_t at, int64_t stride, int live,
+                                            int dtype, float *v) {
+  uint32_t w[32];
+  if (dtype == SV_FP32) {
+    const uint32_t *q = static_cast<const uint32_t *>(p) + at;
+#pragma unroll
+    for (int r = 0; r < 32; ++r, q += stride) w[r] = r < live ? *q : 0;
+  } else {
+    const uint16_t *q = static_cast<const uint16_t *>(p) + at;
+#pragma unroll
+    for (int r = 0; r < 32; ++r, q += stride) w[r] = r < live ? *q : 0;
+  }
+#pragma unroll
+  for (int r = 0; r < 32; ++r)
+    v[r] = dtype == SV_FP32   ? __uint_as_float(w[r])
+           : dtype == SV_BF16 ? __uint_as_float(w[r] << 16)
+                              : __half2float(__ushort_as_half(static_cast<unsigned short>(w[r])));
+}
+__device__ __forceinline__ void store_rows32(void *p, int64_t at, int64_t stride, int live,
+                                             int dtype, const float *v) {
+  if (dtype == SV_FP32) {
+    float *q = static_cast<float *>(p) + at;
+#pragma unroll
+    for (int r = 0; r < 32; ++r, q += stride)
+      if (r < live) *q = v[r];
+  } else {
+    uint16_t *q = static_cast<uint16_t *>(p) + at;
+#pragma unroll
+    for (int r = 0; r < 32; ++r, q += stride)
+      if (r < live)
+        *q = dtype == SV_BF16 ? __bfloat16_as_ushort(__float2bfloat16_rn(v[r]))
+                              : __half_as_ushort(__float2half_rn(v[r]));
+  }
+}
 __device__ __forceinline__ void activate32(float *v, int act) {
   if (act == SV_ACT_NONE) return;
 #pragma unroll
@@ -194,7 +229,7 @@ __device__ __forceinline__ void finish(const Args &args, int64_t m0, float *piec
 #pragma unroll
     for (int i = 0; i < 32; ++i) y[i] *= u[i];
   }
-  if (args.wide) {
+  if (args.wide && in == 32) {
     const int64_t m = m0 + lane;
     if (m < p.M) {
       if (p.res) {
@@ -205,22 +240,21 @@ __device__ __forceinline__ void finish(const Args &args, int64_t m0, float *piec
       store_row32(p.out, m * p.os + n, p.out_dtype, y);
     }
   } else {
-    // through shared memory, a row at a time with a lane for each column (rows of an
-    // odd stride by single elements of 32 rows at once: 54 us of 205 x 8190 x 8192
-    // without an activation against 38)
+    // Through shared memory, a row at a time with a lane for each column: rows of an
+    // odd stride, by single elements of 32 rows at once, took 54 us of 205 x 8190 x
+    // 8192 without an activation, and 38 so.
 #pragma unroll
     for (int i = 0; i < 32; ++i) piece[lane * 32 + (i ^ lane)] = y[i];
+    const int live = lane < in ? static_cast<int>(min(static_cast<int64_t>(32), p.M - m0)) : 0;
+    if (p.res) load_rows32(p.res, m0 * p.rs + n + lane, p.rs, live, p.out_dtype, u);
     __syncwarp();
-    const int live = static_cast<int>(min(static_cast<int64_t>(32), p.M - m0));
-#pragma unroll 4
-    for (int r = 0; r < live; ++r) {
-      float v = piece[r * 32 + (lane ^ r)];
-      const int64_t m = m0 + r;
-      if (lane < in) {
-        if (p.res) v += load_any(p.res, m * p.rs + n + lane, p.out_dtype);
-        store_any(p.out, m * p.os + n + lane, v, p.out_dtype);
-      }
+#pragma unroll
+    for (int r = 0; r < 32; ++r) y[r] = piece[r * 32 + (lane ^ r)];
+    if (p.res) {
+#pragma unroll
+      for (int r = 0; r < 32; ++r) y[r] += u[r];
     }
+    store_rows32(p.out, m0 * p.os + n + lane, p.os, live, p.out_dtype, y);
   }
   __syncwarp();
 }
@@ -502,8 +536,11 @@ int launch(const spec_target &h, const LinearParams &P, cudaStream_t stream) {
   auto wide = [](const void *p, int64_t stride_bytes, int64_t rows) {
     return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && (rows <= 1 || stride_bytes % 16 == 0);
   };
-  args.wide = P.N % 32 == 0 && wide(P.out, P.os * es, P.M) && wide(P.res, P.rs * es, P.M);
-  args.stages = args.wide || args.split > 1 ? kMaxStages : kMaxStages - 1;
+  args.wide = wide(P.out, P.os * es, P.M) && wide(P.res, P.rs * es, P.M);
+  // (rows that leave through shared memory take the last stage's; a cluster's ring is
+  // idle by then)
+  args.stages =
+      (args.wide && P.N % 32 == 0) || args.split > 1 ? kMaxStages : kMaxStages - 1;
   CUtensorMap x, w, u;
   if (!lin_encode(&x, P.x, P.xs, P.K, P.M, kLanes) ||
       !lin_encode(&w, P.w, P.ws, P.K, P.N, args.bn / 2) ||
