@@ -368,9 +368,9 @@ int launch(const spec_target &h, const LinearParams &P, cudaStream_t stream) {
   args.bn = static_cast<int>((P.M + 15) / 16 * 16);
   args.tiles = static_cast<int>((P.N + kRows - 1) / kRows);
   args.kblocks = static_cast<int>((P.K + kLinBlk - 1) / kLinBlk);
-  // CTAs of a tile, by the K blocks that the longest-working one takes: waves of
-  // tiles over the clusters of a size that run at once (the product in 8 bits
-  // asked for these: one CTA an SM, as here).
+  // CTAs of a tile, by the K blocks that the longest-working one takes, and two more a
+  // tile for its exchange: waves of tiles over the clusters of a size that run at once
+  // (the product in 8 bits asked for these: one CTA an SM, as here).
   int64_t best = INT64_MAX;
   int clusters = 1;
   for (int s = 1; s <= kMaxSplit && s <= args.kblocks; ++s) {
@@ -378,7 +378,7 @@ int launch(const spec_target &h, const LinearParams &P, cudaStream_t stream) {
     if (most < 1) continue;
     const int c = args.tiles < most ? args.tiles : most;
     const int64_t time =
-        static_cast<int64_t>((args.tiles + c - 1) / c) * ((args.kblocks + s - 1) / s);
+        static_cast<int64_t>((args.tiles + c - 1) / c) * ((args.kblocks + s - 1) / s + 2);
     if (time < best) {
       best = time;
       args.split = s;
