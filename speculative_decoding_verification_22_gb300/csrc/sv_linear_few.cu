@@ -13,13 +13,15 @@
 //    for the products.
 //
 // What bounds it (times of kernels in a CUDA graph): the bytes of the weight and about
-// 4 us of start, first load and exchange.  5 x 4096 x 4096 takes 10.4 us (its bytes
-// 5.0), 5 x 14336 x 4096 gated 40.0 (34.6), 20 x 28672 x 8192 gated 142.6 (138.7).  From
-// 64 rows on x's blocks, which every tile reads again from L2, and the exchange count
-// too: 64 x 4096 x 4096 13.2, 128 21.1.  Parts of sums that went by plain remote stores
-// and one release each took 105 us for the gated weight at eight CTAs a tile, 51 as
-// stores that count their bytes; taking K from another place in each tile, so that not
-// all read the same rows of x, took 11.5 us for the first case.
+// 4 us of start, first load and exchange.  5 x 4096 x 4096 takes 9.3 us (its bytes
+// 5.0), 5 x 14336 x 4096 gated 39.4 (34.6), 20 x 28672 x 8192 gated 140.8 (138.7).  With
+// many rows x's blocks, which every tile reads again from L2, and the epilogue count
+// too: 64 x 4096 x 4096 10.4, 128 with a residual 12.6.  The epilogue's code is short
+// because a tile that is a CTA's only one waits for it: with each activation and type
+// unrolled over a thread's elements the last case took 21.  Parts of sums that went by
+// plain remote stores and one release each took 105 us for the 5-row gated weight at
+// eight CTAs a tile, 51 as stores that count their bytes; taking K from another place in
+// each tile, so that not all read the same rows of x, made the first case 10% slower.
 #include "sv_linear_tc.cuh"
 
 namespace sv {

@@ -16,12 +16,12 @@
 //  * The columns of a tile are chosen so that the tiles fill whole waves.
 //
 // What bounds it (times of kernels in a CUDA graph): many rows the tensor cores (4096 x
-// 14336 x 4096 gated 497 us, 1.93 PFLOP/s, their pipe 97% active; 4096 x 4096 x 14336
-// 269 us, 1.79, in four waves of 224 columns; under the power cap of long runs 1.66 and
+// 14336 x 4096 gated 480 us, 2.0 PFLOP/s, their pipe 97% active; 4096 x 4096 x 14336
+// 264 us, 1.82, in four waves of 224 columns; under the power cap of long runs 1.70 and
 // 1.53).  Few tiles: about 8 us of start, first load, exchange and epilogue, and x, whose
-// rows all tiles read at once: 205 x 8190 x 8192 takes 38 us (the weight's bytes 21), 43
+// rows all tiles read at once: 205 x 8192 x 8192 takes 32 us (the weight's bytes 21), 43
 // if every load of x is of the same rows, 29 if the weight's are.  Other places in K for
-// each tile's start: 5 to 25% slower.
+// each tile's start: 5 to 25% slower.  A short K: the epilogue.
 #include <algorithm>
 
 #include "sv_linear_tc.cuh"
@@ -242,7 +242,7 @@ __device__ __forceinline__ void finish(const Args &args, int64_t m0, float *piec
   } else {
     // Through shared memory, a row at a time with a lane for each column: rows of an
     // odd stride, by single elements of 32 rows at once, took 54 us of 205 x 8190 x
-    // 8192 without an activation, and 38 so.
+    // 8192 without an activation, and 32 so.
 #pragma unroll
     for (int i = 0; i < 32; ++i) piece[lane * 32 + (i ^ lane)] = y[i];
     const int live = lane < in ? static_cast<int>(min(static_cast<int64_t>(32), p.M - m0)) : 0;
