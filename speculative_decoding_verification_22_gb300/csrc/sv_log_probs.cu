@@ -14,12 +14,13 @@
 // again by a form that halves its way to the exact one.  A row is read by one CTA, or,
 // where rows are few, by a cluster whose parts the first CTA joins.
 //
-// What bounds it (times of kernels in a CUDA graph): HBM in fp32 (320 x 128256 with 20
-// alternatives 37 us, 2000 x 128256 181 us, 5.7 TB/s; without alternatives 307 us for
-// 4095 x 128000, all of the copy rate), instructions in 16 bits (4095 x 128003 in bf16
-// 213 us with five alternatives, 4.9 TB/s, 73% of the SM's issue; 179 without), and
-// latencies for few rows: 5 x 128256 takes 8.8 us, 4.8 without alternatives.  A CTA that
-// goes on to the next row with its first tile on the way spills: 337 us against 226.
+// What bounds it (times of kernels in a CUDA graph): HBM in fp32 (2000 x 128256 with 20
+// alternatives 164 us, 6.3 TB/s; 320 x 128256 35 us, two CTAs on some SMs, three on
+// others), instructions in 16 bits (4095 x 128003 in bf16 207 us with five alternatives,
+// 5.1 TB/s; 167 without), and latencies for few rows: 5 x 128256 takes 8.6 us, 4.7
+// without alternatives.  With one tile ahead in registers in place of two in shared
+// memory these took 181, 37, 213, 179, 8.8 and 4.8; a CTA that goes on to the next row
+// with its first tile on the way spills: 337 us for the bf16 rows.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -33,8 +34,12 @@ namespace {
 constexpr int kVec = 4;             // loads of a thread in a tile
 constexpr int kResident = 24;       // warps on an SM (the registers are bounded for it)
 constexpr int kBytes = 16;          // of a load
-constexpr int kStage = 1024;        // loads with candidates that a row keeps
-constexpr int kCap = 1024;          // candidates of a tile, where it is taken by itself
+constexpr int kRing = 3;            // tiles of a thread in shared memory
+// Loads with candidates that a row keeps, and candidates of a tile where it is taken by
+// itself: for a row of this many warps (fewer in short rows, of which more CTAs are to
+// fit an SM).
+template <int kWarps>
+constexpr int stage_loads() { return kWarps == 8 ? 1024 : 192 + 32 * kWarps; }
 constexpr int kFew = 256;           // candidates that are ranked
 constexpr int kMaxCluster = 8;
 
@@ -61,6 +66,7 @@ struct Part {
 };
 template <int kWarps>
 struct Shared {
+  static constexpr int kStage = stage_loads<kWarps>(), kCap = stage_loads<kWarps>();
   Part part;
   uint64_t list[2][SV_MAX_TOP];
   uint64_t few[kFew];
@@ -125,6 +131,35 @@ struct Tile {
     for (int i = 0; i < kVec; ++i) {
       v[i] = make_uint4(w, w, w, w);
       if (s.has(first + i * kThreads)) v[i] = __ldcs(p + i * kThreads);
+    }
+  }
+  // The same in two steps: the copy of the thread's loads into its own places of a ring
+  // in shared memory, and the read of what it copied itself.
+  __device__ __forceinline__ static void copy(const S &s, int v0, uint32_t ring) {
+    const int first = v0 + threadIdx.x;
+    const uint4 *p = reinterpret_cast<const uint4 *>(s.row) + first;
+#pragma unroll
+    for (int i = 0; i < kVec; ++i)
+      if (s.has(first + i * kThreads))
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                         ring + i * kThreads * kBytes),
+                     "l"(p + i * kThreads)
+                     : "memory");
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+  __device__ __forceinline__ void read(const S &s, int v0, uint32_t ring) {
+    const T low = from_float<T>(-INFINITY);
+    uint32_t w = 0xFF800000u;
+    if constexpr (sizeof(T) == 2) w = *reinterpret_cast<const uint16_t *>(&low) * 0x10001u;
+    const int first = v0 + threadIdx.x;
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) {
+      v[i] = make_uint4(w, w, w, w);
+      if (s.has(first + i * kThreads))
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(v[i].x), "=r"(v[i].y), "=r"(v[i].z), "=r"(v[i].w)
+                     : "r"(ring + i * kThreads * kBytes)
+                     : "memory");
     }
   }
   // The largest element of each load (a NaN stays).
@@ -240,7 +275,7 @@ __device__ __noinline__ Best<kWarps> best_of_each(const Span<T, kWarps> s, int e
     int upto = s.id0 + s.end * S::kWidth;  // of those that equal lo
     int n = count([&](uint32_t u, int) { return u >= lo; });
     if (n == 0) continue;
-    if (n > kCap) {
+    if (n > sh.kCap) {
       // the value of the tile's last alternative, then the ids of those that equal
       // it, by halving
       uint32_t hi = kHighest + 1;  // count(lo) >= top > count(hi)
@@ -268,11 +303,11 @@ __device__ __noinline__ Best<kWarps> best_of_each(const Span<T, kWarps> s, int e
       if (s.has(first + i / S::kWidth * kThreads) && u <= kHighest &&
           (u > lo || (u == lo && id <= upto))) {
         const int j = atomicAdd(&sh.count, 1);
-        if (j < kCap) sh.cand[j] = order_key(tile.at(i), id);
+        if (j < sh.kCap) sh.cand[j] = order_key(tile.at(i), id);
       }
     }
     __syncthreads();
-    n = min(sh.count, kCap);
+    n = min(sh.count, static_cast<int>(sh.kCap));
     __syncthreads();
     best.rank(n, sh);
   }
@@ -337,8 +372,13 @@ __global__ void __launch_bounds__(32 * kWarps, kResident / kWarps)
   pdl_wait();
   pdl_launch_dependents();
 
-  Tile<T, kWarps> tile, next;
-  next.load(s, s.begin);
+  // two tiles are on their way while one is worked on
+  extern __shared__ uint4 ring_raw[];
+  const uint32_t ring = smem_u32(ring_raw) + tid * kBytes;
+  constexpr uint32_t kSlot = S::kTile * kBytes;
+  Tile<T, kWarps> tile;
+  for (int i = 0; i + 1 < kRing; ++i) tile.copy(s, s.begin + i * S::kTile, ring + i * kSlot);
+  uint32_t slot = 0;
   float m = -INFINITY, sum = 0.0f, t = 0.0f;  // of this thread's elements, d in log2
   if (tid < edges) {
     const int id = tid < s.id0 ? tid : tail + tid - s.id0;
@@ -362,8 +402,11 @@ __global__ void __launch_bounds__(32 * kWarps, kResident / kWarps)
   // that rises from time to time.
   int next_start = 0, number = 0;
   for (int v0 = s.begin; v0 < s.end; v0 += S::kTile, ++number) {
-    tile = next;
-    if (v0 + S::kTile < s.end) next.load(s, v0 + S::kTile);
+    asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 2) : "memory");
+    tile.read(s, v0, ring + slot * kSlot);
+    // (into the place of the last tile, which this thread has read)
+    tile.copy(s, v0 + (kRing - 1) * S::kTile, ring + (slot == 0 ? kRing - 1 : slot - 1) * kSlot);
+    slot = slot + 1 == kRing ? 0 : slot + 1;
     float mv[kVec];
     tile.maxima(mv);
     float most = mv[0];
@@ -406,7 +449,7 @@ __global__ void __launch_bounds__(32 * kWarps, kResident / kWarps)
         for (int i = 0; i < kVec; ++i) {
           if (!(mv[i] >= lim) || !s.has(v0 + tid + i * kThreads)) continue;
           const int j = atomicAdd(&sh.count, 1);
-          if (j < kStage) {
+          if (j < sh.kStage) {
             sh.stage.load[j] = tile.v[i];
             sh.stage.at[j] = v0 + tid + i * kThreads;
           }
@@ -420,7 +463,7 @@ __global__ void __launch_bounds__(32 * kWarps, kResident / kWarps)
     best.raise(sh);
     const int n = sh.count;
     const float lim = from_ordered(best.lim);
-    if (n <= kStage) {
+    if (n <= sh.kStage) {
       for (int i = tid; i < n * S::kWidth; i += kThreads) {
         const int j = i / S::kWidth, k = i % S::kWidth;
         const float y = to_float(reinterpret_cast<const T *>(&sh.stage.load[j])[k]);
@@ -431,7 +474,7 @@ __global__ void __launch_bounds__(32 * kWarps, kResident / kWarps)
       __syncthreads();
     }
     const int few = sh.few_count;
-    if (n > kStage || few > kFew) {
+    if (n > sh.kStage || few > kFew) {
       best = best_of_each(s, edges, best, sh);  // some were not kept
     } else {
       rank_keys(sh.few, few, top, sh.list[0]);
@@ -532,6 +575,11 @@ cudaError_t launch_warps(const sv_log_probs_t &a, int parts, int *status, cudaSt
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(a.rows * parts));
   cfg.blockDim = dim3(32 * kWarps);
+  cfg.dynamicSmemBytes = kRing * Span<T, kWarps>::kTile * kBytes;
+  const cudaError_t e = cudaFuncSetAttribute(log_probs_kernel<T, kWarps>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             kRing * Span<T, kWarps>::kTile * kBytes);
+  if (e != cudaSuccess) return e;
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = parts > 1 ? 2 : 1;
@@ -542,11 +590,11 @@ cudaError_t launch_typed(const sv_log_probs_t &a, int num_sms, int *status,
                          cudaStream_t stream) {
   // Eight warps a CTA where a row has eight of their tiles (128 KB), fewer for short
   // rows, whose start and end then run beside more others': 4000 rows of 20000 in
-  // bf16 take 75 us with eight warps, 55 with four, 56 with two; 16000 of 2000 take
-  // 156, 82 and 56; 4095 of 128003 226, 216 and 261, 320 of 128256 in fp32 36.5, 50
-  // and 87.  Parts of a row only where rows leave SMs idle, as clusters start slowly:
-  // 40 rows of 128256 take 16.8 us in one part, 11.3 in six; 320 take 44 in one and
-  // 51 in two.
+  // bf16 took 75 us with eight warps, 55 with four, 56 with two; 16000 of 2000 156, 82
+  // and 56; 4095 of 128003 226, 216 and 261, 320 of 128256 in fp32 36.5, 50 and 87 (with
+  // one tile ahead, in registers).  Parts of a row only where rows leave SMs idle, as
+  // clusters start slowly: 40 rows of 128256 took 16.8 us in one part, 11.3 in six; 320
+  // 44 in one and 51 in two.
   constexpr int64_t kTileBytes = 256 * kVec * kBytes;
   const int64_t bytes = a.V * static_cast<int64_t>(sizeof(T));
   const int64_t most = std::min<int64_t>(2 * num_sms / a.rows, (bytes - 1) / kTileBytes + 1);

@@ -541,6 +541,48 @@ def test_a_wait_limit_of_nothing(M, N, K):
     ops.close()
 
 
+def some_rows(n):
+    return torch.tensor([0, 1, n // 2, n - 2, n - 1], device="cuda")
+
+
+def test_products_past_32_bits_of_elements(ops):
+    """An output of more than 2^31 elements, and rows 2^31 elements apart."""
+    g = gen(1)
+    M, N, K = 140001, 16384, 64
+
+    def whole(*shape):
+        return torch.randint(-2, 3, shape, generator=g, device="cuda").bfloat16()
+    x, w, r = whole(M, K), whole(N, K), some_rows(M)
+    out = ops.linear(x, w)
+    want = x[r].double() @ w.double().t()
+    assert torch.equal(out[r], want.bfloat16())
+    ops.gated_linear(x, w, w, activation="none", out=out)
+    assert torch.equal(out[r], (want * want).float().bfloat16())
+    del out
+    far = torch.zeros(2, (1 << 31) + 64, dtype=torch.bfloat16, device="cuda")[:, :64]
+    ops.linear(x[:2], w[:64], out=far)
+    assert torch.equal(far, (x[:2].double() @ w[:64].double().t()).bfloat16())
+
+
+def test_rows_past_32_bits_of_elements(ops):
+    g = gen(2)
+    R, V, bf = 17001, 128257, torch.bfloat16
+    x = torch.empty(R, V, dtype=bf, device="cuda").normal_(0, 3, generator=g)
+    t = torch.randint(0, V, (R, 1), generator=g, device="cuda", dtype=torch.int32)
+    r = some_rows(R)
+    got, want = ops.log_probs(x, t, 5), log_probs_ref(x[r], t[r], 5, 1.0)
+    within(got[0][r], want[0], log_probs_error(want[0], V))
+    assert torch.equal(got[2][r], want[2])
+    del x
+    far = torch.empty(2, (1 << 31) + 64, dtype=bf, device="cuda")[:, :64]
+    far.normal_(generator=g)
+    near, w = randn(g, (2, 64), bf), randn(g, (64,), bf)
+    want, h, dout, dh = block_norm_ref(far, near, w, w)
+    out, ho = ops.block_norm(far, near, w, w)
+    within(out, want, rounded(want, dout, bf))
+    within(ho, h, rounded(h, dh, bf))
+
+
 def test_refused_before_anything_is_launched(ops):
     x, w = torch.ones(4, 64, device="cuda").bfloat16(), torch.ones(8, 64, device="cuda").bfloat16()
     r = torch.ones(4, 8, device="cuda").bfloat16()
