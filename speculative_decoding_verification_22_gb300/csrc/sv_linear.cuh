@@ -74,6 +74,29 @@ __device__ __forceinline__ float4 activate4(float4 v, int act) {
   }
 }
 
+// Eight at a time: twice as many independent chains in a call.
+struct Eight {
+  float4 a, b;
+};
+template <int kAct>
+__device__ __noinline__ Eight activate8_call(Eight v) {
+  Eight r;
+  r.a = make_float4(activate<kAct>(v.a.x), activate<kAct>(v.a.y), activate<kAct>(v.a.z),
+                    activate<kAct>(v.a.w));
+  r.b = make_float4(activate<kAct>(v.b.x), activate<kAct>(v.b.y), activate<kAct>(v.b.z),
+                    activate<kAct>(v.b.w));
+  return r;
+}
+__device__ __forceinline__ Eight activate8(Eight v, int act) {
+  switch (act) {
+    case SV_ACT_RELU: return activate8_call<SV_ACT_RELU>(v);
+    case SV_ACT_GELU: return activate8_call<SV_ACT_GELU>(v);
+    case SV_ACT_GELU_TANH: return activate8_call<SV_ACT_GELU_TANH>(v);
+    case SV_ACT_SILU: return activate8_call<SV_ACT_SILU>(v);
+    default: return v;
+  }
+}
+
 __device__ __forceinline__ float load_any(const void *p, int64_t at, int dtype) {
   if (dtype == SV_BF16) return __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[at]);
   if (dtype == SV_FP16) return __half2float(static_cast<const __half *>(p)[at]);

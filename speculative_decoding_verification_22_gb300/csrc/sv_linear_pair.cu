@@ -190,9 +190,12 @@ __device__ __forceinline__ void store_rows32(void *p, int64_t at, int64_t stride
 __device__ __forceinline__ void activate32(float *v, int act) {
   if (act == SV_ACT_NONE) return;
 #pragma unroll
-  for (int i = 0; i < 32; i += 4) {
-    const float4 r = activate4(make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]), act);
-    v[i] = r.x, v[i + 1] = r.y, v[i + 2] = r.z, v[i + 3] = r.w;
+  for (int i = 0; i < 32; i += 8) {
+    const Eight r = activate8({make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]),
+                               make_float4(v[i + 4], v[i + 5], v[i + 6], v[i + 7])},
+                              act);
+    v[i] = r.a.x, v[i + 1] = r.a.y, v[i + 2] = r.a.z, v[i + 3] = r.a.w;
+    v[i + 4] = r.b.x, v[i + 5] = r.b.y, v[i + 6] = r.b.z, v[i + 7] = r.b.w;
   }
 }
 // The biases of 32 columns, one a lane, of which the lanes hand each other theirs.
