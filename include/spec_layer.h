@@ -122,11 +122,11 @@ int spec_layer_block_norm(spec_target_t *h, const sv_block_norm_t *a, void *stre
  *   top_ids        device, int32 [rows, top]; top from 0 to SV_MAX_TOP and V
  *   top_log_probs  device, fp32 [rows, top]
  * Logits of -inf are tokens of probability 0.  A row with a NaN or +inf, or
- * with -inf alone, gets NaN throughout and ids of -1.  rows == 0 is a no-op.
- * Errors: SV_ERR_ARG (null pointer, dtype, a temperature that is not above 0 or not
- * finite, or whose reciprocal is not, n negative), SV_ERR_SHAPE (V outside 1..2^24, top outside
- * 0..min(SV_MAX_TOP, V), n above 2^16, rows negative or above 2^24, a stride
- * below V), SV_ERR_ALIGN, SV_ERR_CUDA. */
+ * with -inf alone, gets NaN throughout (but 0 for a token of -1) and ids of -1.
+ * rows == 0 is a no-op.  Errors: SV_ERR_ARG (null pointer, dtype, n negative, a
+ * temperature that is not above 0 or not finite, or for which 1.4427 / T is not
+ * finite), SV_ERR_SHAPE (V outside 1..2^24, top outside 0..min(SV_MAX_TOP, V), n above
+ * 2^16, rows negative or above 2^24, a stride below V), SV_ERR_ALIGN, SV_ERR_CUDA. */
 #define SV_MAX_TOP 64
 typedef struct {
   const void *logits;
