@@ -15,9 +15,9 @@
 // where rows are few, by a cluster whose parts the first CTA joins.
 //
 // What bounds it (times of kernels in a CUDA graph): HBM in fp32 (2000 x 128256 with 20
-// alternatives 164 us, 6.3 TB/s; 320 x 128256 35 us, two CTAs on some SMs, three on
-// others), instructions in 16 bits (4095 x 128003 in bf16 207 us with five alternatives,
-// 5.1 TB/s; 167 without), and latencies for few rows: 5 x 128256 takes 8.6 us, 4.7
+// alternatives 167 us, 6.1 TB/s; 320 x 128256 36 us, two CTAs on some SMs, three on
+// others), instructions in 16 bits (4095 x 128003 in bf16 210 us with five alternatives,
+// 5.0 TB/s; 169 without), and latencies for few rows: 5 x 128256 takes 8.8 us, 4.7
 // without alternatives.  With one tile ahead in registers in place of two in shared
 // memory these took 181, 37, 213, 179, 8.8 and 4.8; a CTA that goes on to the next row
 // with its first tile on the way spills: 337 us for the bf16 rows.
@@ -56,7 +56,7 @@ __device__ __forceinline__ float from_ordered(uint32_t u) {
 __device__ __forceinline__ uint64_t order_key(float x, int id) {
   return static_cast<uint64_t>(ordered(x)) << 32 | static_cast<uint32_t>(~id);
 }
-constexpr uint32_t kLowest = 0x007FFFFFu, kHighest = 0xFF800000u;  // ordered(-inf), (inf)
+constexpr uint32_t kFinite = 0x00800000u, kHighest = 0xFF800000u;  // ordered(-FLT_MAX), (inf)
 
 // What one CTA knows of its part of a row, read by the first of its cluster.
 struct Part {
@@ -78,7 +78,7 @@ struct Shared {
     uint64_t cand[kCap + SV_MAX_TOP];
   };
   float red[3][kMaxCluster];
-  uint32_t bound[kWarps];
+  uint32_t bound[kWarps], first;
   int count, few_count;
 };
 
@@ -194,7 +194,7 @@ struct Best {
   static constexpr int kThreads = 32 * kWarps;
   int top, warps;
   int found = 0, cur = 0;   // the list's keys and its buffer
-  uint32_t lim = kLowest;   // ordered values from here are candidates
+  uint32_t lim = kFinite;   // ordered values from here are candidates
 
   // Ranks the n candidates with the list.
   __device__ __forceinline__ void rank(int n, Sh &sh) {
@@ -234,8 +234,9 @@ struct Best {
 };
 
 // The best of a part whose tiles are taken one by one, however many of their
-// elements equal each other or rise; `edges` keys of the row's edges lie in `few`
-// and come last, so that the tiles are met in the order of their ids.
+// elements equal each other or rise; `edges` keys of the row's edges (and of a
+// part's first elements) lie in `few` and come last, so that the tiles are met in the order of their
+// ids.
 template <class T, int kWarps>
 __device__ __noinline__ Best<kWarps> best_of_each(const Span<T, kWarps> s, int edges,
                                                  Best<kWarps> best, Shared<kWarps> &sh) {
@@ -345,6 +346,7 @@ __global__ void __launch_bounds__(32 * kWarps, kResident / kWarps)
     log_probs_kernel(const sv_log_probs_t P, int *status) {
   using S = Span<T, kWarps>;
   constexpr int kThreads = S::kThreads;
+  static_assert(kThreads >= SV_MAX_TOP);
   __shared__ Shared<kWarps> sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   uint32_t rank, parts;
@@ -364,10 +366,11 @@ __global__ void __launch_bounds__(32 * kWarps, kResident / kWarps)
   s.end = static_cast<int>(static_cast<int64_t>(loads) * (rank + 1) / parts);
   // the edges: one element for some of the first CTA's threads
   const int tail = s.id0 + loads * S::kWidth;
-  const int edges = rank == 0 ? s.id0 + V - tail : 0;
+  int edges = rank == 0 ? s.id0 + V - tail : 0;
   if (tid == 0) {
     sh.count = 0;
     sh.few_count = edges;
+    sh.first = kFinite - 1;
   }
   pdl_wait();
   pdl_launch_dependents();
@@ -441,6 +444,21 @@ __global__ void __launch_bounds__(32 * kWarps, kResident / kWarps)
         best.publish(m, sh);
         if (number == 0) __syncthreads();
         best.raise(sh);
+        // Behind the part's first `top` elements, one that only equals the least of them
+        // is no alternative.  Ties at a row's least value, as a mask makes them, are no
+        // candidates so, but for those first ones (with them, rows of 128256 masked down
+        // to 10 were read again: 5 rows took 26.8 us in place of 8.1, 320 rows 120 in
+        // place of 32).  A warp looks there if all its threads have a candidate.
+        if (number == 0 && __all_sync(0xffffffffu, ordered(most) >= best.lim) &&
+            (s.end - s.begin) * S::kWidth >= top) {
+          uint32_t u = kHighest;
+#pragma unroll 1
+          for (int i = lane; i < top; i += 32)
+            u = min(u, ordered(to_float(s.row[s.begin * S::kWidth + i])));
+          u = max(__reduce_min_sync(0xffffffffu, u), kFinite - 1);
+          if (lane == 0) sh.first = u;
+          best.lim = max(best.lim, u + 1);
+        }
         next_start = number == 0 ? 1 : number < 32 ? 2 * number : number + 32;
       }
       const float lim = from_ordered(best.lim);
@@ -461,13 +479,22 @@ __global__ void __launch_bounds__(32 * kWarps, kResident / kWarps)
     best.publish(m, sh);
     __syncthreads();
     best.raise(sh);
+    best.lim = max(best.lim, sh.first + 1);
     const int n = sh.count;
-    const float lim = from_ordered(best.lim);
+    if (best.lim == sh.first + 1) {
+      // maybe not `top` from it on: the first ones fill up
+      const bool inside = tid < min(top, (s.end - s.begin) * S::kWidth);
+      const float y = inside ? to_float(s.row[s.begin * S::kWidth + tid]) : INFINITY;
+      const bool fill = ordered(y) < best.lim;
+      if (fill)
+        sh.few[atomicAdd(&sh.few_count, 1)] = order_key(y, s.id0 + s.begin * S::kWidth + tid);
+      edges += __syncthreads_count(fill);
+    }
     if (n <= sh.kStage) {
       for (int i = tid; i < n * S::kWidth; i += kThreads) {
         const int j = i / S::kWidth, k = i % S::kWidth;
         const float y = to_float(reinterpret_cast<const T *>(&sh.stage.load[j])[k]);
-        if (!(y >= lim)) continue;
+        if (ordered(y) < best.lim) continue;
         const int at = atomicAdd(&sh.few_count, 1);
         if (at < kFew) sh.few[at] = order_key(y, s.id0 + sh.stage.at[j] * S::kWidth + k);
       }

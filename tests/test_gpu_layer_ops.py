@@ -385,6 +385,30 @@ def test_log_probs_of_hard_rows(ops, R, V, kind):
     check_log_probs(ops, x.to(dt).contiguous(), t, 20, 1.0)
 
 
+@pytest.mark.parametrize("R,V", [(3, 70), (2, 1000), (5, 128256), (300, 20003)])
+@pytest.mark.parametrize("keep", [1, 9, 64, 65])
+@pytest.mark.parametrize("where", ["anywhere", "first", "last"])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("mask", [-math.inf, -30000.0])
+def test_log_probs_of_rows_with_few_tokens_left(ops, R, V, keep, where, dtype, mask):
+    """As many tokens allowed as alternatives, one more, fewer: the first of those that
+    are not fill up.  Of the allowed ones two are equal and one is the lowest value, which may be below
+    the mask's."""
+    g = gen(V + keep)
+    order = torch.rand(R, V, generator=g, device="cuda").argsort(1).argsort(1)
+    if where != "anywhere":
+        order = torch.arange(V, device="cuda")[None].repeat(R, 1)
+        order = order if where == "first" else V - 1 - order
+    x = randn(g, (R, V), torch.float32, 3.0).to(DTYPES[dtype])
+    x[order == 1] = 1.0
+    x[order == 2] = 1.0
+    x[order == 3] = torch.finfo(x.dtype).min
+    x[order >= keep] = mask
+    t = torch.randint(0, V, (R, 2), generator=g, device="cuda", dtype=torch.int32)
+    for top in (1, 8, 64):
+        check_log_probs(ops, x, t, top, 1.0)
+
+
 @pytest.mark.parametrize("V", [50, 70001])
 def test_log_probs_of_rows_without_a_finite_maximum(ops, V):
     g = gen(V)
