@@ -17,8 +17,8 @@
 //
 // What bounds it (times of kernels in a CUDA graph): many rows the tensor cores (4096 x
 // 14336 x 4096 gated 480 us, 2.0 PFLOP/s, their pipe 97% active; 4096 x 4096 x 14336
-// 264 us, 1.82, in four waves of 224 columns; under the power cap of long runs 1.70 and
-// 1.53).  Few tiles: about 8 us of start, first load, exchange and epilogue, and x, whose
+// 264 us, 1.82, in four waves of 224 columns; under the power cap of long runs 1.77 and
+// 1.58).  Few tiles: about 8 us of start, first load, exchange and epilogue, and x, whose
 // rows all tiles read at once: 205 x 8192 x 8192 takes 32 us (the weight's bytes 21), 43
 // if every load of x is of the same rows, 29 if the weight's are.  Other places in K for
 // each tile's start: 5 to 25% slower.  A short K: the epilogue.
@@ -569,8 +569,8 @@ int launch(const spec_target &h, const LinearParams &P, cudaStream_t stream) {
   args.col_tiles = static_cast<int>(col_tiles);
   // Row tiles of a band: eight, and up to sixteen where their rows of x (36 MB) stay in
   // L2 while the weight passes, which then comes from HBM once a band (under the power
-  // cap 4096 x 14336 x 4096 gated takes 557 us with sixteen, 580 with eight; 8192 x 8192
-  // x 8192 693 and 680).
+  // cap, with an epilogue of 10 us more, 4096 x 14336 x 4096 gated took 557 us with
+  // sixteen, 580 with eight; 8192 x 8192 x 8192 693 and 680).
   const int64_t fit = (int64_t(36) << 20) / (512 * P.K);
   args.group = static_cast<int>(std::min(row_tiles, std::clamp<int64_t>(fit, 8, 16)));
   const int es = P.out_dtype == SV_FP32 ? 4 : 2;

@@ -234,9 +234,9 @@ struct Best {
 };
 
 // The best of a part whose tiles are taken one by one, however many of their
-// elements equal each other or rise; `edges` keys of the row's edges (and of a
-// part's first elements) lie in `few` and come last, so that the tiles are met in the order of their
-// ids.
+// elements equal each other or rise; `edges` keys of the row's edges (and of a part's
+// first elements) lie in `few` and come last, so that the tiles are met in the order of
+// their ids.
 template <class T, int kWarps>
 __device__ __noinline__ Best<kWarps> best_of_each(const Span<T, kWarps> s, int edges,
                                                  Best<kWarps> best, Shared<kWarps> &sh) {
