@@ -9,6 +9,7 @@ entry points raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -45,7 +46,7 @@ EXPORTS = ("spec_verify_create", "spec_verify_run", "spec_verify_run_host",
            "spec_verify_run_noalloc", "spec_ngram_draft", "spec_verify_run_truncated",
            "spec_verify_tree_greedy", "spec_verify_run_fp8", "spec_verify_plan",
            "spec_verify_debug_stall", "spec_verify_submit_host", "spec_verify_wait_host",
-           "spec_verify_log_probs",
+           "spec_verify_log_probs", "spec_verify_stream",
            "spec_target_create", "spec_target_destroy", "spec_target_status",
            "spec_target_set_wait_limit", "spec_target_rms_norm", "spec_target_rms_norm_fp8",
            "spec_target_matmul_fp8", "spec_target_rope_freqs", "spec_target_rope_append",
@@ -91,6 +92,8 @@ def load_library():
         lib.spec_verify_run_host.argtypes = [vp, vp, vp, vp, vp, vp, f32, vp, vp]
         lib.spec_verify_status.argtypes = [vp]
         lib.spec_verify_set_stream.argtypes = [vp, vp]
+        lib.spec_verify_stream.argtypes = [vp]
+        lib.spec_verify_stream.restype = vp
         lib.spec_verify_debug_logits.argtypes = [vp, vp]
         lib.spec_verify_debug_lse.argtypes = [vp, vp]
         lib.spec_verify_set_wait_limit.argtypes = [vp, ctypes.c_uint64]
@@ -136,7 +139,7 @@ def load_library():
         for name in ("linear", "gated_linear", "block_norm", "log_probs"):
             getattr(lib, f"spec_layer_{name}").argtypes = [vp, vp, vp]
         for name in EXPORTS:
-            if name not in ("spec_verify_strerror", "spec_verify_destroy",
+            if name not in ("spec_verify_strerror", "spec_verify_destroy", "spec_verify_stream",
                             "spec_target_destroy"):
                 getattr(lib, name).restype = ctypes.c_int
         _lib = lib
@@ -232,6 +235,11 @@ def spec_verify_status(h) -> int:
 def spec_verify_set_stream(h, stream=None) -> None:
     _check(load_library().spec_verify_set_stream(h, _stream_handle(stream)),
            "spec_verify_set_stream")
+
+
+def spec_verify_stream(h) -> int:
+    """The number of the stream that calls are enqueued on (0: the legacy default one)."""
+    return load_library().spec_verify_stream(h) or 0
 
 
 def spec_verify_debug_logits(h, dst) -> None:
@@ -358,6 +366,7 @@ class SpecVerify:
         self.V, self.d, self.B, self.K, self.dtype = V, d, B, K, dtype
         self.device = torch.device("cuda" if device is None else device)
         with torch.cuda.device(self.device):
+            self.device = torch.device("cuda", torch.cuda.current_device())
             self.h = spec_verify_create(V, d, B, K, dtype, stream)
 
     def run(self, hidden, W_lm, draft_tokens, q_logits, uniforms, temperature,
@@ -404,25 +413,51 @@ class SpecVerify:
                                 out_nodes, out_n)
         return out_t, out_nodes[:, :self.K], out_n
 
-    def log_probs(self, tokens=None, top=0, temperature=1.0):
+    def _own_stream(self):
+        """The handle's stream made the current one (nothing to do where it is), so that
+        what is allocated meanwhile is that stream's memory."""
+        raw = spec_verify_stream(self.h)
+        if (torch.cuda.current_device() == self.device.index
+                and torch.cuda.current_stream().cuda_stream == raw):
+            return contextlib.nullcontext()
+        return torch.cuda.stream(torch.cuda.ExternalStream(raw, self.device) if raw > 1
+                                 else torch.cuda.default_stream(self.device))
+
+    def log_probs(self, tokens=None, top=0, temperature=1.0, out=None):
         """What the last run's logits say of its answers: log probabilities
-        [B, K+1] of ``tokens`` (int32 [B, K+1], as ``run`` returns them; -1 gets 0),
-        the rows' entropies [B, K+1], and with ``top`` > 0 the most likely ids int32
-        [B, K+1, top] and their log probabilities."""
+        [B, K+1] of ``tokens`` (int32 [B, K+1], as ``run`` returns them; -1 gets 0;
+        None in their place without tokens), the rows' entropies [B, K+1], and with
+        ``top`` > 0 the most likely ids int32 [B, K+1, top] and their log
+        probabilities.  ``out``: the same tensors to be filled.  Enqueued on the
+        handle's stream, whose memory the outputs made here are."""
         shape = (self.B, self.K + 1)
-        if tokens is not None and (tuple(tokens.shape) != shape or tokens.dtype != torch.int32
-                                   or tokens.device.type != "cuda"):
-            raise ValueError(f"log_probs: tokens must be int32 {shape} on the GPU")
+
+        def check(t, what, want, dtype):
+            if (not torch.is_tensor(t) or tuple(t.shape) != want or t.dtype != dtype
+                    or t.device.type != "cuda" or t.device != self.device):
+                raise ValueError(f"log_probs: {what} must be {dtype} {want} on the handle's GPU")
+        if tokens is not None:
+            check(tokens, "tokens", shape, torch.int32)
         if not 0 <= top <= min(64, self.V):
             raise ValueError("log_probs: top must be from 0 to 64 and at most V")
-
-        def made(*more, dtype=torch.float32):
-            return torch.empty(shape + more, dtype=dtype, device=self.device)
-        out = [made() if tokens is not None else None, made()]
+        kinds = [(shape, torch.float32), (shape, torch.float32)]
         if top:
-            out += [made(top, dtype=torch.int32), made(top)]
-        spec_verify_log_probs(self.h, tokens, temperature, top, out[0], out[1],
-                              *(out[2:] or (None, None)))
+            kinds += [(shape + (top,), torch.int32), (shape + (top,), torch.float32)]
+        if out is not None:
+            out = list(out)
+            if len(out) != len(kinds) or (out[0] is None) != (tokens is None):
+                raise ValueError("log_probs: out must hold two tensors, or four with top (the "
+                                 "first None without tokens)")
+            for i, (want, dtype) in enumerate(kinds):
+                if i or tokens is not None:
+                    check(out[i], "out", want, dtype)
+        with self._own_stream():
+            if out is None:
+                out = [torch.empty(want, dtype=dtype, device=self.device)
+                       if i or tokens is not None else None
+                       for i, (want, dtype) in enumerate(kinds)]
+            spec_verify_log_probs(self.h, tokens, temperature, top, out[0], out[1],
+                                  *(out[2:] or (None, None)))
         return out
 
     def status(self) -> int:

@@ -364,6 +364,8 @@ int spec_verify_set_stream(spec_verify_t *h, void *stream) {
   return SV_OK;
 }
 
+void *spec_verify_stream(const spec_verify_t *h) { return h ? h->stream : nullptr; }
+
 int spec_verify_set_wait_limit(spec_verify_t *h, uint64_t limit_ns) {
   if (!h) return SV_ERR_ARG;
   h->wait_limit_ns = limit_ns;
@@ -779,6 +781,9 @@ int spec_verify_log_probs(spec_verify_t *h, const int32_t *tokens, float tempera
   a.temperature = temperature;
   const int c = sv::log_probs_checks(a);
   if (c != SV_OK) return c;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return SV_ERR_CUDA;
+  if (dev != h->device) return SV_ERR_ARG;
   return sv::launch_log_probs(a, h->num_sms, h->w.status, h->stream) == cudaSuccess ? SV_OK
                                                                                    : SV_ERR_CUDA;
 }
