@@ -28,7 +28,9 @@ namespace sv {
 namespace {
 
 // Warps of the epilogue: more of them for wider tiles (128 x 16384 x 64 takes 9.5 us
-// with sixteen, 12.5 with eight), fewer where two CTAs are to fit an SM.
+// with sixteen, 12.5 with eight), fewer for narrow ones, whose columns are few (5 x 4096 x
+// 4096 9.0 us with eight, 9.3 with sixteen; 32 x 16384 x 64 5.6 and 5.0, but 32 x 1024 x
+// 4096 6.0 and 6.3).
 template <int kCols>
 constexpr int epi_warps() { return kCols <= 32 ? 8 : 16; }
 template <int kCols>
@@ -392,13 +394,19 @@ int launch(const spec_target &h, const LinearParams &P, cudaStream_t stream) {
   args.bufs = P.M <= 32 ? 2 : 1;
   const int fixed =
       1024 + args.bufs * args.split * per * kLanes * 4 + static_cast<int>(sizeof(Ctl));
-  // Where a CTA's part of the weight is short and x has few rows, two CTAs fit an SM,
-  // so that the next kernel of a stream starts and reads ahead while this one ends
-  // (5 x 4096 x 4096: 10.2 us against 10.8 with the whole ring; of the long parts of
-  // 20 x 28672 x 8192, gated, the whole ring takes 143 and the half 155).
+  // Where a CTA's part of the weight is short, half the ring leaves shared memory to the
+  // next kernel of a stream, which starts and reads ahead while this one ends: the norm
+  // behind a product (gated projections, product and norm of 5 x 4096 in bf16, F 4096, take
+  // 26.4 us in place of 27.9), but not this kernel again, as the registers hold one CTA an
+  // SM (5 x 4096 x 4096 9.05 us against 9.21; 5 x 1024 x 4096 5.95 against 5.72). From 17
+  // rows on x's blocks and the parts of sums take half of that half, and the whole ring is
+  // better (32 x 4096 x 4096: 9.6 us against 10.3, 32 x 6144 x 4096 11.9 against 13.9,
+  // layers of 32 rows 28.4 against 29.7); so it is for most long parts (16 x 5120 x 8192
+  // 16.9 us against 18.3, 5 x 4096 x 14336 21.0 against 21.7, 5 x 14336 x 4096, gated, 39.0
+  // against 38.2).
   const int64_t part = static_cast<int64_t>(args.tiles) * args.kblocks * kLanes * 128 /
                        (static_cast<int64_t>(clusters) * args.split);
-  const int room = P.M <= 32 && part <= 512 * 1024 ? h.smem_optin / 2 - 1024 : h.smem_optin;
+  const int room = P.M <= 16 && part <= 512 * 1024 ? h.smem_optin / 2 - 1024 : h.smem_optin;
   args.stages = (room - fixed) / stage_bytes<kCols>();
   if (args.stages > kMaxStages) args.stages = kMaxStages;
   if (args.stages < 2) return SV_ERR_CUDA;
