@@ -202,9 +202,9 @@ void *spec_verify_stream(const spec_verify_t *h);
  * The temperature is the caller's (a greedy round is scored at any), the cuts
  * of a truncated run are not applied.  Enqueued on the handle's stream; rows
  * without a finite largest logit get NaN (but 0 for -1) and ids of -1.  Errors:
- * SV_ERR_ARG (null handle or pointers, no run yet, another current device than the
- * handle's, a temperature that is not above 0 or not finite), SV_ERR_SHAPE (top),
- * SV_ERR_ALIGN, SV_ERR_CUDA. */
+ * SV_ERR_ARG (null handle or pointers, no run yet or a last one that returned
+ * SV_ERR_CUDA, another current device than the handle's, a temperature that is not
+ * above 0 or not finite), SV_ERR_SHAPE (top), SV_ERR_ALIGN, SV_ERR_CUDA. */
 int spec_verify_log_probs(spec_verify_t *h, const int32_t *tokens, float temperature,
                           int32_t top, float *log_probs, float *entropy, int32_t *top_ids,
                           float *top_log_probs);

@@ -49,6 +49,7 @@ struct spec_verify {
   sv::Work w{};
   sv::TcPlan plan{};
   unsigned epoch = 0;
+  bool scored = false;  // the logits scratch is that of the last run, which was enqueued
   uint64_t wait_limit_ns = 1000000000ull;
   // staging for spec_verify_run_host
   void *st_hidden = nullptr;
@@ -478,6 +479,7 @@ int run_impl(spec_verify_t *h, const void *hidden, const void *W_lm,
 
   cudaStream_t st = h->stream;
   const unsigned epoch = ++h->epoch;
+  h->scored = false;
   // Fast tail: the contraction (drain mode) leaves per-CTA row statistics
   // and the draft logits at the draft tokens, and one CTA per sequence
   // decides from them.  Truncated rows, greedy and tree verification keep
@@ -609,6 +611,7 @@ int run_impl(spec_verify_t *h, const void *hidden, const void *W_lm,
     if (sv::launch_trunc(TP, st) != cudaSuccess) return SV_ERR_CUDA;
   }
   if (sv::launch_tail(T, st) != cudaSuccess) return SV_ERR_CUDA;
+  h->scored = true;
   return SV_OK;
 }
 
@@ -765,7 +768,7 @@ int spec_verify_wait_host(spec_verify_t *h, int slot) {
 int spec_verify_log_probs(spec_verify_t *h, const int32_t *tokens, float temperature,
                           int32_t top, float *log_probs, float *entropy, int32_t *top_ids,
                           float *top_log_probs) {
-  if (!h || h->epoch == 0) return SV_ERR_ARG;
+  if (!h || !h->scored) return SV_ERR_ARG;
   sv_log_probs_t a{};
   a.logits = h->w.logits;
   a.tokens = tokens;
