@@ -471,13 +471,13 @@ cudaError_t launch_typed(const sv_block_norm_t &a, int num_sms, cudaStream_t str
   // Few rows: one vector a thread, as many threads as that takes.  Many: four of 16-bit
   // rows (16384 rows of 4096 in bf16 to E4M3 with a gate: 93 us, 5.1 TB/s; 112 with
   // two; 4000 of 8192 to E4M3 49 against 65), two of fp32 rows (16384 of 4096 with a
-  // full gate: 212 us; 241 with four).
-  const int many = sizeof(T) == 2 || nvec > 2048 ? 4 : 2;
-  const int kvec = a.rows <= num_sms && nvec <= 1024 ? 1 : many;
-  switch (kvec) {
-    case 1: return launch_vec<T, 1>(a, stream);
-    case 2: return launch_vec<T, 2>(a, stream);
-    default: return launch_vec<T, 4>(a, stream);
+  // full gate: 212 us; 241 with four) while 1024 threads hold one.
+  if (a.rows <= num_sms && nvec <= 1024) return launch_vec<T, 1>(a, stream);
+  if constexpr (sizeof(T) == 2) {
+    return launch_vec<T, 4>(a, stream);
+  } else {
+    if (nvec <= 2048) return launch_vec<T, 2>(a, stream);
+    return launch_block<T, 4, 1024>(a, static_cast<int>((nvec + 127) / 128), 1, stream);
   }
 }
 
