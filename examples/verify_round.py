@@ -101,7 +101,7 @@ class Block:
                                (start + n).int())
         if self.ffn:
             return self.feed_forward(o.view(-1, hq * D), x).view(B, n, self.d)
-        o = o.view(-1, hq * D) @ self.w_out.t()
+        o = self.ops.linear(o.view(-1, hq * D), self.w_out)
         return self.ops.rms_norm(o, self.norm2, residual=x)[0].view(B, n, self.d)
 
     def feed_forward(self, o, x):
