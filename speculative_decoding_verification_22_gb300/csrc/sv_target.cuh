@@ -16,7 +16,9 @@ struct spec_target {
   int *status = nullptr;   // device: first error since it was last read
   float *scratch = nullptr;  // device: partial results
   size_t scratch_bytes = 0;
-  int clusters[9] = {};    // the product's clusters of 1..8 CTAs that run at once
+  // Clusters of 1..8 CTAs that run at once, one CTA an SM: asked for the 8-bit product, and
+  // the same for the 16-bit products' kernels (76, 46, 36, 28, 23, 15, 15 from two CTAs on).
+  int clusters[9] = {};
 };
 
 namespace sv {

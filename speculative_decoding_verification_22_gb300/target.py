@@ -191,9 +191,9 @@ class TargetOps:
     def linear(self, x, weight, bias=None, activation=None, residual=None, out_dtype=None,
                out=None, stream=None):
         """act(x weight^T + bias) + residual, x [M, K], weight [N, K], bias [N] of one
-        type; ``activation`` one of ``ACTIVATIONS``.  The output [M, N] has
-        ``out_dtype`` (x's if not given), the residual the output's type; it may be
-        ``out`` itself."""
+        type; ``activation`` one of ``ACTIVATIONS``.  The output [M, N] has ``out``'s
+        type if that is given, else ``out_dtype`` (x's if not given), the residual the
+        output's type; it may be ``out`` itself."""
         return _bound.linear(self, x, weight, bias, _activation(activation), residual,
                              _out_code(out_dtype), out, stream)
 
@@ -201,7 +201,8 @@ class TargetOps:
                      out_dtype=None, out=None, stream=None):
         """act(x w_gate^T + bias_gate) * (x w_up^T + bias_up): the first half of a
         gated feed-forward block, whose second is ``linear`` with the residual.
-        x [M, K], w_gate and w_up [N, K] (halves of one fused weight or two)."""
+        x [M, K], w_gate and w_up [N, K] (halves of one fused weight or two).  The
+        output's type as in ``linear``."""
         return _bound.gated(self, x, w_gate, w_up, bias_gate, bias_up, _activation(activation),
                             _out_code(out_dtype), out, stream)
 
