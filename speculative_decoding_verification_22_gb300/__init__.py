@@ -360,7 +360,9 @@ def spec_verify_destroy(h) -> None:
 
 
 class SpecVerify:
-    """Owns one handle; ``run`` writes tokens [B, K+1] and n_accepted [B]."""
+    """Owns one handle; ``run`` writes tokens [B, K+1] and n_accepted [B].  Everything is
+    enqueued on the handle's stream, whose memory the outputs made here are: used on
+    another stream, they have to be kept until that use has ended, or recorded there."""
 
     def __init__(self, V, d, B, K, dtype="bf16", device=None, stream=None):
         self.V, self.d, self.B, self.K, self.dtype = V, d, B, K, dtype
@@ -368,50 +370,6 @@ class SpecVerify:
         with torch.cuda.device(self.device):
             self.device = torch.device("cuda", torch.cuda.current_device())
             self.h = spec_verify_create(V, d, B, K, dtype, stream)
-
-    def run(self, hidden, W_lm, draft_tokens, q_logits, uniforms, temperature,
-            out_tokens=None, out_n_accepted=None):
-        if out_tokens is None:
-            out_tokens = torch.empty((self.B, self.K + 1), dtype=torch.int32,
-                                     device=self.device)
-        if out_n_accepted is None:
-            out_n_accepted = torch.empty((self.B,), dtype=torch.int32, device=self.device)
-        spec_verify_run(self.h, hidden, W_lm, draft_tokens, q_logits, uniforms,
-                        temperature, out_tokens, out_n_accepted)
-        return out_tokens, out_n_accepted
-
-    def run_truncated(self, hidden, W_lm, draft_tokens, q_logits, uniforms, temperature,
-                      target_top_k=0, target_top_p=1.0, draft_top_k=0, draft_top_p=1.0,
-                      out_tokens=None, out_n_accepted=None):
-        if out_tokens is None:
-            out_tokens = torch.empty((self.B, self.K + 1), dtype=torch.int32,
-                                     device=self.device)
-        if out_n_accepted is None:
-            out_n_accepted = torch.empty((self.B,), dtype=torch.int32, device=self.device)
-        spec_verify_run_truncated(self.h, hidden, W_lm, draft_tokens, q_logits, uniforms,
-                                  temperature, target_top_k, target_top_p, draft_top_k,
-                                  draft_top_p, out_tokens, out_n_accepted)
-        return out_tokens, out_n_accepted
-
-    def run_fp8(self, hidden8, hidden_scale, W8, w_scale, draft_tokens, q_logits, uniforms,
-                temperature, out_tokens=None, out_n_accepted=None):
-        if out_tokens is None:
-            out_tokens = torch.empty((self.B, self.K + 1), dtype=torch.int32,
-                                     device=self.device)
-        if out_n_accepted is None:
-            out_n_accepted = torch.empty((self.B,), dtype=torch.int32, device=self.device)
-        spec_verify_run_fp8(self.h, hidden8, hidden_scale, W8, w_scale, draft_tokens, q_logits,
-                            uniforms, temperature, out_tokens, out_n_accepted)
-        return out_tokens, out_n_accepted
-
-    def run_tree_greedy(self, hidden, W_lm, tree_tokens, tree_parents):
-        """Returns (tokens [B, N+1], nodes [B, N], n [B])."""
-        out_t = torch.empty((self.B, self.K + 1), dtype=torch.int32, device=self.device)
-        out_nodes = torch.empty((self.B, max(self.K, 1)), dtype=torch.int32, device=self.device)
-        out_n = torch.empty((self.B,), dtype=torch.int32, device=self.device)
-        spec_verify_tree_greedy(self.h, hidden, W_lm, tree_tokens, tree_parents, out_t,
-                                out_nodes, out_n)
-        return out_t, out_nodes[:, :self.K], out_n
 
     def _own_stream(self):
         """The handle's stream made the current one (nothing to do where it is), so that
@@ -422,6 +380,50 @@ class SpecVerify:
             return contextlib.nullcontext()
         return torch.cuda.stream(torch.cuda.ExternalStream(raw, self.device) if raw > 1
                                  else torch.cuda.default_stream(self.device))
+
+    def _outputs(self, out_tokens, out_n_accepted, nodes=False):
+        """A run's outputs, those that are not given made under the handle's stream."""
+        missing = [s for s, t in (((self.B, self.K + 1), out_tokens),
+                                  ((self.B,), out_n_accepted)) if t is None]
+        if nodes:
+            missing.append((self.B, max(self.K, 1)))
+        if not missing:
+            return out_tokens, out_n_accepted
+        with self._own_stream():
+            made = [torch.empty(s, dtype=torch.int32, device=self.device) for s in missing]
+        given = (made.pop(0) if out_tokens is None else out_tokens,
+                 made.pop(0) if out_n_accepted is None else out_n_accepted)
+        return (*given, *made)
+
+    def run(self, hidden, W_lm, draft_tokens, q_logits, uniforms, temperature,
+            out_tokens=None, out_n_accepted=None):
+        out_tokens, out_n_accepted = self._outputs(out_tokens, out_n_accepted)
+        spec_verify_run(self.h, hidden, W_lm, draft_tokens, q_logits, uniforms,
+                        temperature, out_tokens, out_n_accepted)
+        return out_tokens, out_n_accepted
+
+    def run_truncated(self, hidden, W_lm, draft_tokens, q_logits, uniforms, temperature,
+                      target_top_k=0, target_top_p=1.0, draft_top_k=0, draft_top_p=1.0,
+                      out_tokens=None, out_n_accepted=None):
+        out_tokens, out_n_accepted = self._outputs(out_tokens, out_n_accepted)
+        spec_verify_run_truncated(self.h, hidden, W_lm, draft_tokens, q_logits, uniforms,
+                                  temperature, target_top_k, target_top_p, draft_top_k,
+                                  draft_top_p, out_tokens, out_n_accepted)
+        return out_tokens, out_n_accepted
+
+    def run_fp8(self, hidden8, hidden_scale, W8, w_scale, draft_tokens, q_logits, uniforms,
+                temperature, out_tokens=None, out_n_accepted=None):
+        out_tokens, out_n_accepted = self._outputs(out_tokens, out_n_accepted)
+        spec_verify_run_fp8(self.h, hidden8, hidden_scale, W8, w_scale, draft_tokens, q_logits,
+                            uniforms, temperature, out_tokens, out_n_accepted)
+        return out_tokens, out_n_accepted
+
+    def run_tree_greedy(self, hidden, W_lm, tree_tokens, tree_parents):
+        """Returns (tokens [B, N+1], nodes [B, N], n [B])."""
+        out_t, out_n, out_nodes = self._outputs(None, None, True)
+        spec_verify_tree_greedy(self.h, hidden, W_lm, tree_tokens, tree_parents, out_t,
+                                out_nodes, out_n)
+        return out_t, out_nodes[:, :self.K], out_n
 
     def log_probs(self, tokens=None, top=0, temperature=1.0, out=None):
         """What the last run's logits say of its answers: log probabilities

@@ -81,3 +81,35 @@ def test_given_outputs_and_another_stream_set_later():
         with pytest.raises(ValueError):
             eng.log_probs(tokens, 7, out=bad)
     eng.close()
+
+
+def test_outputs_of_a_run_and_of_a_tree_belong_to_the_handle_too():
+    wl = si.workload("tiny", dtype="bf16", B=2, K=3, V=3000, d=256)
+    W = si.make_weights(wl, seed=3, device="cuda")
+    inp = si.make_round(wl, W, seed=4, T=1.0)
+    torch.cuda.synchronize()
+    eng = sv.SpecVerify(wl.V, wl.d, wl.B, wl.K, wl.dtype, stream=torch.cuda.Stream())
+    args = inp["hidden"], W, inp["draft"], inp["q_logits"], inp["uniforms"], 1.0
+    tokens = inp["draft"].view(wl.B, wl.K)
+    parents = torch.arange(-1, wl.K - 1, dtype=torch.int32, device="cuda").repeat(wl.B, 1)
+    calls = (lambda: eng.run(*args), lambda: eng.run_truncated(*args, target_top_k=50),
+             lambda: eng.run_tree_greedy(inp["hidden"], W, tokens, parents))
+    for call in calls:
+        got = call()
+        torch.cuda.synchronize()
+        want = [t.clone() for t in got]
+        old = [torch.empty_like(t) for t in got]
+        places = {o.data_ptr() for o in old}
+        torch.cuda._sleep(20_000_000)
+        for o in old:
+            o.fill_(7)
+        del old, o, got
+        got = call()
+        assert not places & {t.data_ptr() for t in got}
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    mine = torch.empty(wl.B, dtype=torch.int32, device="cuda")
+    assert eng.run(*args, out_n_accepted=mine)[1] is mine
+    torch.cuda.synchronize()
+    assert eng.status() == sv.SV_OK
+    eng.close()
